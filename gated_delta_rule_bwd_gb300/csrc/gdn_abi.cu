@@ -221,7 +221,9 @@ const char* kernel_name(int id) {
       "simt_fwd", "simt_states", "simt_bwd", "simt_bwd_reduce",
       "tc_fwd", "tc_states", "tc_bwd", "tc_solve", "tc_fwd_segment", "tc_combine", "decode",
       "kda_tc_prep", "kda_tc_fwd", "kda_tc_states", "kda_tc_bwd", "seqlens_setup",
-      "short_conv_fwd", "short_conv_bwd", "gated_rmsnorm_fwd", "gated_rmsnorm_bwd", "sum_partials"};
+      "short_conv_fwd", "short_conv_bwd", "gated_rmsnorm_fwd", "gated_rmsnorm_bwd", "sum_partials",
+      "attn_fwd", "attn_delta", "attn_bwd_kv", "attn_bwd_q", "attn_decode", "attn_combine",
+      "layer_norm_fwd", "layer_norm_bwd", "layer_norm_sum"};
   return (id >= 0 && id < kNumKernelIds) ? names[id] : "unknown";
 }
 

@@ -202,6 +202,63 @@ cudaError_t gated_rmsnorm_fwd(const NormProblem& p, cudaStream_t s);
 cudaError_t gated_rmsnorm_bwd(const NormProblem& p, cudaStream_t s);
 cudaError_t nb_read_and_clear_status(int* status);
 
+// Causal attention over whole prompts (attn_simt.cu, attn_tc.cu); see
+// include/gdn.h.  Strides are batch, token, head, in elements.
+struct AttnProblem {
+  int B = 0, Tq = 0, Tk = 0, H = 0, Hkv = 0, D = 0;
+  bool bf16 = true;
+  float scale = 1.f;
+  long long qs[3] = {}, ks[3] = {}, vs[3] = {};
+  const int *cu_q = nullptr, *cu_k = nullptr;  // packed sequences, or both NULL
+  int nseq = 0;
+  const void *q = nullptr, *k = nullptr, *v = nullptr;
+  void* o = nullptr;
+  float* lse = nullptr;
+  const void* do_ = nullptr;
+  void *dq = nullptr, *dk = nullptr, *dv = nullptr;
+  void* ws = nullptr;
+};
+cudaError_t attn_simt_fwd(const AttnProblem& p, cudaStream_t s);
+cudaError_t attn_simt_bwd(const AttnProblem& p, cudaStream_t s);
+// delta [B, H, Tq] = rowsum(do * o), fp32, into p.ws: the workspace of the
+// backward (both kernel families).
+size_t attn_bwd_workspace(const AttnProblem& p);
+cudaError_t attn_delta(const AttnProblem& p, cudaStream_t s);
+
+struct AttnDecodeProblem {
+  int B = 0, T = 0, S = 0, H = 0, Hkv = 0, D = 0;
+  bool bf16 = true;
+  float scale = 1.f;
+  long long kcs[3] = {}, vcs[3] = {};
+  const void *q = nullptr, *k = nullptr, *v = nullptr;
+  void *kc = nullptr, *vc = nullptr;
+  const int* lens = nullptr;
+  void* o = nullptr;
+  void* ws = nullptr;
+};
+size_t attn_decode_workspace(const AttnDecodeProblem& p);
+cudaError_t attn_decode(const AttnDecodeProblem& p, cudaStream_t s);
+
+struct LayerNormProblem {
+  long rows = 0;
+  int D = 0;
+  bool bf16 = true;
+  float eps = 1e-6f;
+  const void* x = nullptr;
+  const float *weight = nullptr, *bias = nullptr;
+  void* y = nullptr;
+  float *mean = nullptr, *rstd = nullptr;
+  const void* dy = nullptr;
+  void* dx = nullptr;
+  float *dweight = nullptr, *dbias = nullptr;
+  void* ws = nullptr;
+};
+size_t layer_norm_bwd_workspace(const LayerNormProblem& p);
+cudaError_t layer_norm_fwd(const LayerNormProblem& p, cudaStream_t s);
+cudaError_t layer_norm_bwd(const LayerNormProblem& p, cudaStream_t s);
+cudaError_t attn_simt_read_and_clear_status(int* status);
+cudaError_t attn_decode_read_and_clear_status(int* status);
+
 // Kernel ids reported by the timing hook (gdn_profile_*).
 enum KernelId {
   kSimtFwd = 0,
@@ -225,7 +282,16 @@ enum KernelId {
   kNormFwd = 18,
   kNormBwd = 19,
   kSumPartials = 20,
-  kNumKernelIds = 21
+  kAttnFwd = 21,
+  kAttnDelta = 22,
+  kAttnBwdKv = 23,
+  kAttnBwdQ = 24,
+  kAttnDecode = 25,
+  kAttnCombine = 26,
+  kLnFwd = 27,
+  kLnBwd = 28,
+  kLnSum = 29,
+  kNumKernelIds = 30
 };
 const char* kernel_name(int id);
 

@@ -362,6 +362,112 @@ GDN_API int gdn_gated_rmsnorm_bwd(const gdn_norm_shape* shape, const void* o, co
                                   float* dweight, float eps, void* ws, size_t ws_bytes,
                                   void* stream);
 
+/* The softmax attention layers of a hybrid model (Primus hybrid-LLM pretraining
+ * blog, section "How hybrid models are defined in Primus": attention layers
+ * stand between the linear-recurrent ones).  Causal attention over whole
+ * prompts with grouped heads: query head h reads key / value head
+ * h / (H / Hkv).  For a sequence of lq queries and lk keys, query i sees the
+ * keys j <= i + lk - lq (the queries are the sequence's last lq tokens; with
+ * lq = lk this is plain causal attention):
+ *   s_ij = scale q_i . k_j,   lse_i = log sum_j exp(s_ij),
+ *   o_i = sum_j exp(s_ij - lse_i) v_j.
+ * A query that sees no key (lk < lq) gets o = 0, lse = -inf and contributes no
+ * gradient.
+ *
+ * Layout: q [B, Tq, H, D], k and v [B, Tk, Hkv, D], each with the D elements
+ * of a head contiguous and any (non-negative) batch, token and head strides,
+ * in elements: q, k and v may be views of one fused projection.  o, do_ and
+ * dq are [B, Tq, H, D], dk and dv [B, Tk, Hkv, D], all contiguous; lse is
+ * [B, H, Tq] fp32, contiguous.  D in [1, 128]; dtype GDN_F32 or GDN_BF16;
+ * H a multiple of Hkv.
+ *
+ * Packed sequences: cu_q and cu_k non-NULL, B = 1, each a DEVICE array of
+ * nseq + 1 int32 offsets (sequence s is queries [cu_q[s], cu_q[s+1]) and keys
+ * [cu_k[s], cu_k[s+1]); they may be the same array).  Offsets that do not
+ * rise from 0 to Tq / Tk give unspecified outputs (every access stays inside
+ * the arrays) and gdn_device_status() returns GDN_ERR_SEQLENS.  With both
+ * NULL, nseq is ignored and each of the B rows is one sequence of Tq queries
+ * and Tk keys.
+ *
+ * The backward returns the gradients of q, k and v from o and lse of the
+ * forward and do_; heads that share a key head are summed into its gradient
+ * in a fixed order.  Results are deterministic.
+ *
+ * Kernel selection: bf16 with D a multiple of 8 and q, k, v aligned (16-byte
+ * base, strides multiples of 8 elements and not 0 where the dimension is
+ * longer than 1) runs the tensor-core kernels; everything else the CUDA-core
+ * fp32 kernels.  bf16 probabilities feed the tensor cores; scores, sums and
+ * accumulators are fp32 everywhere.
+ *
+ * Errors: GDN_ERR_ARG (NULL pointer, scale not a positive finite number, only
+ * one of cu_q and cu_k given), GDN_ERR_SHAPE, GDN_ERR_DTYPE, GDN_ERR_ALIGN (o,
+ * lse, do_, dq, dk, dv or ws not 16-byte aligned; q, k, v not aligned to their
+ * element), GDN_ERR_WORKSPACE, GDN_ERR_CUDA.  A call with no query writes
+ * nothing but the (zero) dk and dv; pointers of empty tensors may be NULL. */
+typedef struct {
+  int B, Tq, Tk;      /* batch rows; queries / keys per row; each >= 0         */
+  int H, Hkv, D;      /* query heads, key heads, head dimension                */
+  int dtype;          /* gdn_dtype                                             */
+  long long q_stride[3], k_stride[3], v_stride[3]; /* batch, token, head       */
+} gdn_attn_shape;
+
+GDN_API size_t gdn_attn_fwd_workspace(const gdn_attn_shape* shape, int nseq);
+GDN_API int gdn_attn_fwd(const gdn_attn_shape* shape, const void* q, const void* k, const void* v,
+                         float scale, const int* cu_q, const int* cu_k, int nseq, void* o,
+                         float* lse, void* ws, size_t ws_bytes, void* stream);
+GDN_API size_t gdn_attn_bwd_workspace(const gdn_attn_shape* shape, int nseq);
+GDN_API int gdn_attn_bwd(const gdn_attn_shape* shape, const void* q, const void* k, const void* v,
+                         float scale, const int* cu_q, const int* cu_k, int nseq, const void* o,
+                         const float* lse, const void* do_, void* dq, void* dk, void* dv,
+                         void* ws, size_t ws_bytes, void* stream);
+
+/* Attention of T new tokens (T = 1 in single-token generation) per batch row
+ * against a cache, which the call extends: row b holds lens[b] tokens, the new
+ * tokens' k and v [B, T, Hkv, D] are written to slots lens[b] .. lens[b]+T-1 of
+ * k_cache and v_cache [B, S, Hkv, D], and o [B, T, H, D] is the attention of q
+ * [B, T, H, D] over them: new token t sees the slots <= lens[b] + t.  Slots
+ * from lens[b] + T on are never read.  lens (DEVICE, int32 [B]) is not
+ * changed; the caller adds T.  Everything is contiguous but the caches, whose
+ * batch, token and head strides (in elements) the shape gives.  A row whose
+ * lens[b] is negative or leaves less than T free slots gets o = 0 and no cache
+ * write, and gdn_device_status() returns GDN_ERR_SEQLENS.
+ *
+ * The used part of both caches is read once per 16 query rows (H / Hkv heads
+ * times T tokens share a key head).  The work is split along the cache where
+ * there are few rows, and the parts are joined by a second kernel through the
+ * workspace.  Errors as above (GDN_ERR_ALIGN: q, k, v, o or ws not 16-byte
+ * aligned). */
+typedef struct {
+  int B, T, S;        /* batch rows, new tokens per row, cache slots per row   */
+  int H, Hkv, D;
+  int dtype;
+  long long kc_stride[3], vc_stride[3]; /* batch, token, head */
+} gdn_attn_decode_shape;
+
+GDN_API size_t gdn_attn_decode_workspace(const gdn_attn_decode_shape* shape);
+GDN_API int gdn_attn_decode(const gdn_attn_decode_shape* shape, const void* q, const void* k,
+                            const void* v, void* k_cache, void* v_cache, const int* lens,
+                            float scale, void* o, void* ws, size_t ws_bytes, void* stream);
+
+/* Layer norm of rows of D values (the pre-norm of a layer), with weight [D]
+ * and bias [D] (fp32; bias may be NULL):
+ *   mean = sum(x) / D,  rstd = 1 / sqrt(sum((x - mean)^2) / D + eps),
+ *   y = (x - mean) * rstd * weight + bias.
+ * mean and rstd ([rows], fp32) are written for the backward unless NULL.  The
+ * backward writes dx (layout and dtype of x) and dweight, dbias [D] (fp32,
+ * overwritten, summed over the rows in a fixed order; dbias may be NULL) from
+ * x, weight, mean, rstd and dy.  x, y, dy, dx contiguous and 16-byte aligned,
+ * D in [1, 65536], rows >= 0; dtype GDN_F32 or GDN_BF16.  Errors as for the
+ * gated RMS norm. */
+GDN_API int gdn_layer_norm_fwd(const gdn_norm_shape* shape, const void* x, const float* weight,
+                               const float* bias, void* y, float* mean, float* rstd, float eps,
+                               void* stream);
+GDN_API size_t gdn_layer_norm_bwd_workspace(const gdn_norm_shape* shape);
+GDN_API int gdn_layer_norm_bwd(const gdn_norm_shape* shape, const void* x, const float* weight,
+                               const float* mean, const float* rstd, const void* dy, void* dx,
+                               float* dweight, float* dbias, void* ws, size_t ws_bytes,
+                               void* stream);
+
 /* Human-readable name of a gdn_status value. */
 GDN_API const char* gdn_status_str(int status);
 
