@@ -126,7 +126,8 @@ int gdn_attn_fwd(const gdn_attn_shape* shape, const void* q, const void* k, cons
   if (!all_aligned16({o, lse, ws})) return GDN_ERR_ALIGN;
   (void)ws_bytes;
   p.o = o, p.lse = lse, p.ws = ws;
-  return done(gdn::attn_simt_fwd(p, static_cast<cudaStream_t>(stream)));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return done(gdn::attn_tc_supported(p) ? gdn::attn_tc_fwd(p, st) : gdn::attn_simt_fwd(p, st));
 }
 
 size_t gdn_attn_bwd_workspace(const gdn_attn_shape* shape, int nseq) {
