@@ -223,6 +223,7 @@ cudaError_t attn_simt_bwd(const AttnProblem& p, cudaStream_t s);
 // Tensor-core kernels: bf16, D a multiple of 8, q, k, v fit for tensor maps.
 bool attn_tc_supported(const AttnProblem& p);
 cudaError_t attn_tc_fwd(const AttnProblem& p, cudaStream_t s);
+cudaError_t attn_tc_bwd(const AttnProblem& p, cudaStream_t s);
 // delta [B, H, Tq] = rowsum(do * o), fp32, into p.ws: the workspace of the
 // backward (both kernel families).
 size_t attn_bwd_workspace(const AttnProblem& p);
@@ -261,6 +262,7 @@ cudaError_t layer_norm_fwd(const LayerNormProblem& p, cudaStream_t s);
 cudaError_t layer_norm_bwd(const LayerNormProblem& p, cudaStream_t s);
 cudaError_t attn_simt_read_and_clear_status(int* status);
 cudaError_t attn_tc_fwd_read_and_clear_status(int* status);
+cudaError_t attn_tc_bwd_read_and_clear_status(int* status);
 cudaError_t attn_decode_read_and_clear_status(int* status);
 
 // Kernel ids reported by the timing hook (gdn_profile_*).

@@ -51,7 +51,7 @@ cudaError_t read_and_clear_device_status(int* status) {
   cudaError_t e = tc::read_and_clear_file_status(&a);
   for (auto read : {kda_read_and_clear_status, nb_read_and_clear_status,
                     attn_simt_read_and_clear_status, attn_tc_fwd_read_and_clear_status,
-                    attn_decode_read_and_clear_status}) {
+                    attn_tc_bwd_read_and_clear_status, attn_decode_read_and_clear_status}) {
     int b = GDN_OK;
     if (e == cudaSuccess) e = read(&b);
     if (a == GDN_OK) a = b;
