@@ -616,6 +616,27 @@ def kda_decode(q, k, v, g, beta, state=None, inplace=True):
 
 
 # ---------------------------------------------------------------- attention layers
+#
+# Small calls are bound by the host: the checks below take one expression per
+# tensor, and build their messages only when it fails.
+
+def _same(x, dtype, device, shape):
+    return (isinstance(x, torch.Tensor) and x.dtype is dtype and x.shape == shape
+            and x.device == device and x.is_contiguous())
+
+
+def _raw_stream(device):
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _addr(x):
+    return None if x is None else x.data_ptr()
+
+
+def _call(rc):
+    if rc:
+        _check(rc)
+
 
 def _attn_tensor(name, x, dtype, device):
     """A [B, T, H, D] tensor whose head rows are contiguous (any other strides)."""
@@ -623,24 +644,28 @@ def _attn_tensor(name, x, dtype, device):
         raise GdnError(f"{name} must be a tensor")
     if x.device.type != "cuda":
         raise GdnError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-    if x.dim() != 4 or x.dtype != dtype or x.device != device:
+    if x.dim() != 4 or x.dtype is not dtype or x.device != device:
         raise GdnError(f"{name}: expected a [B, T, H, D] {dtype} tensor on {device}, got "
                        f"{tuple(x.shape)} {x.dtype} on {x.device}")
-    if x.shape[3] > 1 and x.stride(3) != 1:
+    st = x.stride()
+    if st[3] != 1 and x.shape[3] > 1:
         raise GdnError(f"{name}: the D values of a head must be contiguous")
+    return st[:3]
 
 
 def _attn_cu(name, cu, device):
-    if (not isinstance(cu, torch.Tensor) or cu.dtype != torch.int32 or cu.device != device
+    if (not isinstance(cu, torch.Tensor) or cu.dtype is not torch.int32 or cu.device != device
             or cu.dim() != 1 or cu.numel() < 1 or not cu.is_contiguous()):
         raise GdnError(f"{name} must be a contiguous 1-D int32 tensor on the inputs' device")
 
 
 def _attn_args(q, k, v, cu_seqlens, cu_seqlens_k, scale):
+    """The ABI shape and scale of a prompt call, the offsets and their number."""
     if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPES:
         raise GdnError("q must be a fp32 or bf16 tensor")
-    for name, x in (("q", q), ("k", k), ("v", v)):
-        _attn_tensor(name, x, q.dtype, q.device)
+    dtype, device = q.dtype, q.device
+    qs, ks, vs = (_attn_tensor("q", q, dtype, device), _attn_tensor("k", k, dtype, device),
+                  _attn_tensor("v", v, dtype, device))
     B, Tq, H, D = q.shape
     Bk, Tk, Hkv, Dk = k.shape
     if v.shape != k.shape or Bk != B or Dk != D:
@@ -650,14 +675,14 @@ def _attn_args(q, k, v, cu_seqlens, cu_seqlens_k, scale):
         raise GdnError(f"{Hkv} key heads do not divide the {H} query heads")
     nseq = 0
     if cu_seqlens is not None:
-        _attn_cu("cu_seqlens", cu_seqlens, q.device)
+        _attn_cu("cu_seqlens", cu_seqlens, device)
         if cu_seqlens_k is None:
             if Tk != Tq:
                 raise GdnError(f"{Tk} keys for {Tq} queries: packed keys of other lengths need "
                                "cu_seqlens_k")
             cu_seqlens_k = cu_seqlens
         else:
-            _attn_cu("cu_seqlens_k", cu_seqlens_k, q.device)
+            _attn_cu("cu_seqlens_k", cu_seqlens_k, device)
             if cu_seqlens_k.numel() != cu_seqlens.numel():
                 raise GdnError("cu_seqlens and cu_seqlens_k must have the same length")
         if B != 1:
@@ -665,8 +690,7 @@ def _attn_args(q, k, v, cu_seqlens, cu_seqlens_k, scale):
         nseq = cu_seqlens.numel() - 1
     elif cu_seqlens_k is not None:
         raise GdnError("cu_seqlens_k needs cu_seqlens")
-    s = AttnShape(B, Tq, Tk, H, Hkv, D, _DTYPES[q.dtype], q.stride()[:3], k.stride()[:3],
-                  v.stride()[:3])
+    s = AttnShape(B, Tq, Tk, H, Hkv, D, _DTYPES[dtype], qs, ks, vs)
     return s, D ** -0.5 if scale is None else float(scale), cu_seqlens, cu_seqlens_k, nseq
 
 
@@ -679,13 +703,13 @@ def attn_fwd(q, k, v, cu_seqlens=None, cu_seqlens_k=None, scale=None, workspace=
     ``D ** -0.5``.  Returns ``(o [B, Tq, H, D], lse [B, H, Tq] fp32)``; a query
     without keys has o = 0 and lse = -inf."""
     s, scale, cu, cuk, nseq = _attn_args(q, k, v, cu_seqlens, cu_seqlens_k, scale)
-    o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    lse = torch.empty((s.B, s.H, s.Tq), dtype=torch.float32, device=q.device)
-    need = int(lib().gdn_attn_fwd_workspace(ctypes.byref(s), nseq))
-    ws = _workspace(need, workspace, q.device) if need else None
-    _check(lib().gdn_attn_fwd(ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), scale, _ptr(cu),
-                              _ptr(cuk), nseq, _ptr(o), _ptr(lse), _ptr(ws), need,
-                              _stream(q.device)))
+    device, L, sp = q.device, lib(), ctypes.byref(s)
+    o = torch.empty(q.shape, dtype=q.dtype, device=device)
+    lse = torch.empty((s.B, s.H, s.Tq), dtype=torch.float32, device=device)
+    need = L.gdn_attn_fwd_workspace(sp, nseq)
+    ws = _workspace(need, workspace, device) if need else None
+    _call(L.gdn_attn_fwd(sp, q.data_ptr(), k.data_ptr(), v.data_ptr(), scale, _addr(cu), _addr(cuk),
+                         nseq, o.data_ptr(), lse.data_ptr(), _addr(ws), need, _raw_stream(device)))
     return o, lse
 
 
@@ -693,17 +717,20 @@ def attn_bwd(q, k, v, o, lse, do, cu_seqlens=None, cu_seqlens_k=None, scale=None
     """Gradients of ``attn_fwd`` for the output gradient ``do``, from its inputs
     and its ``o`` and ``lse``: returns ``(dq, dk, dv)`` (contiguous)."""
     s, scale, cu, cuk, nseq = _attn_args(q, k, v, cu_seqlens, cu_seqlens_k, scale)
-    _nb_check("o", o, q.dtype, q.device, q.shape)
-    _nb_check("do", do, q.dtype, q.device, q.shape)
-    _nb_check("lse", lse, torch.float32, q.device, (s.B, s.H, s.Tq))
-    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-    dv = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-    need = int(lib().gdn_attn_bwd_workspace(ctypes.byref(s), nseq))
-    ws = _workspace(need, workspace, q.device) if need else None
-    _check(lib().gdn_attn_bwd(ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), scale, _ptr(cu),
-                              _ptr(cuk), nseq, _ptr(o), _ptr(lse), _ptr(do), _ptr(dq), _ptr(dk),
-                              _ptr(dv), _ptr(ws), need, _stream(q.device)))
+    dtype, device, L, sp = q.dtype, q.device, lib(), ctypes.byref(s)
+    if not (_same(o, dtype, device, q.shape) and _same(do, dtype, device, q.shape)
+            and _same(lse, torch.float32, device, (s.B, s.H, s.Tq))):
+        _nb_check("o", o, dtype, device, q.shape)
+        _nb_check("do", do, dtype, device, q.shape)
+        _nb_check("lse", lse, torch.float32, device, (s.B, s.H, s.Tq))
+    dq = torch.empty(q.shape, dtype=dtype, device=device)
+    dk = torch.empty(k.shape, dtype=dtype, device=device)
+    dv = torch.empty(k.shape, dtype=dtype, device=device)
+    need = L.gdn_attn_bwd_workspace(sp, nseq)
+    ws = _workspace(need, workspace, device) if need else None
+    _call(L.gdn_attn_bwd(sp, q.data_ptr(), k.data_ptr(), v.data_ptr(), scale, _addr(cu), _addr(cuk),
+                         nseq, o.data_ptr(), lse.data_ptr(), do.data_ptr(), dq.data_ptr(),
+                         dk.data_ptr(), dv.data_ptr(), _addr(ws), need, _raw_stream(device)))
     return dq, dk, dv
 
 
@@ -715,38 +742,45 @@ def attn_decode(q, k, v, k_cache, v_cache, lens, scale=None, workspace=None):
     ``lens`` itself is left to the caller.  Returns ``o [B, T, H, D]``."""
     if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPES:
         raise GdnError("q must be a fp32 or bf16 tensor")
-    _attn_tensor("q", q, q.dtype, q.device)
+    dtype, device = q.dtype, q.device
+    _attn_tensor("q", q, dtype, device)
+    kst = _attn_tensor("k_cache", k_cache, dtype, device)
+    vst = _attn_tensor("v_cache", v_cache, dtype, device)
     B, T, H, D = q.shape
-    _attn_tensor("k_cache", k_cache, q.dtype, q.device)
-    _attn_tensor("v_cache", v_cache, q.dtype, q.device)
-    Hkv = k_cache.shape[2]
-    if k_cache.shape != v_cache.shape or k_cache.shape[0] != B or k_cache.shape[3] != D:
+    Bc, S, Hkv, Dc = k_cache.shape
+    if v_cache.shape != k_cache.shape or Bc != B or Dc != D:
         raise GdnError(f"the caches must be [{B}, S, Hkv, {D}], got {tuple(k_cache.shape)} and "
                        f"{tuple(v_cache.shape)}")
     if H > 0 and (Hkv == 0 or H % Hkv):
         raise GdnError(f"{Hkv} key heads do not divide the {H} query heads")
     if not q.is_contiguous():
         raise GdnError("q must be contiguous")
-    _nb_check("k", k, q.dtype, q.device, (B, T, Hkv, D))
-    _nb_check("v", v, q.dtype, q.device, (B, T, Hkv, D))
-    _nb_check("lens", lens, torch.int32, q.device, (B,))
-    s = AttnDecodeShape(B, T, k_cache.shape[1], H, Hkv, D, _DTYPES[q.dtype], k_cache.stride()[:3],
-                        v_cache.stride()[:3])
+    new = (B, T, Hkv, D)
+    if not (_same(k, dtype, device, new) and _same(v, dtype, device, new)
+            and _same(lens, torch.int32, device, (B,))):
+        _nb_check("k", k, dtype, device, new)
+        _nb_check("v", v, dtype, device, new)
+        _nb_check("lens", lens, torch.int32, device, (B,))
+    s = AttnDecodeShape(B, T, S, H, Hkv, D, _DTYPES[dtype], kst, vst)
+    L, sp = lib(), ctypes.byref(s)
     o = torch.empty_like(q)
-    need = int(lib().gdn_attn_decode_workspace(ctypes.byref(s)))
-    ws = _workspace(need, workspace, q.device) if need else None
-    _check(lib().gdn_attn_decode(ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), _ptr(k_cache),
-                                 _ptr(v_cache), _ptr(lens), D ** -0.5 if scale is None else float(scale),
-                                 _ptr(o), _ptr(ws), need, _stream(q.device)))
+    need = L.gdn_attn_decode_workspace(sp)
+    ws = _workspace(need, workspace, device) if need else None
+    _call(L.gdn_attn_decode(sp, q.data_ptr(), k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
+                            v_cache.data_ptr(), lens.data_ptr(),
+                            D ** -0.5 if scale is None else float(scale), o.data_ptr(), _addr(ws),
+                            need, _raw_stream(device)))
     return o
 
 
 def _ln_args(x, weight):
-    _nb_check("x", x)
-    if x.dtype not in _DTYPES or x.dim() < 1 or x.shape[-1] < 1:
+    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dtype in _DTYPES and x.is_contiguous()
+            and x.dim() > 0 and x.shape[-1] > 0):
+        _nb_check("x", x)
         raise GdnError("x must be [..., D] fp32 or bf16, D >= 1")
     D = x.shape[-1]
-    _nb_check("weight", weight, torch.float32, x.device, (D,))
+    if not _same(weight, torch.float32, x.device, (D,)):
+        _nb_check("weight", weight, torch.float32, x.device, (D,))
     return NormShape(x.numel() // D, D, _DTYPES[x.dtype])
 
 
@@ -755,13 +789,15 @@ def layer_norm_fwd(x, weight, bias=None, eps=NORM_EPS):
     (``weight``, ``bias`` ``[D]`` fp32).  Returns ``(y, mean, rstd)``, the
     statistics ``[...]`` in fp32 for ``layer_norm_bwd``."""
     s = _ln_args(x, weight)
-    if bias is not None:
-        _nb_check("bias", bias, torch.float32, x.device, weight.shape)
+    device = x.device
+    if bias is not None and not _same(bias, torch.float32, device, weight.shape):
+        _nb_check("bias", bias, torch.float32, device, weight.shape)
     y = torch.empty_like(x)
-    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
     rstd = torch.empty_like(mean)
-    _check(lib().gdn_layer_norm_fwd(ctypes.byref(s), _ptr(x), _ptr(weight), _ptr(bias), _ptr(y),
-                                    _ptr(mean), _ptr(rstd), float(eps), _stream(x.device)))
+    _call(lib().gdn_layer_norm_fwd(ctypes.byref(s), x.data_ptr(), weight.data_ptr(), _addr(bias),
+                                   y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), float(eps),
+                                   _raw_stream(device)))
     return y, mean, rstd
 
 
@@ -769,16 +805,18 @@ def layer_norm_bwd(x, weight, mean, rstd, dy, workspace=None):
     """Gradients of ``layer_norm_fwd``: returns ``(dx, dweight, dbias)`` (the last
     two fp32, reproducible sums over the rows)."""
     s = _ln_args(x, weight)
-    _nb_check("dy", dy, x.dtype, x.device, x.shape)
-    _nb_check("mean", mean, torch.float32, x.device, x.shape[:-1])
-    _nb_check("rstd", rstd, torch.float32, x.device, x.shape[:-1])
+    device, lead, L, sp = x.device, x.shape[:-1], lib(), ctypes.byref(s)
+    if not (_same(dy, x.dtype, device, x.shape) and _same(mean, torch.float32, device, lead)
+            and _same(rstd, torch.float32, device, lead)):
+        _nb_check("dy", dy, x.dtype, device, x.shape)
+        _nb_check("mean", mean, torch.float32, device, lead)
+        _nb_check("rstd", rstd, torch.float32, device, lead)
     dx = torch.empty_like(x)
     dweight, dbias = torch.empty_like(weight), torch.empty_like(weight)
-    need = int(lib().gdn_layer_norm_bwd_workspace(ctypes.byref(s)))
-    ws = _workspace(need, workspace, x.device)
-    _check(lib().gdn_layer_norm_bwd(ctypes.byref(s), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd),
-                                    _ptr(dy), _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(ws),
-                                    ws.numel(), _stream(x.device)))
+    ws = _workspace(L.gdn_layer_norm_bwd_workspace(sp), workspace, device)
+    _call(L.gdn_layer_norm_bwd(sp, x.data_ptr(), weight.data_ptr(), mean.data_ptr(),
+                               rstd.data_ptr(), dy.data_ptr(), dx.data_ptr(), dweight.data_ptr(),
+                               dbias.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(device)))
     return dx, dweight, dbias
 
 
