@@ -27,6 +27,27 @@ __device__ __forceinline__ bool wait_live(uint64_t* bar, uint32_t parity, volati
   return false;
 }
 
+// One lane of a converged warp.  A role that one lane plays is put behind it
+// as a whole: the compiler then knows that a single lane is active and feeds
+// an MMA's descriptors straight to its uniform registers (9-17 cycles per MMA
+// to issue; behind lane == 0 it is 60, as long as the MMA itself runs).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// wait_live for a whole warp: one lane polls.
+__device__ __forceinline__ bool warp_wait_live(uint64_t* bar, uint32_t parity, volatile int* dead) {
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) ok = wait_live(bar, parity, dead);
+  return __shfl_sync(0xffffffffu, ok, 0);
+}
+
 // ---------------------------------------------------------------- MMA with A in TMEM
 
 // D[tmem] (+)= A[tmem] * B[smem]^T: A is K-major, two bf16 of a row per 32-bit

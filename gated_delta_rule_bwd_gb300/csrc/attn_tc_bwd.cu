@@ -171,7 +171,7 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegOther));
-    if (warp == 8 && lane == 0 && N) {
+    if (warp == 8 && N && elect_one()) {
       // ------------------------------------------------------------ loads
       mbar_arrive_expect_tx(kv_full, 2 * C::kTile);
       load_tile<C::NH>(sm, &tm_k, kv_full, hk, t.k0 + j0, t.b);
@@ -196,7 +196,7 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
           mbar_wait(do_full + (x & 1), (x >> 1) & 1, 10000);
         }
       }
-    } else if (warp == 9 && lane == 0 && N) {
+    } else if (warp == 9 && N && elect_one()) {
       // ------------------------------------------------------------ MMAs
       const uint64_t rows = sw128_desc(smem_u32(sm), 16, 1024);      // K-major
       const uint64_t cols = sw128_desc(smem_u32(sm), 16384, 1024);   // MN-major, 64-column blocks 16 KB apart
@@ -258,11 +258,17 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         if (!__shfl_sync(0xffffffffu, ok, 0)) break;
         const int r = (i0 + it % ni) * 128;
         const long long at = ((long long)t.b * a.H + hk * G + it / ni) * a.sq.Tq + t.q0 + r;
+        float ls[4], dl[4];  // all in flight before the first is stored
 #pragma unroll
-        for (int x = lane; x < 128; x += 32) {
-          const bool in = r + x < t.lq;
-          stats[st * 256 + x] = in ? a.lse[at + x] * kLog2e : 0.f;
-          stats[st * 256 + 128 + x] = in ? a.delta[at + x] : 0.f;
+        for (int x = 0; x < 4; ++x) {
+          const bool in = r + lane + 32 * x < t.lq;
+          ls[x] = in ? a.lse[at + lane + 32 * x] * kLog2e : 0.f;
+          dl[x] = in ? a.delta[at + lane + 32 * x] : 0.f;
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          stats[st * 256 + lane + 32 * x] = ls[x];
+          stats[st * 256 + 128 + lane + 32 * x] = dl[x];
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(st_full + st);
@@ -280,8 +286,8 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     for (int it = 0; it < N; ++it) {
       const int r = (i0 + it % ni) * 128;
       const float *lse = stats + it % 3 * 256 + 64 * g, *delta = lse + 128;
-      ok = __all_sync(0xffffffffu, wait_live(st_full + it % 3, (it / 3) & 1, dead) &&
-                                       wait_live(s_full, it & 1, dead));
+      ok = warp_wait_live(st_full + it % 3, (it / 3) & 1, dead) &&
+                                       warp_wait_live(s_full, it & 1, dead);
       if (!ok) break;
       tc_fence_after();
       float p[64];
@@ -312,7 +318,7 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full);
 
-      ok = __all_sync(0xffffffffu, wait_live(dp_full, it & 1, dead));
+      ok = warp_wait_live(dp_full, it & 1, dead);
       if (!ok) break;
       tc_fence_after();
       float d[64];
@@ -346,7 +352,7 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     __nv_bfloat16* dst = g ? a.dk : a.dv;  // warps 0-3: dV, 4-7: dK
     dst = key < t.lk ? dst + (((long long)t.b * a.sq.Tk + t.k0 + key) * a.Hkv + hk) * a.D : nullptr;
     if (N) {
-      ok = ok && __all_sync(0xffffffffu, wait_live(acc_full, 0, dead));
+      ok = ok && warp_wait_live(acc_full, 0, dead);
       tc_fence_after();
       if (ok) store_acc<DP>(tmem + lanes + (g ? kDK : kDV), g ? a.scale : 1.f, dst, a.D);
     } else if (dst) {
@@ -426,7 +432,7 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegOther));
-    if (warp == 8 && lane == 0 && N) {
+    if (warp == 8 && N && elect_one()) {
       // ------------------------------------------------------------ loads
       mbar_arrive_expect_tx(q_full, 2 * C::kTile);
       load_tile<C::NH>(sm, &tm_q, q_full, h, t.q0 + r0, t.b);
@@ -451,7 +457,7 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           mbar_wait(v_full + (x & 1), (x >> 1) & 1, 10000);
         }
       }
-    } else if (warp == 9 && lane == 0 && N) {
+    } else if (warp == 9 && N && elect_one()) {
       // ------------------------------------------------------------ MMAs
       const uint64_t rows = sw128_desc(smem_u32(sm), 16, 1024);
       const uint64_t cols = sw128_desc(smem_u32(sm), 16384, 1024);
@@ -515,7 +521,7 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     bool ok = true;
     for (int j = 0; j < N; ++j) {
       const uint32_t ts = tmem + lanes + kS + 128 * (j & 1) + 64 * g;
-      ok = __all_sync(0xffffffffu, wait_live(s_full + (j & 1), (j >> 1) & 1, dead));
+      ok = warp_wait_live(s_full + (j & 1), (j >> 1) & 1, dead);
       if (!ok) break;
       tc_fence_after();
       float p[64], d[64];
@@ -529,7 +535,7 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         const float2 e = unpack(fma2(f2(p[x], p[x + 1]), cc, ls));
         p[x] = ex2(e.x), p[x + 1] = ex2(e.y);
       }
-      ok = __all_sync(0xffffffffu, wait_live(dp_full, j & 1, dead));
+      ok = warp_wait_live(dp_full, j & 1, dead);
       if (!ok) break;
       tc_fence_after();
       tmem_ld32_start(td, d);
@@ -562,7 +568,7 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     __nv_bfloat16* dst =
         row < nr ? a.dq + (((long long)t.b * a.sq.Tq + t.q0 + r0 + row) * a.H + h) * a.D : nullptr;
     if (N) {
-      ok = ok && __all_sync(0xffffffffu, wait_live(acc_full, 0, dead));
+      ok = ok && warp_wait_live(acc_full, 0, dead);
       tc_fence_after();
       if (ok && g == 0) store_acc<DP>(tmem + lanes + kDQ, a.scale, dst, a.D);
     } else if (dst && g == 0) {

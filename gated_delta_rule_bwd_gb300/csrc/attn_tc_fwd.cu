@@ -123,7 +123,7 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegOther));
-    if (warp == 8 && lane == 0) {
+    if (warp == 8 && elect_one()) {
       // ------------------------------------------------------------ loads
       for (int i = 0; i < 2; ++i)
         if (n[i]) {
@@ -144,7 +144,7 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         for (int x = max(0, it - C::kStages); x < it; ++x)
           mbar_wait(kv_full + x % C::kStages, (x / C::kStages) & 1, 10000);
       }
-    } else if (warp == 9 && lane == 0) {
+    } else if (warp == 9 && elect_one()) {
       // ------------------------------------------------------------ MMAs
       const uint64_t dq = sw128_desc(smem_u32(sm), 16, 1024);     // K-major
       const uint64_t dv = sw128_desc(smem_u32(sm), 16384, 1024);  // MN-major, 64-column blocks 16 KB apart
@@ -219,7 +219,7 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     F2 l0 = f2(0.f, 0.f), l1 = l0;
     bool ok = true;
     for (int j = 0; j < n[i]; ++j) {
-      ok = __all_sync(0xffffffffu, wait_live(s_full + i, j & 1, dead));
+      ok = warp_wait_live(s_full + i, j & 1, dead);
       if (!ok) break;
       tc_fence_after();
       float s[128];
@@ -275,7 +275,7 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       if (lane == 0) mbar_arrive(p_full + i);
     }
     if (ok && n[i]) {
-      ok = __all_sync(0xffffffffu, wait_live(o_full + i, 0, dead));
+      ok = warp_wait_live(o_full + i, 0, dead);
       tc_fence_after();
     }
     if (ok && nr[i]) {
