@@ -381,6 +381,24 @@ __global__ void __launch_bounds__(kThreads) attn_simt_bwd_q_kernel(Args a) {
   }
 }
 
+// delta [B, H, Tq] = rowsum(do * o) into the workspace
+cudaError_t attn_delta(const AttnProblem& p, cudaStream_t s) {
+  const long long rows = (long long)p.B * p.Tq * p.H;
+  if (rows == 0) return cudaSuccess;
+  const unsigned grid = (unsigned)((rows + 7) / 8);
+  float* delta = static_cast<float*>(p.ws);
+  prof_before(s);
+  if (p.bf16)
+    attn_delta_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(p.o),
+                                           static_cast<const __nv_bfloat16*>(p.do_), delta, p.Tq, p.H, p.D, rows);
+  else
+    attn_delta_kernel<<<grid, 256, 0, s>>>(static_cast<const float*>(p.o), static_cast<const float*>(p.do_),
+                                           delta, p.Tq, p.H, p.D, rows);
+  cudaError_t e = cudaGetLastError();
+  prof_after(s, kAttnDelta);
+  return e;
+}
+
 template <typename K>
 cudaError_t launch(K kernel, dim3 grid, int smem, const Args& a, cudaStream_t s, int id) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -401,9 +419,9 @@ cudaError_t fwd(const AttnProblem& p, cudaStream_t s) {
 
 template <typename T, int DP>
 cudaError_t bwd(const AttnProblem& p, cudaStream_t s) {
-  cudaError_t e = cudaSuccess;
+  cudaError_t e = attn_delta(p, s);
   const Args a = args_of(p);
-  if (p.Tk > 0) {
+  if (e == cudaSuccess && p.Tk > 0) {
     const int smem = (4 * tile_floats<DP>() + 2 * kM * kLdP + 2 * kM) * 4;
     const dim3 grid((unsigned)AttnSeqs::slots(p, kM, true), p.Hkv);
     e = launch(attn_simt_bwd_kv_kernel<T, DP>, grid, smem, a, s, kAttnBwdKv);
@@ -419,23 +437,6 @@ cudaError_t bwd(const AttnProblem& p, cudaStream_t s) {
 }  // namespace
 
 size_t attn_bwd_workspace(const AttnProblem& p) { return (size_t)p.B * p.H * p.Tq * sizeof(float); }
-
-cudaError_t attn_delta(const AttnProblem& p, cudaStream_t s) {
-  const long long rows = (long long)p.B * p.Tq * p.H;
-  if (rows == 0) return cudaSuccess;
-  const unsigned grid = (unsigned)((rows + 7) / 8);
-  float* delta = static_cast<float*>(p.ws);
-  prof_before(s);
-  if (p.bf16)
-    attn_delta_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(p.o),
-                                           static_cast<const __nv_bfloat16*>(p.do_), delta, p.Tq, p.H, p.D, rows);
-  else
-    attn_delta_kernel<<<grid, 256, 0, s>>>(static_cast<const float*>(p.o), static_cast<const float*>(p.do_),
-                                           delta, p.Tq, p.H, p.D, rows);
-  cudaError_t e = cudaGetLastError();
-  prof_after(s, kAttnDelta);
-  return e;
-}
 
 cudaError_t attn_simt_fwd(const AttnProblem& p, cudaStream_t s) {
   if (p.bf16) return p.D <= 64 ? fwd<__nv_bfloat16, 64>(p, s) : fwd<__nv_bfloat16, 128>(p, s);

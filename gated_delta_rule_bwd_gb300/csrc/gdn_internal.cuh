@@ -224,10 +224,9 @@ cudaError_t attn_simt_bwd(const AttnProblem& p, cudaStream_t s);
 bool attn_tc_supported(const AttnProblem& p);
 cudaError_t attn_tc_fwd(const AttnProblem& p, cudaStream_t s);
 cudaError_t attn_tc_bwd(const AttnProblem& p, cudaStream_t s);
-// delta [B, H, Tq] = rowsum(do * o), fp32, into p.ws: the workspace of the
-// backward (both kernel families).
+// delta [B, H, Tq] = rowsum(do * o), fp32: the workspace of the backward (both
+// kernel families).
 size_t attn_bwd_workspace(const AttnProblem& p);
-cudaError_t attn_delta(const AttnProblem& p, cudaStream_t s);
 
 struct AttnDecodeProblem {
   int B = 0, T = 0, S = 0, H = 0, Hkv = 0, D = 0;

@@ -152,9 +152,7 @@ int gdn_attn_bwd(const gdn_attn_shape* shape, const void* q, const void* k, cons
   p.o = const_cast<void*>(o), p.lse = const_cast<float*>(lse), p.do_ = do_;
   p.dq = dq, p.dk = dk, p.dv = dv, p.ws = ws;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = gdn::attn_delta(p, st);
-  if (e == cudaSuccess) e = gdn::attn_tc_supported(p) ? gdn::attn_tc_bwd(p, st) : gdn::attn_simt_bwd(p, st);
-  return done(e);
+  return done(gdn::attn_tc_supported(p) ? gdn::attn_tc_bwd(p, st) : gdn::attn_simt_bwd(p, st));
 }
 
 size_t gdn_attn_decode_workspace(const gdn_attn_decode_shape* shape) {
