@@ -14,13 +14,36 @@ namespace tc {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// The tiles' swizzle wants shared memory that starts at a multiple of 1024
+// bytes, which is where the dynamic part of a kernel without static arrays starts.
+__device__ __forceinline__ bool aligned_smem(const void* sm) {
+  if ((smem_u32(sm) & 1023) == 0) return true;
+  if (threadIdx.x == 0) atomicExch(&g_file_status, GDN_ERR_ALIGN);
+  return false;
+}
+
 // ---------------------------------------------------------------- waits
 
+// One poll with the hardware's own suspend limit.
+__device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Bounded wait that also gives up once another warp of the CTA has
-// (*dead != 0); running out sets *dead.
+// (*dead != 0); running out (about two seconds) sets *dead.
 __device__ __forceinline__ bool wait_live(uint64_t* bar, uint32_t parity, volatile int* dead) {
-  for (uint32_t i = 0; i < 100000; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
+  if (try_wait(bar, parity)) return true;
+  const long long begin = clock64();
+  for (uint32_t i = 0; clock64() - begin < 4000000000LL; ++i) {
+    if (try_wait(bar, parity)) return true;
     if (*dead) return false;
   }
   *dead = 1;
@@ -46,6 +69,103 @@ __device__ __forceinline__ bool warp_wait_live(uint64_t* bar, uint32_t parity, v
   int ok = 1;
   if ((threadIdx.x & 31) == 0) ok = wait_live(bar, parity, dead);
   return __shfl_sync(0xffffffffu, ok, 0);
+}
+
+// A position in a ring of n barriers: its index and the parity of its use.  A
+// consumer waits for full[i] with ph; a producer for empty[i] with ph ^ 1,
+// which a fresh barrier passes.
+template <int n>
+struct Ring {
+  int i = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++i == n) i = 0, ph ^= 1;
+  }
+};
+
+// After giving up: waits (bounded) for the loads last issued to each stage of
+// a ring whose next stage is r, so that nothing is written at exit.
+template <int n>
+__device__ __forceinline__ void drain_loads(uint64_t* full, const Ring<n>& r) {
+  for (int i = 0; i < n; ++i) mbar_wait(full + i, i < r.i ? r.ph : r.ph ^ 1, 10000);
+}
+
+// ---------------------------------------------------------------- tiles of a persistent CTA
+//
+// A CTA works on its own tile and then takes over tiles of CTAs that have not
+// started (cluster launch control), so that setting up barriers and TMEM
+// happens once per SM and the next tile's loads overlap the last one's
+// epilogue, while tiles still go out in the order of the grid, heaviest first.
+// One warp runs the scheduler, a tile ahead: it gets and decodes the next tile
+// and puts it into one of two slots, from which every other warp takes it.
+struct __align__(16) TileSlots {
+  int job[2][12];  // what the roles need to know of a tile; [11] = 0: no more tiles
+  uint4 response;
+  uint64_t full[2], empty[2], response_full;
+
+  __device__ void init(int takers) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, takers);
+    }
+    mbar_init(&response_full, 1);
+  }
+};
+
+// The next tile's job, for one lane (whole = false) or a whole warp; NULL: none.
+// It stays in place until the taker says done.
+__device__ __forceinline__ const int* next_job(TileSlots* ts, const Ring<2>& r, bool whole, volatile int* dead) {
+  const bool ok = whole ? warp_wait_live(ts->full + r.i, r.ph, dead) : wait_live(ts->full + r.i, r.ph, dead);
+  const int* j = ts->job[r.i];
+  return ok && j[11] ? j : nullptr;
+}
+__device__ __forceinline__ void job_done(TileSlots* ts, Ring<2>& r, bool whole) {
+  if (whole) __syncwarp();
+  if (!whole || (threadIdx.x & 31) == 0) mbar_arrive(ts->empty + r.i);
+  r.next();
+}
+
+// Scheduler warp: puts a job into the next slot.
+__device__ __forceinline__ bool put_job(TileSlots* ts, Ring<2>& r, const int (&j)[12], volatile int* dead) {
+  if (!warp_wait_live(ts->empty + r.i, r.ph ^ 1, dead)) return false;
+  if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+    for (int i = 0; i < 12; i += 4)
+      *reinterpret_cast<int4*>(ts->job[r.i] + i) = make_int4(j[i], j[i + 1], j[i + 2], j[i + 3]);
+    mbar_arrive(ts->full + r.i);
+  }
+  r.next();
+  return true;
+}
+
+// Scheduler warp: takes over a CTA that has not started; its index in x, or
+// false if there is none left (after which this must not be called again).
+__device__ __forceinline__ bool next_cta(TileSlots* ts, uint32_t& ph, int& x, volatile int* dead) {
+  if ((threadIdx.x & 31) == 0) {
+    mbar_arrive_expect_tx(&ts->response_full, 16);
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+            smem_u32(&ts->response)),
+        "r"(smem_u32(&ts->response_full))
+        : "memory");
+  }
+  __syncwarp();
+  if (!warp_wait_live(&ts->response_full, ph, dead)) return false;
+  ph ^= 1;
+  uint32_t got, at = 0;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+      "ld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+      : "=r"(got), "+r"(at)
+      : "r"(smem_u32(&ts->response))
+      : "memory");
+  fence_async_shared();  // the response is overwritten by the next request
+  __syncwarp();
+  x = (int)at;
+  return got != 0;
 }
 
 // ---------------------------------------------------------------- MMA with A in TMEM
@@ -113,6 +233,60 @@ __device__ __forceinline__ void tmem_st16_start(uint32_t taddr, const uint32_t* 
       : "memory");
 }
 
+// A warp's 16 lanes x 64 columns (shape 16x256b, from the lane of taddr on):
+// v[4 g + 2 a + e] is lane t / 4 + 8 a, column 8 g + 2 (t % 4) + e.  A row is
+// spread over four neighbouring threads, so two warps can share a
+// sub-partition's 32 lanes and a row still needs no exchange between warps.
+__device__ __forceinline__ void tmem_ld16x64_start(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+        "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+        "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
+// 16 lanes x 32 packed columns (shape 16x128b): r[2 g + a] is lane t / 4 + 8 a,
+// column 4 g + t % 4.
+__device__ __forceinline__ void tmem_st16x32_start(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+        "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+        "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// 16 lanes x 32 columns and back, with the waits (shape 16x256b).
+__device__ __forceinline__ void tmem_ld16x32(uint32_t taddr, float (&v)[16]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+        "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+        "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < 16; i += 8)
+    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]),
+                      "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+__device__ __forceinline__ void tmem_st16x32(uint32_t taddr, const float (&v)[16]) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+        "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+        "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+  tmem_st_wait();
+}
+
 // ---------------------------------------------------------------- arithmetic
 
 struct F2 {
@@ -143,6 +317,11 @@ __device__ __forceinline__ F2 mul2(F2 a, F2 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
   return r;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // 2^x, the hardware approximation (2 ulp; 0 for -inf)
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -153,6 +332,34 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// ---------------------------------------------------------------- epilogue
+
+// Writes 16 rows x 32 columns [c0, c0 + 32) held as by tmem_ld16x32, times f[a]
+// per row half a, as bf16: row r goes to base + r * stride (elements), rows below
+// `rows` and columns below D are written.  The four threads of a row trade their
+// 4-byte pieces so that each has 16 bytes, and a row 64, to store.
+__device__ __forceinline__ void store_rows16x32(const float (&v)[16], const float (&f)[2], __nv_bfloat16* base,
+                                                long long stride, int rows, int c0, int D) {
+  const int t = threadIdx.x & 31, q = t & 3, c = c0 + 8 * q;
+#pragma unroll
+  for (int a = 0; a < 2; ++a) {
+    uint32_t w[4];  // piece q of the 8-column groups 0 .. 3
+#pragma unroll
+    for (int g = 0; g < 4; ++g) w[g] = pack_bf16(v[4 * g + 2 * a] * f[a], v[4 * g + 2 * a + 1] * f[a]);
+    auto swap = [&](uint32_t& x, uint32_t& y, bool up, int off) {
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? x : y, off);
+      if (up) x = got;
+      else y = got;
+    };
+    swap(w[0], w[1], q & 1, 1);
+    swap(w[2], w[3], q & 1, 1);
+    swap(w[0], w[2], q & 2, 2);
+    swap(w[1], w[3], q & 2, 2);  // now pieces 0 .. 3 of group q
+    const int r = t / 4 + 8 * a;
+    if (r < rows && c < D) *reinterpret_cast<uint4*>(base + r * stride + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
 }
 
 // ---------------------------------------------------------------- tensor maps

@@ -56,14 +56,6 @@ struct Cfg {
   static constexpr int kSmem = kBar + 384;  // at most 227 KB: no slack for an alignment
 };
 
-// The tiles' swizzle wants shared memory that starts at a multiple of 1024
-// bytes, which is where the dynamic part of a kernel without static arrays starts.
-__device__ __forceinline__ bool aligned_smem(const void* sm) {
-  if ((smem_u32(sm) & 1023) == 0) return true;
-  if (threadIdx.x == 0) atomicExch(&g_file_status, GDN_ERR_ALIGN);
-  return false;
-}
-
 struct Args {
   AttnSeqs sq;
   int H, Hkv, D, tiles;  // tiles: 128-row tiles per batch row (0: packed)

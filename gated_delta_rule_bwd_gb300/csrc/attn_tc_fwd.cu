@@ -6,20 +6,23 @@
 //   S = Q K^T                      (128 x 128, fp32 in TMEM)
 //   P = exp2(c S - c m), c = scale log2 e: bf16, written over S in TMEM
 //   O += P V                       (P is the MMA's A operand in TMEM)
-// with a running row maximum m and row sum l in the registers of the thread
-// that owns the row (128 threads per tile, one row each, so neither needs
-// another thread).  The maximum that scales P may lag behind: it is only
+// with a running row maximum m and row sum l in the registers of the four
+// threads that share a row.  A warp has 16 rows (TMEM shape 16x256b), so that
+// eight warps work on a tile and none needs another for a row.  The maximum that scales P may lag behind: it is only
 // raised, and O and l rescaled, when the row's maximum has grown by more than
 // 8 in the exponent; P is then at most 2^8, which costs no bits, and the
 // rescaling passes over O in TMEM nearly vanish.
 //
-// Warps 0-3 and 4-7 are the two tiles' softmax, warp 8 issues the TMA loads (a
-// ring of K and V tiles), warp 9 the MMAs, warp 10 zeroes the rows of a packed
-// sequence's last V tile that belong to the next one.  The two tiles take
-// turns: while one is in its softmax the tensor cores run the other's
+// Warps 0-7 and 8-15 are the two tiles' softmax, warp 16 issues the TMA loads (a
+// ring of K and V tiles), warp 17 the MMAs, warp 18 gets the next tiles and zeroes
+// the rows of a packed sequence's last V tile that belong to the next one.  CTAs
+// are persistent (see TileSlots).  The two tiles take turns: while one is in its softmax the tensor cores run the other's
 // products, in the order P V (j), Q K^T (j + 1) per tile.  That Q K^T
 // overwrites P, which is safe behind the P V issued before it; its completion
-// also says that O is up to date.
+// also says that O is up to date.  What bounds the kernel is that turn: a
+// softmax (load, maximum, 64 exponentials a thread, store) has to fit into the
+// other tile's products.  Code that runs once per job is kept rolled: its
+// instructions come from beyond the instruction cache, at some 2 cycles a byte.
 
 #include <math.h>
 
@@ -35,10 +38,9 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 384;
-// 168 registers a thread at launch; the softmax warps take 208, the others 88:
-// 256 * 208 + 128 * 88 = 384 * 168.
-constexpr int kRegSoftmax = 208, kRegOther = 88;
+constexpr int kSoftmax = 512, kThreads = kSoftmax + 128;
+// 96 registers a thread at launch: 512 * 104 + 128 * 64 = 640 * 96
+constexpr int kRegSoftmax = 104, kRegOther = 64;
 constexpr float kLag = 8.f;  // exponent by which the row maximum may lag
 
 template <int DP>
@@ -47,63 +49,77 @@ struct Cfg {
   static constexpr int kTile = 128 * DP * 2;
   static constexpr int kStages = DP == 128 ? 5 : 8;
   static constexpr int kBar = (2 + kStages) * kTile;
-  static constexpr int kSmem = kBar + 512 + 1024;
+  static constexpr int kSmem = kBar + 640;  // at most 227 KB: no slack for an alignment
   static constexpr uint32_t kS = 0, kO = 256;  // TMEM columns: S of tile t at 128 t, O at 256 + DP t
 };
 
 struct Args {
   AttnSeqs sq;
-  int H, Hkv, D, tiles;  // tiles: 256-row tiles per batch row (0: packed)
+  int H, G, D, tiles;  // tiles: 256-row tiles per batch row (0: packed)
   float c, scale;
   __nv_bfloat16* o;
   float* lse;
 };
+
+// A job (256 query rows of one head) as the scheduler hands it out.
+enum { kHead, kB, kQ0, kK0, kLk, kFirst, kNr0, kNr1, kN0, kN1, kFix, kValid };
+// kQ0, kK0: first query and key token; kFirst: the last key that the first row
+// sees; kNr: rows of each 128-row tile; kN: key tiles they see; kFix: the last
+// key tile holds rows of the next packed sequence.
+
+__device__ __forceinline__ bool decode(const Args& a, int cta, int ctas, int (&j)[12]) {
+  // the tiles with the most keys first
+  const int u = cta / a.H;
+  const int slot = a.tiles ? u % a.sq.B * a.tiles + a.tiles - 1 - u / a.sq.B : ctas / a.H - 1 - u;
+  AttnTile t;
+  j[kValid] = a.sq.get<false>(slot, 256, t);
+  if (!j[kValid]) return false;
+  const int r0 = t.tile * 256, shift = t.lk - t.lq;
+  j[kHead] = cta % a.H, j[kB] = t.b, j[kQ0] = t.q0 + r0, j[kK0] = t.k0, j[kLk] = t.lk, j[kFirst] = r0 + shift;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int nr = max(0, min(128, t.lq - r0 - 128 * i));
+    j[kNr0 + i] = nr;
+    j[kN0 + i] = nr ? (max(0, min(t.lk, r0 + 128 * i + nr + shift)) + 127) / 128 : 0;
+  }
+  j[kFix] = a.sq.cu_q && max(j[kN0], j[kN1]) * 128 > t.lk;
+  return true;
+}
 
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, Args a) {
   using C = Cfg<DP>;
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* sm = reinterpret_cast<unsigned char*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* q_full = reinterpret_cast<uint64_t*>(sm + C::kBar);  // [2]
-  uint64_t* s_full = q_full + 2;                                 // [2]
-  uint64_t* p_full = s_full + 2;                                 // [2]
-  uint64_t* o_full = p_full + 2;                                 // [2]
-  uint64_t* v_landed = o_full + 2;  // the last V tile is there; its foreign rows are zero
+  extern __shared__ __align__(1024) unsigned char sm[];
+  TileSlots* slots = reinterpret_cast<TileSlots*>(sm + C::kBar);
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(slots + 1);  // [2]
+  uint64_t* q_empty = q_full + 2;                             // [2]
+  uint64_t* s_full = q_empty + 2;                             // [2]
+  uint64_t* p_full = s_full + 2;                              // [2]
+  uint64_t* o_full = p_full + 2;                              // [2]
+  uint64_t* o_empty = o_full + 2;                             // [2]
+  uint64_t* v_landed = o_empty + 2;  // a job's last V tile is there; its foreign rows are zero
   uint64_t* v_fixed = v_landed + 1;
   uint64_t* drain = v_fixed + 1;
-  uint64_t* kv_full = drain + 1;                                 // [kStages]
-  uint64_t* kv_empty = kv_full + C::kStages;                     // [kStages]
+  uint64_t* kv_full = drain + 1;              // [kStages]
+  uint64_t* kv_empty = kv_full + C::kStages;  // [kStages]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(kv_empty + C::kStages);
   volatile int* dead = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  if (!aligned_smem(sm)) return;
   if (blockIdx.x == 0 && !a.sq.valid() && threadIdx.x == 0) atomicExch(&g_file_status, GDN_ERR_SEQLENS);
-  // the tiles with the most keys first
-  const int h = blockIdx.x % a.H, u = blockIdx.x / a.H;
-  const int slot = a.tiles ? u % a.sq.B * a.tiles + a.tiles - 1 - u / a.sq.B : gridDim.x / a.H - 1 - u;
-  AttnTile t;
-  if (!a.sq.get<false>(slot, 256, t)) return;
-  const int r0 = t.tile * 256, shift = t.lk - t.lq, hk = h / (a.H / a.Hkv);
-  int nr[2], n[2];  // rows of each tile, key tiles they see
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    nr[i] = max(0, min(128, t.lq - r0 - 128 * i));
-    n[i] = nr[i] ? (max(0, min(t.lk, r0 + 128 * i + nr[i] + shift)) + 127) / 128 : 0;
-  }
-  const int nmax = max(n[0], n[1]);
-  // the last V tile holds rows of the next packed sequence
-  const bool fix = a.sq.cu_q && nmax * 128 > t.lk;
-
-  if (threadIdx.x == 256) {
+  if (threadIdx.x == kSoftmax) {
     *dead = 0;
+    slots->init(18);
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full + i, 1);
+      mbar_init(q_empty + i, 1);
       mbar_init(s_full + i, 1);
-      mbar_init(p_full + i, 4);
+      mbar_init(p_full + i, 8);
       mbar_init(o_full + i, 1);
+      mbar_init(o_empty + i, 8);
     }
     mbar_init(v_landed, 1);
     mbar_init(v_fixed, 1);
@@ -113,202 +129,289 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       mbar_init(kv_empty + i, 1);
     }
     fence_barrier_init();
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
   }
-  if (warp == 9) {
+  if (warp == 17) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
   cta_sync();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp >= 8) {
+  Ring<2> take;
+  if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegOther));
-    if (warp == 8 && elect_one()) {
+    if (warp == 16 && elect_one()) {
       // ------------------------------------------------------------ loads
-      for (int i = 0; i < 2; ++i)
-        if (n[i]) {
+      Ring<C::kStages> kv;
+      uint32_t qph[2] = {0, 0};
+      bool ok = true;
+      while (const int* j = ok ? next_job(slots, take, false, dead) : nullptr) {
+        const int h = j[kHead], hk = h / a.G, b = j[kB], q0 = j[kQ0], k0 = j[kK0], n[2] = {j[kN0], j[kN1]};
+        const int nmax = max(n[0], n[1]);
+        job_done(slots, take, false);
+        auto load_q = [&](int i) {
+          if (!n[i]) return;
+          ok = ok && wait_live(q_empty + i, qph[i] ^ 1, dead);
+          if (!ok) return;
+          qph[i] ^= 1;
           mbar_arrive_expect_tx(q_full + i, C::kTile);
-          load_tile<C::NH>(sm + i * C::kTile, &tm_q, q_full + i, h, t.q0 + r0 + 128 * i, t.b);
+          load_tile<C::NH>(sm + i * C::kTile, &tm_q, q_full + i, h, q0 + 128 * i, b);
+        };
+        auto load_kv = [&](const CUtensorMap* tm, int x) {
+          ok = ok && wait_live(kv_empty + kv.i, kv.ph ^ 1, dead);
+          if (!ok) return;
+          mbar_arrive_expect_tx(kv_full + kv.i, C::kTile);
+          load_tile<C::NH>(sm + (2 + kv.i) * C::kTile, tm, kv_full + kv.i, hk, k0 + x * 128, b);
+          kv.next();
+        };
+        load_q(0);
+        if (nmax) load_kv(&tm_k, 0);
+        load_q(1);
+        for (int x = 0; x < nmax && ok; ++x) {  // K 0, V 0, K 1, V 1, ...
+          if (x) load_kv(&tm_k, x);
+          load_kv(&tm_v, x);
         }
-      int it = 0;  // ring use: K 0, V 0, K 1, V 1, ...
-      for (; it < 2 * nmax; ++it) {
-        const int st = it % C::kStages, use = it / C::kStages;
-        if (use && !wait_live(kv_empty + st, (use - 1) & 1, dead)) break;
-        mbar_arrive_expect_tx(kv_full + st, C::kTile);
-        load_tile<C::NH>(sm + (2 + st) * C::kTile, it & 1 ? &tm_v : &tm_k, kv_full + st, hk,
-                         t.k0 + it / 2 * 128, t.b);
       }
-      if (*dead) {  // nothing may still be written at exit (bounded)
-        for (int i = 0; i < 2; ++i)
-          if (n[i]) mbar_wait(q_full + i, 0, 10000);
-        for (int x = max(0, it - C::kStages); x < it; ++x)
-          mbar_wait(kv_full + x % C::kStages, (x / C::kStages) & 1, 10000);
+      if (*dead) {
+        for (int i = 0; i < 2; ++i) mbar_wait(q_full + i, qph[i] ^ 1, 10000);
+        drain_loads(kv_full, kv);
       }
-    } else if (warp == 9 && elect_one()) {
+    } else if (warp == 17 && elect_one()) {
       // ------------------------------------------------------------ MMAs
       const uint64_t dq = sw128_desc(smem_u32(sm), 16, 1024);     // K-major
       const uint64_t dv = sw128_desc(smem_u32(sm), 16384, 1024);  // MN-major, 64-column blocks 16 KB apart
       constexpr uint32_t id_s = idesc_bf16(128, 128, false, false), id_o = idesc_bf16(128, DP, false, true);
-      auto full = [&](int it) { return wait_live(kv_full + it % C::kStages, (it / C::kStages) & 1, dead); };
-      auto tile = [&](int it) { return (uint32_t)(2 + it % C::kStages) * C::kTile; };
-      auto qk = [&](int i, int j) {
-        const uint32_t kt = tile(2 * j);
+      Ring<C::kStages> kv;  // the next tile to wait for
+      uint32_t qph = 0, pph = 0, oph = 0, fph = 0;  // parities, one bit per tile
+      bool ok = true;
+      auto flip = [](uint32_t& ph, int i) {
+        const uint32_t old = (ph >> i) & 1;
+        ph ^= 1u << i;
+        return old;
+      };
+      auto qk = [&](int i, int stage) {
+        const uint64_t q = desc_at(dq, i * C::kTile), k = desc_at(dq, (2 + stage) * C::kTile);
 #pragma unroll
-        for (int k = 0; k < DP / 16; ++k) {
-          const uint32_t off = (k / 4) * 16384 + (k % 4) * 32;
-          mma_bf16(tmem + C::kS + 128 * i, desc_at(dq, i * C::kTile + off), desc_at(dq, kt + off), id_s, k > 0);
+        for (int x = 0; x < DP / 16; ++x) {
+          const uint32_t off = (x / 4) * 16384 + (x % 4) * 32;
+          mma_bf16(tmem + C::kS + 128 * i, desc_at(q, off), desc_at(k, off), id_s, x > 0);
         }
         mma_commit(s_full + i);
       };
-      bool ok = true;
-      if (nmax) {
-        ok = full(0);
-        for (int i = 0; i < 2 && ok; ++i)
-          if (n[i]) {
-            ok = wait_live(q_full + i, 0, dead);
-            if (ok) qk(i, 0);
+      while (const int* j = ok ? next_job(slots, take, false, dead) : nullptr) {
+        const int n0 = j[kN0], n1 = j[kN1], nmax = max(n0, n1);
+        const bool fix = j[kFix];
+        job_done(slots, take, false);
+        // pass x: P V of key tile x (x >= 0), then Q K^T of tile x + 1, per query tile
+        int vs = 0;
+#pragma unroll 1
+        for (int x = -1; x < nmax && ok; ++x) {
+          if (x >= 0) {
+            vs = kv.i;
+            ok = wait_live(kv_full + vs, kv.ph, dead);
+            kv.next();
           }
-        mma_commit(kv_empty + 0);
-      }
-      for (int j = 0; j < nmax && ok; ++j) {
-        ok = full(2 * j + 1) && (j + 1 == nmax || full(2 * j + 2));
-        if (ok && fix && j + 1 == nmax) {
-          mbar_arrive(v_landed);
-          ok = wait_live(v_fixed, 0, dead);
-        }
-        const uint32_t vt = tile(2 * j + 1);
-        for (int i = 0; i < 2 && ok; ++i) {
-          if (j >= n[i]) continue;
-          ok = wait_live(p_full + i, j & 1, dead);
-          if (!ok) break;
-          tc_fence_after();
+          const int ks = kv.i;
+          const bool more = x + 1 < nmax;
+          if (more) {
+            ok = ok && wait_live(kv_full + ks, kv.ph, dead);
+            kv.next();
+          } else if (ok && fix) {
+            mbar_arrive(v_landed);
+            ok = wait_live(v_fixed, fph, dead);
+            fph ^= 1;
+          }
+          const uint64_t v = desc_at(dv, (2 + vs) * C::kTile);
+#pragma unroll 1
+          for (int i = 0; i < 2; ++i) {
+            const int n = i ? n1 : n0;
+            if (!ok || n == 0 || x >= n) continue;
+            if (x < 0) {
+              ok = wait_live(q_full + i, flip(qph, i), dead);
+            } else {
+              if (x == 0) ok = wait_live(o_empty + i, flip(oph, i) ^ 1, dead);  // the job before has read O
+              ok = ok && wait_live(p_full + i, flip(pph, i), dead);
+              if (ok) {
+                tc_fence_after();
+                const uint32_t o = tmem + C::kO + DP * i, p = tmem + C::kS + 128 * i;
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_bf16_ts(tmem + C::kO + DP * i, tmem + C::kS + 128 * i + 8 * k, desc_at(dv, vt + k * 2048), id_o,
-                        j > 0 || k > 0);
-          if (j + 1 < n[i]) qk(i, j + 1);
-          else mma_commit(o_full + i);
+                for (int y = 0; y < 8; ++y)
+                  mma_bf16_ts(o, p + 8 * y, desc_at(v, y * 2048), id_o, x > 0 || y > 0);
+                if (x + 1 == n) mma_commit(o_full + i);
+              }
+            }
+            if (ok && x + 1 < n) {
+              qk(i, ks);
+              if (x + 2 == n) mma_commit(q_empty + i);
+            }
+          }
+          if (x >= 0) mma_commit(kv_empty + vs);
+          if (more) mma_commit(kv_empty + ks);
         }
-        mma_commit(kv_empty + (2 * j + 1) % C::kStages);
-        if (j + 1 < nmax) mma_commit(kv_empty + (2 * j + 2) % C::kStages);
       }
       if (*dead) {
         mma_commit(drain);
         mbar_wait(drain, 0, 10000);
       }
-    } else if (warp == 10 && fix) {
-      const int it = 2 * nmax - 1;
-      bool ok = true;
-      if (lane == 0) ok = wait_live(v_landed, 0, dead);
-      if (__shfl_sync(0xffffffffu, ok, 0)) {
-        zero_rows<C::NH>(sm + (2 + it % C::kStages) * C::kTile, t.lk - (nmax - 1) * 128, lane);
-        if (lane == 0) mbar_arrive(v_fixed);
+    } else if (warp == 18) {
+      // ------------------------------------------------------------ tiles, one ahead; foreign rows
+      int cta = blockIdx.x, it = 0;  // it: K and V tiles so far
+      bool left = true, ok = true;
+      uint32_t ph = 0, fph = 0;
+      int j[12];
+      // fix: V tile it - 1 of the ring, from row `rows` on
+      int fix = 0, rows = 0, fix_it = 0;
+      for (bool more = true; ok && more;) {
+        more = false;
+        while (left && !(more = decode(a, cta, gridDim.x, j))) left = next_cta(slots, ph, cta, dead);
+        j[kValid] = more;
+        ok = put_job(slots, take, j, dead);
+        if (ok && fix) {  // of the job before: its last V tile comes while this one waits
+          ok = warp_wait_live(v_landed, fph, dead);
+          fph ^= 1;
+          if (ok) {
+            zero_rows<C::NH>(sm + (2 + (fix_it - 1) % C::kStages) * C::kTile, rows, lane);
+            if (lane == 0) mbar_arrive(v_fixed);
+          }
+        }
+        if (more) {
+          const int n = max(j[kN0], j[kN1]);
+          it += 2 * n, fix = j[kFix], fix_it = it, rows = j[kLk] - (n - 1) * 128;
+          left = left && next_cta(slots, ph, cta, dead);
+        }
       }
     }
     __syncwarp();
   } else {
     // -------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegSoftmax));
-    const int i = warp >> 2, row = threadIdx.x & 127;
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + C::kS + 128 * i, to = tmem + lanes + C::kO + DP * i;
-    const int first = r0 + 128 * i + shift;         // last key of the tile's first row
-    const int last = min(first + row, t.lk - 1);    // and of this row
+    // this thread: rows w0 + lane / 4 + {0, 8} of tile i, columns 8 g + 2 (lane % 4) + {0, 1}
+    const int i = warp >> 3, w0 = 32 * (warp & 3) + 4 * (warp & 4), col = 2 * (lane & 3);
+    const uint32_t lanes = (uint32_t)w0 << 16, ts = tmem + lanes + C::kS + 128 * i, to = tmem + lanes + C::kO + DP * i;
     const float c = a.c;
-    float m = -INFINITY;
-    F2 l0 = f2(0.f, 0.f), l1 = l0;
+    const F2 cc = f2(c, c);
+    uint32_t sph = 0, oph = 0;
     bool ok = true;
-    for (int j = 0; j < n[i]; ++j) {
-      ok = warp_wait_live(s_full + i, j & 1, dead);
+    while (const int* j = ok ? next_job(slots, take, true, dead) : nullptr) {
+      const int n = j[kN0 + i], lk = j[kLk];
+      const int first = min(j[kFirst] + 128 * i + w0, lk - 1);  // last key that the warp's first row sees
+      float m[2] = {-INFINITY, -INFINITY};
+      F2 l[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll 1
+      for (int x = 0; x < n; ++x) {
+        if (!(ok = warp_wait_live(s_full + i, sph, dead))) break;
+        sph ^= 1;
+        tc_fence_after();
+        float s[64];
+        tmem_ld16x64_start(ts, s);
+        tmem_ld16x64_start(ts + 64, s + 32);
+        tmem_ld_wait();
+        tmem_landed(s);
+        tmem_landed(s + 32);
+        if (x * 128 + 127 > first) {
+          const int see = j[kFirst] + 128 * i + w0 + lane / 4 - x * 128 - col, end = lk - 1 - x * 128 - col;
+#pragma unroll
+          for (int y = 0; y < 64; ++y)
+            s[y] = 8 * (y >> 2) + (y & 1) <= min(see + 4 * (y & 2), end) ? s[y] : -INFINITY;
+        }
+        float f[2], base[2];
+        bool raise = false;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float u = fmaxf(s[2 * r], s[2 * r + 1]), v = fmaxf(s[2 * r + 4], s[2 * r + 5]);
+#pragma unroll
+          for (int y = 8; y < 64; y += 8) {
+            u = max3(u, s[y + 2 * r], s[y + 2 * r + 1]);
+            v = max3(v, s[y + 2 * r + 4], s[y + 2 * r + 5]);
+          }
+          u = fmaxf(u, v);
+          u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, 1));
+          u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, 2));
+          f[r] = 1.f;
+          if ((u - m[r]) * c > kLag) {  // also the row's first keys (m = -inf)
+            f[r] = ex2((m[r] - u) * c);
+            m[r] = u;
+            raise = true;
+          }
+          base[r] = m[r] == -INFINITY ? 0.f : -m[r] * c;  // no key so far: every term is 0
+        }
+        if (x > 0 && __any_sync(0xffffffffu, raise)) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) l[r] = mul2(l[r], f2(f[r], f[r]));
+#pragma unroll 1
+          for (int q = 0; q < DP / 32; ++q) {
+            float o[16];
+            tmem_ld16x32(to + 32 * q, o);
+#pragma unroll
+            for (int y = 0; y < 16; ++y) o[y] *= f[(y >> 1) & 1];
+            tmem_st16x32(to + 32 * q, o);
+          }
+        }
+        const F2 mm[2] = {f2(base[0], base[0]), f2(base[1], base[1])};
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t p[16];
+#pragma unroll
+          for (int y = 0; y < 16; ++y) {
+            const float2 e = unpack(fma2(f2(s[32 * q + 2 * y], s[32 * q + 2 * y + 1]), cc, mm[y & 1]));
+            const float e0 = ex2(e.x), e1 = ex2(e.y);
+            l[y & 1] = add2(l[y & 1], f2(e0, e1));
+            p[y] = pack_bf16(e0, e1);
+          }
+          tmem_st16x32_start(ts + 32 * q, p);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + i);
+      }
+      if (ok && n) {
+        ok = warp_wait_live(o_full + i, oph, dead);
+        oph ^= 1;
+        tc_fence_after();
+      }
       if (!ok) break;
-      tc_fence_after();
-      float s[128];
+      const int h = j[kHead], nr = j[kNr0 + i] - w0, q0 = j[kQ0] + 128 * i + w0, b = j[kB];
+      job_done(slots, take, true);
+      float inv[2];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_ld32_start(ts + 32 * q, s + 32 * q);
-      tmem_ld_wait();
-#pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_landed(s + 32 * q);
-      if (j * 128 + 127 > min(first, t.lk - 1)) {
-        const int see = last - j * 128;
-#pragma unroll
-        for (int x = 0; x < 128; ++x) s[x] = x <= see ? s[x] : -INFINITY;
+      for (int r = 0; r < 2; ++r) {
+        const float2 two = unpack(l[r]);
+        float sum = two.x + two.y;
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        inv[r] = sum == 0.f ? 0.f : 1.f / sum;
+        if (col == 0 && lane / 4 + 8 * r < nr)
+          a.lse[((long long)b * a.H + h) * a.sq.Tq + q0 + lane / 4 + 8 * r] =
+              sum == 0.f ? -INFINITY : m[r] * a.scale + kLn2 * log2f(sum);
       }
-      float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-      for (int x = 4; x < 128; ++x) mx[x & 3] = fmaxf(mx[x & 3], s[x]);
-      const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-      float f = 1.f;
-      if ((top - m) * c > kLag) {  // also the row's first keys (m = -inf)
-        f = ex2((m - top) * c);
-        m = top;
-      }
-      if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {
-        const F2 ff = f2(f, f);
-        l0 = mul2(l0, ff), l1 = mul2(l1, ff);
-#pragma unroll
-        for (int q = 0; q < DP / 32; ++q) {
-          float x[32];
-          tmem_ld32(to + 32 * q, x);
-#pragma unroll
-          for (int y = 0; y < 32; ++y) x[y] *= f;
-          tmem_st32(to + 32 * q, x);
-        }
-      }
-      const float base = m == -INFINITY ? 0.f : m * c;  // no key so far: every term is 0
-      const F2 cc = f2(c, c), mm = f2(-base, -base);
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t p[32];
-#pragma unroll
-        for (int x = 0; x < 32; ++x) {
-          const float2 e = unpack(fma2(f2(s[64 * q + 2 * x], s[64 * q + 2 * x + 1]), cc, mm));
-          const float e0 = ex2(e.x), e1 = ex2(e.y);
-          if (x & 1) l1 = add2(l1, f2(e0, e1));
-          else l0 = add2(l0, f2(e0, e1));
-          p[x] = pack_bf16(e0, e1);
-        }
-        tmem_st32_start(ts + 32 * q, p);
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full + i);
-    }
-    if (ok && n[i]) {
-      ok = warp_wait_live(o_full + i, 0, dead);
-      tc_fence_after();
-    }
-    if (ok && nr[i]) {
-      const float2 la = unpack(add2(l0, l1));
-      const float l = la.x + la.y, inv = l == 0.f ? 0.f : 1.f / l;
-      const int r = r0 + 128 * i + row;
-      __nv_bfloat16* o = a.o + (((long long)t.b * a.sq.Tq + t.q0 + r) * a.H + h) * a.D;
-#pragma unroll
+      __nv_bfloat16* o = a.o + (((long long)b * a.sq.Tq + q0) * a.H + h) * a.D;
+#pragma unroll 1
       for (int q = 0; q < DP / 32; ++q) {
-        float x[32];
-        if (n[i]) {
-          tmem_ld32(to + 32 * q, x);
+        float v[16];
+        if (n) {
+          tmem_ld16x32(to + 32 * q, v);
         } else {
 #pragma unroll
-          for (int y = 0; y < 32; ++y) x[y] = 0.f;
+          for (int y = 0; y < 16; ++y) v[y] = 0.f;
         }
-#pragma unroll
-        for (int y = 0; y < 32; y += 8) {
-          uint4 w;
-          w.x = pack_bf16(x[y] * inv, x[y + 1] * inv), w.y = pack_bf16(x[y + 2] * inv, x[y + 3] * inv);
-          w.z = pack_bf16(x[y + 4] * inv, x[y + 5] * inv), w.w = pack_bf16(x[y + 6] * inv, x[y + 7] * inv);
-          if (row < nr[i] && 32 * q + y < a.D) *reinterpret_cast<uint4*>(o + 32 * q + y) = w;
+        if (q + 1 == DP / 32 && n) {  // O has been read
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(o_empty + i);
         }
+        store_rows16x32(v, inv, o, (long long)a.H * a.D, nr, 32 * q, a.D);
       }
-      if (row < nr[i])
-        a.lse[((long long)t.b * a.H + h) * a.sq.Tq + t.q0 + r] = l == 0.f ? -INFINITY : m * a.scale + kLn2 * log2f(l);
     }
-    tc_fence_before();
   }
+  tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (threadIdx.x == 0 && *dead) report_timeout();
-  if (warp == 9) tmem_dealloc(tmem, 512);
+  if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
 template <int DP>
@@ -323,7 +426,7 @@ cudaError_t run(const AttnProblem& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   Args a;
   a.sq = AttnSeqs::of(p);
-  a.H = p.H, a.Hkv = p.Hkv, a.D = p.D;
+  a.H = p.H, a.G = p.H / p.Hkv, a.D = p.D;
   a.tiles = p.cu_q ? 0 : (p.Tq + 255) / 256;
   a.scale = p.scale, a.c = p.scale * kLog2e;
   a.o = static_cast<__nv_bfloat16*>(p.o), a.lse = p.lse;
