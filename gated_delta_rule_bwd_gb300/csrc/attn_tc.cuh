@@ -96,12 +96,16 @@ __device__ __forceinline__ void drain_loads(uint64_t* full, const Ring<n>& r) {
 // started (cluster launch control), so that setting up barriers and TMEM
 // happens once per SM and the next tile's loads overlap the last one's
 // epilogue, while tiles still go out in the order of the grid, heaviest first.
-// One warp runs the scheduler, a tile ahead: it gets and decodes the next tile
-// and puts it into one of two slots, from which every other warp takes it.
+// One warp runs the scheduler: when the thread that issues the MMAs is some
+// iterations from the end of a tile it gets and decodes the next one and puts it
+// into one of two slots, from which every other warp takes it.  (Asking earlier
+// would deal the tiles out before it is known which SMs are free first: 1.6 times
+// the time for a few long sequences.)
 struct __align__(16) TileSlots {
   int job[2][12];  // what the roles need to know of a tile; [11] = 0: no more tiles
   uint4 response;
   uint64_t full[2], empty[2], response_full;
+  uint64_t soon;  // the issuing thread is near the end of a job
 
   __device__ void init(int takers) {
     for (int i = 0; i < 2; ++i) {
@@ -109,6 +113,7 @@ struct __align__(16) TileSlots {
       mbar_init(empty + i, takers);
     }
     mbar_init(&response_full, 1);
+    mbar_init(&soon, 1);
   }
 };
 
@@ -166,6 +171,31 @@ __device__ __forceinline__ bool next_cta(TileSlots* ts, uint32_t& ph, int& x, vo
   __syncwarp();
   x = (int)at;
   return got != 0;
+}
+
+// The scheduler warp.  decode(cta, job) fills a job or says that the CTA's tile is
+// empty; early(job) and late(job) do what else a running job needs from this
+// warp, before and after the next job is put out.
+template <class Decode, class Early, class Late>
+__device__ __forceinline__ void schedule(TileSlots* slots, volatile int* dead, Decode decode, Early early, Late late) {
+  Ring<2> put;
+  int cta = blockIdx.x, j[12], now[12];
+  uint32_t ph = 0, soon_ph = 0;
+  bool left = true, more = false;
+  while (left && !(more = decode(cta, j))) left = next_cta(slots, ph, cta, dead);
+  j[11] = more;
+  bool ok = put_job(slots, put, j, dead);
+  while (ok && more) {
+#pragma unroll
+    for (int i = 0; i < 12; ++i) now[i] = j[i];
+    if (!early(now) || !warp_wait_live(&slots->soon, soon_ph, dead)) break;
+    soon_ph ^= 1;
+    more = false;
+    left = left && next_cta(slots, ph, cta, dead);
+    while (left && !(more = decode(cta, j))) left = next_cta(slots, ph, cta, dead);
+    j[11] = more;
+    ok = put_job(slots, put, j, dead) && late(now);
+  }
 }
 
 // ---------------------------------------------------------------- MMA with A in TMEM

@@ -185,13 +185,8 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       const uint64_t dv = sw128_desc(smem_u32(sm), 16384, 1024);  // MN-major, 64-column blocks 16 KB apart
       constexpr uint32_t id_s = idesc_bf16(128, 128, false, false), id_o = idesc_bf16(128, DP, false, true);
       Ring<C::kStages> kv;  // the next tile to wait for
-      uint32_t qph = 0, pph = 0, oph = 0, fph = 0;  // parities, one bit per tile
+      uint32_t qph0 = 0, qph1 = 0, pph0 = 0, pph1 = 0, oph0 = 0, oph1 = 0, fph = 0;
       bool ok = true;
-      auto flip = [](uint32_t& ph, int i) {
-        const uint32_t old = (ph >> i) & 1;
-        ph ^= 1u << i;
-        return old;
-      };
       auto qk = [&](int i, int stage) {
         const uint64_t q = desc_at(dq, i * C::kTile), k = desc_at(dq, (2 + stage) * C::kTile);
 #pragma unroll
@@ -201,54 +196,69 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         mma_commit(s_full + i);
       };
+      // P V of key tile x from stage vs, then Q K^T of tile x + 1 from stage ks
+      auto turn = [&](int i, int x, int n, int vs, int ks, uint32_t& pph, uint32_t& oph) {
+        if (x >= n) return true;
+        if (x == 0) {  // the job before has read O
+          if (!wait_live(o_empty + i, oph ^ 1, dead)) return false;
+          oph ^= 1;
+        }
+        if (!wait_live(p_full + i, pph, dead)) return false;
+        pph ^= 1;
+        tc_fence_after();
+        const uint64_t v = desc_at(dv, (2 + vs) * C::kTile);
+#pragma unroll
+        for (int y = 0; y < 8; ++y)
+          mma_bf16_ts(tmem + C::kO + DP * i, tmem + C::kS + 128 * i + 8 * y, desc_at(v, y * 2048), id_o, x > 0 || y > 0);
+        if (x + 1 < n) {
+          qk(i, ks);
+          if (x + 2 == n) mma_commit(q_empty + i);
+        } else {
+          mma_commit(o_full + i);
+        }
+        return true;
+      };
       while (const int* j = ok ? next_job(slots, take, false, dead) : nullptr) {
         const int n0 = j[kN0], n1 = j[kN1], nmax = max(n0, n1);
         const bool fix = j[kFix];
         job_done(slots, take, false);
-        // pass x: P V of key tile x (x >= 0), then Q K^T of tile x + 1, per query tile
-        int vs = 0;
+        if (!nmax) {
+          mbar_arrive(&slots->soon);
+          continue;
+        }
+        if (!(ok = wait_live(kv_full + kv.i, kv.ph, dead))) break;
+        if (n0) {
+          if (!(ok = wait_live(q_full, qph0, dead))) break;
+          qph0 ^= 1;
+          qk(0, kv.i);
+          if (n0 == 1) mma_commit(q_empty);
+        }
+        if (n1) {
+          if (!(ok = wait_live(q_full + 1, qph1, dead))) break;
+          qph1 ^= 1;
+          qk(1, kv.i);
+          if (n1 == 1) mma_commit(q_empty + 1);
+        }
+        mma_commit(kv_empty + kv.i);
+        kv.next();
 #pragma unroll 1
-        for (int x = -1; x < nmax && ok; ++x) {
-          if (x >= 0) {
-            vs = kv.i;
-            ok = wait_live(kv_full + vs, kv.ph, dead);
-            kv.next();
-          }
+        for (int x = 0; x < nmax; ++x) {
+          if (x == max(0, nmax - 2)) mbar_arrive(&slots->soon);
+          const int vs = kv.i;
+          if (!(ok = wait_live(kv_full + vs, kv.ph, dead))) break;
+          kv.next();
           const int ks = kv.i;
           const bool more = x + 1 < nmax;
           if (more) {
-            ok = ok && wait_live(kv_full + ks, kv.ph, dead);
+            if (!(ok = wait_live(kv_full + ks, kv.ph, dead))) break;
             kv.next();
-          } else if (ok && fix) {
+          } else if (fix) {
             mbar_arrive(v_landed);
-            ok = wait_live(v_fixed, fph, dead);
+            if (!(ok = wait_live(v_fixed, fph, dead))) break;
             fph ^= 1;
           }
-          const uint64_t v = desc_at(dv, (2 + vs) * C::kTile);
-#pragma unroll 1
-          for (int i = 0; i < 2; ++i) {
-            const int n = i ? n1 : n0;
-            if (!ok || n == 0 || x >= n) continue;
-            if (x < 0) {
-              ok = wait_live(q_full + i, flip(qph, i), dead);
-            } else {
-              if (x == 0) ok = wait_live(o_empty + i, flip(oph, i) ^ 1, dead);  // the job before has read O
-              ok = ok && wait_live(p_full + i, flip(pph, i), dead);
-              if (ok) {
-                tc_fence_after();
-                const uint32_t o = tmem + C::kO + DP * i, p = tmem + C::kS + 128 * i;
-#pragma unroll
-                for (int y = 0; y < 8; ++y)
-                  mma_bf16_ts(o, p + 8 * y, desc_at(v, y * 2048), id_o, x > 0 || y > 0);
-                if (x + 1 == n) mma_commit(o_full + i);
-              }
-            }
-            if (ok && x + 1 < n) {
-              qk(i, ks);
-              if (x + 2 == n) mma_commit(q_empty + i);
-            }
-          }
-          if (x >= 0) mma_commit(kv_empty + vs);
+          if (!(ok = turn(0, x, n0, vs, ks, pph0, oph0) && turn(1, x, n1, vs, ks, pph1, oph1))) break;
+          mma_commit(kv_empty + vs);
           if (more) mma_commit(kv_empty + ks);
         }
       }
@@ -257,32 +267,23 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         mbar_wait(drain, 0, 10000);
       }
     } else if (warp == 18) {
-      // ------------------------------------------------------------ tiles, one ahead; foreign rows
-      int cta = blockIdx.x, it = 0;  // it: K and V tiles so far
-      bool left = true, ok = true;
-      uint32_t ph = 0, fph = 0;
-      int j[12];
-      // fix: V tile it - 1 of the ring, from row `rows` on
-      int fix = 0, rows = 0, fix_it = 0;
-      for (bool more = true; ok && more;) {
-        more = false;
-        while (left && !(more = decode(a, cta, gridDim.x, j))) left = next_cta(slots, ph, cta, dead);
-        j[kValid] = more;
-        ok = put_job(slots, take, j, dead);
-        if (ok && fix) {  // of the job before: its last V tile comes while this one waits
-          ok = warp_wait_live(v_landed, fph, dead);
-          fph ^= 1;
-          if (ok) {
-            zero_rows<C::NH>(sm + (2 + (fix_it - 1) % C::kStages) * C::kTile, rows, lane);
+      // ------------------------------------------------------------ the next tiles; foreign rows
+      int it = 0;  // K and V tiles so far
+      uint32_t ph = 0;
+      const int ctas = gridDim.x;
+      schedule(
+          slots, dead, [&](int cta, int(&j)[12]) { return decode(a, cta, ctas, j); },
+          [](const int(&)[12]) { return true; },
+          [&](const int(&j)[12]) {
+            const int n = max(j[kN0], j[kN1]);
+            it += 2 * n;
+            if (!j[kFix]) return true;
+            if (!warp_wait_live(v_landed, ph, dead)) return false;
+            ph ^= 1;
+            zero_rows<C::NH>(sm + (2 + (it - 1) % C::kStages) * C::kTile, j[kLk] - (n - 1) * 128, lane);
             if (lane == 0) mbar_arrive(v_fixed);
-          }
-        }
-        if (more) {
-          const int n = max(j[kN0], j[kN1]);
-          it += 2 * n, fix = j[kFix], fix_it = it, rows = j[kLk] - (n - 1) * 128;
-          left = left && next_cta(slots, ph, cta, dead);
-        }
-      }
+            return true;
+          });
     }
     __syncwarp();
   } else {
