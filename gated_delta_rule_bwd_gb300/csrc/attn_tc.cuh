@@ -212,6 +212,40 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       : "memory");
 }
 
+// The products of the attention kernels.  The descriptors step from MMA to MMA
+// and are hidden from the optimiser in between: as constants off a loop
+// invariant base it would keep all of them in registers and spill.
+__device__ __forceinline__ void step_desc(uint64_t& d, uint32_t bytes) {
+  d += bytes >> 4;
+  asm volatile("" : "+l"(d));
+}
+
+// D = A B^T over DP columns: both tiles of 128 rows, K-major in shared memory
+template <int DP>
+__device__ __forceinline__ void mma_rows(uint32_t d, uint64_t a, uint64_t b) {
+  constexpr uint32_t id = idesc_bf16(128, 128, false, false);
+#pragma unroll
+  for (int k = 0; k < DP / 16; ++k) {
+    if (k) {
+      step_desc(a, k % 4 ? 32 : 16384 - 96);
+      step_desc(b, k % 4 ? 32 : 16384 - 96);
+    }
+    mma_bf16(d, a, b, id, k > 0);
+  }
+}
+
+// D (+)= A B over 128: A in TMEM, its K-step k at column a + (k / per) * skip +
+// (k % per) * 8; B a tile of 128 rows, DP columns, in shared memory (MN-major)
+template <int DP, int per, int skip>
+__device__ __forceinline__ void mma_sum(uint32_t d, uint32_t a, uint64_t b, bool acc) {
+  constexpr uint32_t id = idesc_bf16(128, DP, false, true);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    if (k) step_desc(b, 2048);
+    mma_bf16_ts(d, a + (k / per) * skip + (k % per) * 8, b, id, acc || k > 0);
+  }
+}
+
 // ---------------------------------------------------------------- TMEM in flight
 
 // 32 columns without the wait; the values may be used after tmem_landed().

@@ -70,28 +70,6 @@ struct Args {
   __nv_bfloat16 *dq, *dk, *dv;
 };
 
-// The TMEM column of K-step k of an operand written by the four column groups.
-__device__ __forceinline__ uint32_t a_col(int k) { return (k >> 1) * 32 + (k & 1) * 8; }
-
-// K-major product over DP: D = A B^T (both tiles of 128 rows in shared memory)
-template <int DP>
-__device__ __forceinline__ void mma_rows(uint32_t d, uint64_t da, uint64_t db) {
-  constexpr uint32_t id = idesc_bf16(128, 128, false, false);
-#pragma unroll
-  for (int k = 0; k < DP / 16; ++k) {
-    const uint32_t off = (k / 4) * 16384 + (k % 4) * 32;
-    mma_bf16(d, desc_at(da, off), desc_at(db, off), id, k > 0);
-  }
-}
-
-// D (+)= A B over 128: A in TMEM (see a_col), B a tile of 128 rows, DP columns
-template <int DP>
-__device__ __forceinline__ void mma_sum(uint32_t d, uint32_t a, uint64_t db, bool acc) {
-  constexpr uint32_t id = idesc_bf16(128, DP, false, true);
-#pragma unroll
-  for (int k = 0; k < 8; ++k) mma_bf16_ts(d, a + a_col(k), desc_at(db, k * 2048), id, acc || k > 0);
-}
-
 // A warp's 32 rows x n fp32 columns of an accumulator, times f, as bf16: row r to
 // base + r * stride, columns from c0 on; rows below `rows`, columns below D.
 template <int n>
@@ -271,7 +249,7 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
           }
           if (!(ok = wait_live(p_full, ph, dead))) break;
           tc_fence_after();
-          mma_sum<DP>(tmem + kAcc, tmem + kS, desc_at(cols, (5 + rv.i) * C::kTile), it > 0);
+          mma_sum<DP, 2, 32>(tmem + kAcc, tmem + kS, desc_at(cols, (5 + rv.i) * C::kTile), it > 0);
           mma_commit(do_empty + rv.i);
           rv.next();
           if (it + 1 < N) {
@@ -281,7 +259,7 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
           if (!(ok = wait_live(ds_full, ph, dead))) break;
           ph ^= 1;
           tc_fence_after();
-          mma_sum<DP>(tmem + kAcc + DP, tmem + kDP, desc_at(cols, (2 + rk.i) * C::kTile), it > 0);
+          mma_sum<DP, 2, 32>(tmem + kAcc + DP, tmem + kDP, desc_at(cols, (2 + rk.i) * C::kTile), it > 0);
           mma_commit(q_empty + rk.i);
           rk.next();
           if (it + 1 < N) {
@@ -637,7 +615,7 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           }
           if (!(ok = wait_live(ds_full + sd.i, sd.ph, dead))) break;
           tc_fence_after();
-          mma_sum<DP>(tmem + kDQ, tmem + kS + 128 * sd.i, desc_at(cols, (2 + rd.i) * C::kTile), x > 0);
+          mma_sum<DP, 2, 32>(tmem + kDQ, tmem + kS + 128 * sd.i, desc_at(cols, (2 + rd.i) * C::kTile), x > 0);
           mma_commit(k_empty + rd.i);
           rd.next();
           sd.next();

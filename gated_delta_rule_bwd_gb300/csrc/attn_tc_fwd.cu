@@ -183,17 +183,11 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       // ------------------------------------------------------------ MMAs
       const uint64_t dq = sw128_desc(smem_u32(sm), 16, 1024);     // K-major
       const uint64_t dv = sw128_desc(smem_u32(sm), 16384, 1024);  // MN-major, 64-column blocks 16 KB apart
-      constexpr uint32_t id_s = idesc_bf16(128, 128, false, false), id_o = idesc_bf16(128, DP, false, true);
       Ring<C::kStages> kv;  // the next tile to wait for
       uint32_t qph0 = 0, qph1 = 0, pph0 = 0, pph1 = 0, oph0 = 0, oph1 = 0, fph = 0;
       bool ok = true;
       auto qk = [&](int i, int stage) {
-        const uint64_t q = desc_at(dq, i * C::kTile), k = desc_at(dq, (2 + stage) * C::kTile);
-#pragma unroll
-        for (int x = 0; x < DP / 16; ++x) {
-          const uint32_t off = (x / 4) * 16384 + (x % 4) * 32;
-          mma_bf16(tmem + C::kS + 128 * i, desc_at(q, off), desc_at(k, off), id_s, x > 0);
-        }
+        mma_rows<DP>(tmem + C::kS + 128 * i, desc_at(dq, i * C::kTile), desc_at(dq, (2 + stage) * C::kTile));
         mma_commit(s_full + i);
       };
       // P V of key tile x from stage vs, then Q K^T of tile x + 1 from stage ks
@@ -206,10 +200,7 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (!wait_live(p_full + i, pph, dead)) return false;
         pph ^= 1;
         tc_fence_after();
-        const uint64_t v = desc_at(dv, (2 + vs) * C::kTile);
-#pragma unroll
-        for (int y = 0; y < 8; ++y)
-          mma_bf16_ts(tmem + C::kO + DP * i, tmem + C::kS + 128 * i + 8 * y, desc_at(v, y * 2048), id_o, x > 0 || y > 0);
+        mma_sum<DP, 8, 0>(tmem + C::kO + DP * i, tmem + C::kS + 128 * i, desc_at(dv, (2 + vs) * C::kTile), x > 0);
         if (x + 1 < n) {
           qk(i, ks);
           if (x + 2 == n) mma_commit(q_empty + i);
