@@ -234,13 +234,13 @@ __device__ __forceinline__ void mma_rows(uint32_t d, uint64_t a, uint64_t b) {
   }
 }
 
-// D (+)= A B over 128: A in TMEM, its K-step k at column a + (k / per) * skip +
-// (k % per) * 8; B a tile of 128 rows, DP columns, in shared memory (MN-major)
-template <int DP, int per, int skip>
+// D (+)= A B over 16 n: A in TMEM, its K-step k at column a + (k / per) * skip +
+// (k % per) * 8; B rows of a tile, DP columns, in shared memory (MN-major)
+template <int DP, int n, int per = n, int skip = 0>
 __device__ __forceinline__ void mma_sum(uint32_t d, uint32_t a, uint64_t b, bool acc) {
   constexpr uint32_t id = idesc_bf16(128, DP, false, true);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
+  for (int k = 0; k < n; ++k) {
     if (k) step_desc(b, 2048);
     mma_bf16_ts(d, a + (k / per) * skip + (k % per) * 8, b, id, acc || k > 0);
   }

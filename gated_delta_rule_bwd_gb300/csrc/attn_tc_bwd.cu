@@ -249,7 +249,7 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
           }
           if (!(ok = wait_live(p_full, ph, dead))) break;
           tc_fence_after();
-          mma_sum<DP, 2, 32>(tmem + kAcc, tmem + kS, desc_at(cols, (5 + rv.i) * C::kTile), it > 0);
+          mma_sum<DP, 8, 2, 32>(tmem + kAcc, tmem + kS, desc_at(cols, (5 + rv.i) * C::kTile), it > 0);
           mma_commit(do_empty + rv.i);
           rv.next();
           if (it + 1 < N) {
@@ -259,7 +259,7 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
           if (!(ok = wait_live(ds_full, ph, dead))) break;
           ph ^= 1;
           tc_fence_after();
-          mma_sum<DP, 2, 32>(tmem + kAcc + DP, tmem + kDP, desc_at(cols, (2 + rk.i) * C::kTile), it > 0);
+          mma_sum<DP, 8, 2, 32>(tmem + kAcc + DP, tmem + kDP, desc_at(cols, (2 + rk.i) * C::kTile), it > 0);
           mma_commit(q_empty + rk.i);
           rk.next();
           if (it + 1 < N) {
@@ -615,7 +615,7 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           }
           if (!(ok = wait_live(ds_full + sd.i, sd.ph, dead))) break;
           tc_fence_after();
-          mma_sum<DP, 2, 32>(tmem + kDQ, tmem + kS + 128 * sd.i, desc_at(cols, (2 + rd.i) * C::kTile), x > 0);
+          mma_sum<DP, 8, 2, 32>(tmem + kDQ, tmem + kS + 128 * sd.i, desc_at(cols, (2 + rd.i) * C::kTile), x > 0);
           mma_commit(k_empty + rd.i);
           rd.next();
           sd.next();

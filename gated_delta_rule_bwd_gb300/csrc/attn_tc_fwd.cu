@@ -96,8 +96,8 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   uint64_t* q_full = reinterpret_cast<uint64_t*>(slots + 1);  // [2]
   uint64_t* q_empty = q_full + 2;                             // [2]
   uint64_t* s_full = q_empty + 2;                             // [2]
-  uint64_t* p_full = s_full + 2;                              // [2]
-  uint64_t* o_full = p_full + 2;                              // [2]
+  uint64_t* p_full = s_full + 2;                              // [2][2]: per half of the keys
+  uint64_t* o_full = p_full + 4;                              // [2]
   uint64_t* o_empty = o_full + 2;                             // [2]
   uint64_t* v_landed = o_empty + 2;  // a job's last V tile is there; its foreign rows are zero
   uint64_t* v_fixed = v_landed + 1;
@@ -117,7 +117,8 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       mbar_init(q_full + i, 1);
       mbar_init(q_empty + i, 1);
       mbar_init(s_full + i, 1);
-      mbar_init(p_full + i, 8);
+      mbar_init(p_full + 2 * i, 8);
+      mbar_init(p_full + 2 * i + 1, 8);
       mbar_init(o_full + i, 1);
       mbar_init(o_empty + i, 8);
     }
@@ -197,10 +198,16 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           if (!wait_live(o_empty + i, oph ^ 1, dead)) return false;
           oph ^= 1;
         }
-        if (!wait_live(p_full + i, pph, dead)) return false;
+        // the first 64 keys' products run while the others' exponentials are made
+        const uint32_t o = tmem + C::kO + DP * i, p = tmem + C::kS + 128 * i;
+        const uint64_t v = desc_at(dv, (2 + vs) * C::kTile);
+        if (!wait_live(p_full + 2 * i, pph, dead)) return false;
+        tc_fence_after();
+        mma_sum<DP, 4>(o, p, v, x > 0);
+        if (!wait_live(p_full + 2 * i + 1, pph, dead)) return false;
         pph ^= 1;
         tc_fence_after();
-        mma_sum<DP, 8, 0>(tmem + C::kO + DP * i, tmem + C::kS + 128 * i, desc_at(dv, (2 + vs) * C::kTile), x > 0);
+        mma_sum<DP, 4>(o, p + 32, desc_at(v, 8192), true);
         if (x + 1 < n) {
           qk(i, ks);
           if (x + 2 == n) mma_commit(q_empty + i);
@@ -232,25 +239,39 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         mma_commit(kv_empty + kv.i);
         kv.next();
+        int vs = kv.i, ks = 0;  // V of key tile x, K of x + 1
+        if (!(ok = wait_live(kv_full + vs, kv.ph, dead))) break;
+        kv.next();
+        if (nmax > 1) {
+          ks = kv.i;
+          if (!(ok = wait_live(kv_full + ks, kv.ph, dead))) break;
+          kv.next();
+        }
 #pragma unroll 1
         for (int x = 0; x < nmax; ++x) {
           if (x == max(0, nmax - 2)) mbar_arrive(&slots->soon);
-          const int vs = kv.i;
-          if (!(ok = wait_live(kv_full + vs, kv.ph, dead))) break;
-          kv.next();
-          const int ks = kv.i;
-          const bool more = x + 1 < nmax;
-          if (more) {
-            if (!(ok = wait_live(kv_full + ks, kv.ph, dead))) break;
-            kv.next();
-          } else if (fix) {
+          if (fix && x + 1 == nmax) {
             mbar_arrive(v_landed);
             if (!(ok = wait_live(v_fixed, fph, dead))) break;
             fph ^= 1;
           }
-          if (!(ok = turn(0, x, n0, vs, ks, pph0, oph0) && turn(1, x, n1, vs, ks, pph1, oph1))) break;
+          if (!(ok = turn(0, x, n0, vs, ks, pph0, oph0))) break;
+          // the other tile is still in its softmax: time to wait for the next loads
+          int vn = 0, kn = 0;
+          if (x + 1 < nmax) {
+            vn = kv.i;
+            if (!(ok = wait_live(kv_full + vn, kv.ph, dead))) break;
+            kv.next();
+          }
+          if (x + 2 < nmax) {
+            kn = kv.i;
+            if (!(ok = wait_live(kv_full + kn, kv.ph, dead))) break;
+            kv.next();
+          }
+          if (!(ok = turn(1, x, n1, vs, ks, pph1, oph1))) break;
           mma_commit(kv_empty + vs);
-          if (more) mma_commit(kv_empty + ks);
+          if (x + 1 < nmax) mma_commit(kv_empty + ks);
+          vs = vn, ks = kn;
         }
       }
       if (*dead) {
@@ -354,11 +375,11 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             p[y] = pack_bf16(e0, e1);
           }
           tmem_st16x32_start(ts + 32 * q, p);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full + 2 * i + q);
         }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + i);
       }
       if (ok && n) {
         ok = warp_wait_live(o_full + i, oph, dead);
