@@ -38,16 +38,17 @@ __device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
 }
 
 // Bounded wait that also gives up once another warp of the CTA has
-// (*dead != 0); running out (about two seconds) sets *dead.
+// (*dead != 0); running out (after a second or more: a poll is tens of cycles at
+// least) sets *dead.  Kept small: it stands at every hand-over, and what does not
+// fit the instruction cache is fetched again at every turn of a job.
 __device__ __forceinline__ bool wait_live(uint64_t* bar, uint32_t parity, volatile int* dead) {
-  if (try_wait(bar, parity)) return true;
-  const long long begin = clock64();
-  for (uint32_t i = 0; clock64() - begin < 4000000000LL; ++i) {
-    if (try_wait(bar, parity)) return true;
-    if (*dead) return false;
+  bool ok = try_wait(bar, parity);
+#pragma unroll 1
+  for (uint32_t i = 0; !ok && !*dead; ++i) {
+    ok = try_wait(bar, parity);
+    if (i == (1u << 25)) *dead = 1;
   }
-  *dead = 1;
-  return false;
+  return ok;
 }
 
 // One lane of a converged warp.  A role that one lane plays is put behind it
@@ -139,6 +140,7 @@ __device__ __forceinline__ bool put_job(TileSlots* ts, Ring<2>& r, const int (&j
       *reinterpret_cast<int4*>(ts->job[r.i] + i) = make_int4(j[i], j[i + 1], j[i + 2], j[i + 3]);
     mbar_arrive(ts->full + r.i);
   }
+  __syncwarp();
   r.next();
   return true;
 }
@@ -175,26 +177,32 @@ __device__ __forceinline__ bool next_cta(TileSlots* ts, uint32_t& ph, int& x, vo
 
 // The scheduler warp.  decode(cta, job) fills a job or says that the CTA's tile is
 // empty; early(job) and late(job) do what else a running job needs from this
-// warp, before and after the next job is put out.
+// warp, before and after the next job is put out (they read it from its slot,
+// which is rewritten only by the job after the next).
 template <class Decode, class Early, class Late>
 __device__ __forceinline__ void schedule(TileSlots* slots, volatile int* dead, Decode decode, Early early, Late late) {
   Ring<2> put;
-  int cta = blockIdx.x, j[12], now[12];
+  int cta = blockIdx.x, j[12];
   uint32_t ph = 0, soon_ph = 0;
-  bool left = true, more = false;
-  while (left && !(more = decode(cta, j))) left = next_cta(slots, ph, cta, dead);
-  j[11] = more;
-  bool ok = put_job(slots, put, j, dead);
-  while (ok && more) {
-#pragma unroll
-    for (int i = 0; i < 12; ++i) now[i] = j[i];
-    if (!early(now) || !warp_wait_live(&slots->soon, soon_ph, dead)) break;
-    soon_ph ^= 1;
-    more = false;
-    left = left && next_cta(slots, ph, cta, dead);
-    while (left && !(more = decode(cta, j))) left = next_cta(slots, ph, cta, dead);
+  bool left = true, fresh = true;
+  const volatile int* now = nullptr;
+  for (;;) {
+    if (now) {
+      if (!early(now) || !warp_wait_live(&slots->soon, soon_ph, dead)) break;
+      soon_ph ^= 1;
+    }
+    bool more = false;
+    while (left && !more) {  // the next CTA whose tile is not empty
+      if (!fresh) left = next_cta(slots, ph, cta, dead);
+      fresh = false;
+      if (left) more = decode(cta, j);
+    }
     j[11] = more;
-    ok = put_job(slots, put, j, dead) && late(now);
+    const volatile int* next = slots->job[put.i];
+    if (!put_job(slots, put, j, dead)) break;
+    if (now && !late(now)) break;
+    if (!more) break;
+    now = next;
   }
 }
 
@@ -386,6 +394,17 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// 1 / x and log2 x, the hardware approximations (1 ulp; 2^-22)
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 // 2^x, the hardware approximation (2 ulp; 0 for -inf)
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -468,10 +487,10 @@ __device__ __forceinline__ void load_tile(void* dst, const CUtensorMap* tm, uint
 // product with a zero probability would still carry over its infinities.
 template <int NH>
 __device__ __forceinline__ void zero_rows(unsigned char* tile, int r0, int lane) {
+#pragma unroll 1
+  for (int c = r0 * 8 + lane; c < 128 * 8; c += 32)
 #pragma unroll
-  for (int i = 0; i < NH; ++i)
-    for (int c = r0 * 8 + lane; c < 128 * 8; c += 32)
-      *reinterpret_cast<uint4*>(tile + i * 16384 + c * 16) = make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < NH; ++i) *reinterpret_cast<uint4*>(tile + i * 16384 + c * 16) = make_uint4(0, 0, 0, 0);
   fence_async_shared();
   __syncwarp();
 }

@@ -313,7 +313,7 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       // ------------------------------------------------------------ the next tiles; foreign rows
       int it = 0, head = 0;  // iterations of the jobs before; heads of this one
       uint32_t ph = 0;
-      auto clean = [&](const int(&j)[12]) {
+      auto clean = [&](const volatile int* j) {
         if (!packed || j[kLq] % 128 == 0 || !j[kNi]) return true;
         if (!warp_wait_live(landed, ph, dead)) return false;
         ph ^= 1;
@@ -321,6 +321,7 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         zero_rows<C::NH>(sm + (2 + x % 3) * C::kTile, j[kLq] % 128, lane);
         zero_rows<C::NH>(sm + (5 + (x & 1)) * C::kTile, j[kLq] % 128, lane);
         if (lane == 0) mbar_arrive(fixed);
+        __syncwarp();
         return true;
       };
       schedule(
@@ -336,13 +337,13 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             j[kI0] = max(0, j[kJs]) / 128, j[kNi] = max(0, (t.lq + 127) / 128 - j[kI0]);
             return true;
           },
-          [&](const int(&j)[12]) {  // every head's last tiles but the last head's
+          [&](const volatile int* j) {  // every head's last tiles but the last head's
             head = 0;
             for (int g = 1; g < G; ++g)
               if (!clean(j)) return false;
             return true;
           },
-          [&](const int(&j)[12]) {
+          [&](const volatile int* j) {
             const bool ok = clean(j);
             it += j[kNi] * G;
             return ok;
@@ -645,14 +646,15 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             j[qFirst] = r0 + t.lk - t.lq, j[qN] = (max(0, min(t.lk, j[qFirst] + nr)) + 127) / 128;
             return true;
           },
-          [](const int(&)[12]) { return true; },
-          [&](const int(&j)[12]) {
+          [](const volatile int*) { return true; },
+          [&](const volatile int* j) {
             it += j[qN];
             if (!packed || j[qN] * 128 <= j[qLk]) return true;
             if (!warp_wait_live(landed, ph, dead)) return false;
             ph ^= 1;
             zero_rows<C::NH>(sm + (2 + (it - 1) % 3) * C::kTile, j[qLk] - (j[qN] - 1) * 128, lane);
             if (lane == 0) mbar_arrive(fixed);
+            __syncwarp();
             return true;
           });
     }

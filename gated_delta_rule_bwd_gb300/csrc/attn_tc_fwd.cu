@@ -285,8 +285,8 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       const int ctas = gridDim.x;
       schedule(
           slots, dead, [&](int cta, int(&j)[12]) { return decode(a, cta, ctas, j); },
-          [](const int(&)[12]) { return true; },
-          [&](const int(&j)[12]) {
+          [](const volatile int*) { return true; },
+          [&](const volatile int* j) {
             const int n = max(j[kN0], j[kN1]);
             it += 2 * n;
             if (!j[kFix]) return true;
@@ -294,6 +294,7 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             ph ^= 1;
             zero_rows<C::NH>(sm + (2 + (it - 1) % C::kStages) * C::kTile, j[kLk] - (n - 1) * 128, lane);
             if (lane == 0) mbar_arrive(v_fixed);
+            __syncwarp();
             return true;
           });
     }
@@ -396,10 +397,10 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         float sum = two.x + two.y;
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        inv[r] = sum == 0.f ? 0.f : 1.f / sum;
+        inv[r] = sum == 0.f ? 0.f : rcp(sum);
         if (col == 0 && lane / 4 + 8 * r < nr)
           a.lse[((long long)b * a.H + h) * a.sq.Tq + q0 + lane / 4 + 8 * r] =
-              sum == 0.f ? -INFINITY : m[r] * a.scale + kLn2 * log2f(sum);
+              sum == 0.f ? -INFINITY : m[r] * a.scale + kLn2 * lg2(sum);
       }
       __nv_bfloat16* o = a.o + (((long long)b * a.sq.Tq + q0) * a.H + h) * a.D;
 #pragma unroll 1
