@@ -42,13 +42,14 @@ __device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
 // least) sets *dead.  Kept small: it stands at every hand-over, and what does not
 // fit the instruction cache is fetched again at every turn of a job.
 __device__ __forceinline__ bool wait_live(uint64_t* bar, uint32_t parity, volatile int* dead) {
-  bool ok = try_wait(bar, parity);
+  if (try_wait(bar, parity)) return true;
 #pragma unroll 1
-  for (uint32_t i = 0; !ok && !*dead; ++i) {
-    ok = try_wait(bar, parity);
-    if (i == (1u << 25)) *dead = 1;
+  for (uint32_t i = 0; i < (1u << 25); ++i) {
+    if (try_wait(bar, parity)) return true;
+    if (*dead) return false;
   }
-  return ok;
+  *dead = 1;
+  return false;
 }
 
 // One lane of a converged warp.  A role that one lane plays is put behind it

@@ -13,6 +13,10 @@
 // 8 in the exponent; P is then at most 2^8, which costs no bits, and the
 // rescaling passes over O in TMEM nearly vanish.
 //
+// Where there are fewer such jobs than SMs, each is split along its keys into
+// parts that write o (fp32) and lse to the workspace; a second kernel joins them:
+// o = sum_p exp(lse_p - lse) o_p, lse = log sum_p exp(lse_p).
+//
 // Warps 0-7 and 8-15 are the two tiles' softmax, warp 16 issues the TMA loads (a
 // ring of K and V tiles), warp 17 the MMAs, warp 18 gets the next tiles and zeroes
 // the rows of a packed sequence's last V tile that belong to the next one.  CTAs
@@ -25,6 +29,8 @@
 // instructions come from beyond the instruction cache, at some 2 cycles a byte.
 
 #include <math.h>
+
+#include <algorithm>
 
 #include "attn_tc.cuh"
 
@@ -41,6 +47,7 @@ using namespace tc;
 constexpr int kSoftmax = 512, kThreads = kSoftmax + 128;
 // 96 registers a thread at launch: 512 * 104 + 128 * 64 = 640 * 96
 constexpr int kRegSoftmax = 104, kRegOther = 64;
+constexpr int kMaxParts = 32;  // of a job's keys: a lane each when they are joined
 constexpr float kLag = 8.f;  // exponent by which the row maximum may lag
 
 template <int DP>
@@ -56,33 +63,39 @@ struct Cfg {
 struct Args {
   AttnSeqs sq;
   int H, G, D, tiles;  // tiles: 256-row tiles per batch row (0: packed)
+  int parts;           // of a job's keys
   float c, scale;
   __nv_bfloat16* o;
-  float* lse;
+  float* lse;          // parts > 1: [parts][B, H, Tq] in the workspace
+  float* po;           // parts > 1: [parts][B, Tq, H, D]
 };
 
 // A job (256 query rows of one head) as the scheduler hands it out.
-enum { kHead, kB, kQ0, kK0, kLk, kFirst, kNr0, kNr1, kN0, kN1, kFix, kValid };
-// kQ0, kK0: first query and key token; kFirst: the last key that the first row
-// sees; kNr: rows of each 128-row tile; kN: key tiles they see; kFix: the last
-// key tile holds rows of the next packed sequence.
+enum { kHead, kPart, kQ0, kK0, kLk, kFirst, kNr, kB, kN0, kN1, kFix, kValid };
+// kQ0, kK0: first query and key token; kLk: keys; kFirst: the last key that the
+// first row sees (both counted from kK0); kNr: rows; kN: key tiles that each
+// 128-row tile sees; kFix: the last one holds rows of the next packed sequence.
 
 __device__ __forceinline__ bool decode(const Args& a, int cta, int ctas, int (&j)[12]) {
   // the tiles with the most keys first
-  const int u = cta / a.H;
-  const int slot = a.tiles ? u % a.sq.B * a.tiles + a.tiles - 1 - u / a.sq.B : ctas / a.H - 1 - u;
+  const int part = cta % a.parts, u = cta / a.parts / a.H;
+  const int slot = a.tiles ? u % a.sq.B * a.tiles + a.tiles - 1 - u / a.sq.B : ctas / a.parts / a.H - 1 - u;
   AttnTile t;
   j[kValid] = a.sq.get<false>(slot, 256, t);
   if (!j[kValid]) return false;
   const int r0 = t.tile * 256, shift = t.lk - t.lq;
-  j[kHead] = cta % a.H, j[kB] = t.b, j[kQ0] = t.q0 + r0, j[kK0] = t.k0, j[kLk] = t.lk, j[kFirst] = r0 + shift;
+  j[kHead] = cta / a.parts % a.H, j[kPart] = part, j[kB] = t.b, j[kQ0] = t.q0 + r0, j[kNr] = min(256, t.lq - r0);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int nr = max(0, min(128, t.lq - r0 - 128 * i));
-    j[kNr0 + i] = nr;
-    j[kN0 + i] = nr ? (max(0, min(t.lk, r0 + 128 * i + nr + shift)) + 127) / 128 : 0;
+    const int nr = min(128, j[kNr] - 128 * i);
+    j[kN0 + i] = nr > 0 ? (max(0, min(t.lk, r0 + 128 * i + nr + shift)) + 127) / 128 : 0;
   }
-  j[kFix] = a.sq.cu_q && max(j[kN0], j[kN1]) * 128 > t.lk;
+  // this part's key tiles: [x0, x1) of those that the job sees
+  const int n = max(j[kN0], j[kN1]), x0 = n * part / a.parts, x1 = n * (part + 1) / a.parts;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) j[kN0 + i] = max(0, min(j[kN0 + i], x1) - x0);
+  j[kK0] = t.k0 + x0 * 128, j[kLk] = t.lk - x0 * 128, j[kFirst] = r0 + shift - x0 * 128;
+  j[kFix] = a.sq.cu_q && max(j[kN0], j[kN1]) * 128 > j[kLk];
   return true;
 }
 
@@ -388,7 +401,7 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         tc_fence_after();
       }
       if (!ok) break;
-      const int h = j[kHead], nr = j[kNr0 + i] - w0, q0 = j[kQ0] + 128 * i + w0, b = j[kB];
+      const int h = j[kHead], nr = min(128, j[kNr] - 128 * i) - w0, q0 = j[kQ0] + 128 * i + w0, b = j[kB], part = j[kPart];
       job_done(slots, take, true);
       float inv[2];
 #pragma unroll
@@ -399,10 +412,10 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         inv[r] = sum == 0.f ? 0.f : rcp(sum);
         if (col == 0 && lane / 4 + 8 * r < nr)
-          a.lse[((long long)b * a.H + h) * a.sq.Tq + q0 + lane / 4 + 8 * r] =
+          a.lse[((long long)(part * a.sq.B + b) * a.H + h) * a.sq.Tq + q0 + lane / 4 + 8 * r] =
               sum == 0.f ? -INFINITY : m[r] * a.scale + kLn2 * lg2(sum);
       }
-      __nv_bfloat16* o = a.o + (((long long)b * a.sq.Tq + q0) * a.H + h) * a.D;
+      const long long at = (((long long)(part * a.sq.B + b) * a.sq.Tq + q0) * a.H + h) * a.D;
 #pragma unroll 1
       for (int q = 0; q < DP / 32; ++q) {
         float v[16];
@@ -417,7 +430,17 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           __syncwarp();
           if (lane == 0) mbar_arrive(o_empty + i);
         }
-        store_rows16x32(v, inv, o, (long long)a.H * a.D, nr, 32 * q, a.D);
+        if (a.parts == 1) {
+          store_rows16x32(v, inv, a.o + at, (long long)a.H * a.D, nr, 32 * q, a.D);
+        } else {
+#pragma unroll
+          for (int y = 0; y < 16; y += 2) {
+            const int r = lane / 4 + 4 * (y & 2), x = 32 * q + 2 * y - (y & 2) * 2 + col;
+            if (r < nr && x < a.D)
+              *reinterpret_cast<float2*>(a.po + at + (long long)r * a.H * a.D + x) =
+                  make_float2(v[y] * inv[(y >> 1) & 1], v[y + 1] * inv[(y >> 1) & 1]);
+          }
+        }
       }
     }
   }
@@ -426,6 +449,67 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   tc_fence_after();
   if (threadIdx.x == 0 && *dead) report_timeout();
   if (warp == 17) tmem_dealloc(tmem, 512);
+}
+
+// One warp per (token, head): joins the parts.
+__global__ void __launch_bounds__(256) attn_join_kernel(Args a, __nv_bfloat16* o, float* lse, long long rows) {
+  grid_dep_wait();
+  const long long r = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (r >= rows) return;
+  const int lane = threadIdx.x & 31, h = (int)(r % a.H), Tq = a.sq.Tq;
+  const long long tok = r / a.H, b = tok / Tq, at = (b * a.H + h) * Tq + tok % Tq, all = (long long)a.sq.B * a.H * Tq;
+  // lane p < parts holds part p's lse
+  const float l = lane < a.parts ? a.lse[lane * all + at] : -INFINITY;
+  float m = l;
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+  const float w = m == -INFINITY || l == -INFINITY ? 0.f : ex2((l - m) * kLog2e);
+  float sum = w;
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+  if (lane == 0) lse[at] = sum == 0.f ? -INFINITY : m + kLn2 * lg2(sum);
+  const float f = sum == 0.f ? 0.f : w * rcp(sum);
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int p = 0; p < a.parts; ++p) {
+    const float g = __shfl_sync(0xffffffffu, f, p);
+    if (g == 0.f) continue;  // a part without keys
+    const float* x = a.po + (p * all + r) * a.D + 4 * lane;
+    if (4 * lane < a.D) {
+      const float4 y = *reinterpret_cast<const float4*>(x);
+      acc[0] = fmaf(g, y.x, acc[0]), acc[1] = fmaf(g, y.y, acc[1]);
+      acc[2] = fmaf(g, y.z, acc[2]), acc[3] = fmaf(g, y.w, acc[3]);
+    }
+  }
+  if (4 * lane < a.D)
+    *reinterpret_cast<uint2*>(o + r * a.D + 4 * lane) = make_uint2(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]));
+}
+
+// Parts of a job's keys, from the sizes alone (a packed sequence's own length is
+// on the device: the mean stands for it, and a quarter more for the longest).  The estimate in microseconds: 1.9 per
+// key tile of the longest job, or of the average one times the rounds of jobs
+// over the SMs; 5 for the join's launch, and the parts' o written and read.
+// Measured (one row, D 128; one part -> best number of parts): 2048 tokens and 16
+// heads, 128 jobs, 43 us -> 48 with two, not split; 4096 and 8 heads 69 -> 59;
+// 4096 and 4 heads 68 -> 44; 512 queries, 65536 keys, 8 heads 852 -> 121.
+int parts_of(const AttnProblem& p) {
+  const int nseq = p.cu_q ? std::max(1, p.nseq) : p.B, sms = sm_count();
+  const float tq = (float)p.Tq * p.B / nseq, tk = (float)p.Tk * p.B / nseq;  // mean lengths
+  // a packed sequence's last job is half empty on average
+  const float jobs = (p.cu_q ? tq / 256.f + .5f : (float)((p.Tq + 255) / 256)) * nseq * p.H;
+  if (jobs >= sms) return 1;
+  const float longest = tk / (p.cu_q ? 102.f : 128.f), mean = std::max(tk - std::min(tk, tq) / 2, 0.f) / 128.f;
+  int best = 1;
+  float least = INFINITY;
+  for (int n = 1; n <= kMaxParts; ++n) {
+    const float rounds = ceilf(n * jobs / sms);
+    const float t = 1.9f * std::max(longest, mean * rounds) / n + (n > 1 ? 5.f + 4e-4f * p.D * n * jobs : 0.f);
+    if (t < least) best = n, least = t;
+  }
+  return best;
+}
+
+size_t part_lse_bytes(const AttnProblem& p, int parts) {
+  return align_up((size_t)parts * p.B * p.H * p.Tq * sizeof(float), 256);
 }
 
 template <int DP>
@@ -444,10 +528,23 @@ cudaError_t run(const AttnProblem& p, cudaStream_t s) {
   a.tiles = p.cu_q ? 0 : (p.Tq + 255) / 256;
   a.scale = p.scale, a.c = p.scale * kLog2e;
   a.o = static_cast<__nv_bfloat16*>(p.o), a.lse = p.lse;
+  a.parts = parts_of(p);
+  a.po = nullptr;
+  if (a.parts > 1) {
+    a.lse = static_cast<float*>(p.ws);
+    a.po = reinterpret_cast<float*>(static_cast<unsigned char*>(p.ws) + part_lse_bytes(p, a.parts));
+  }
   prof_before(s);
-  attn_tc_fwd_kernel<DP><<<(unsigned)(AttnSeqs::slots(p, 256, false) * p.H), kThreads, C::kSmem, s>>>(mq, mk, mv, a);
+  attn_tc_fwd_kernel<DP>
+      <<<(unsigned)(AttnSeqs::slots(p, 256, false) * p.H * a.parts), kThreads, C::kSmem, s>>>(mq, mk, mv, a);
   e = cudaGetLastError();
   prof_after(s, kAttnFwd);
+  if (e != cudaSuccess || a.parts == 1) return e;
+  const long long rows = (long long)p.B * p.Tq * p.H;
+  prof_before(s);
+  e = launch_overlapped(attn_join_kernel, (unsigned)((rows + 7) / 8), 256, 0, s, a, static_cast<__nv_bfloat16*>(p.o),
+                        p.lse, rows);
+  prof_after(s, kAttnCombine);
   return e;
 }
 
@@ -456,6 +553,11 @@ cudaError_t run(const AttnProblem& p, cudaStream_t s) {
 bool attn_tc_supported(const AttnProblem& p) {
   return p.bf16 && p.Tq > 0 && p.Tk > 0 && attn_map_ok(p.q, p.B, p.Tq, p.H, p.D, p.qs) &&
          attn_map_ok(p.k, p.B, p.Tk, p.Hkv, p.D, p.ks) && attn_map_ok(p.v, p.B, p.Tk, p.Hkv, p.D, p.vs);
+}
+
+size_t attn_tc_fwd_workspace(const AttnProblem& p) {
+  const int parts = parts_of(p);
+  return parts == 1 ? 0 : part_lse_bytes(p, parts) + (size_t)parts * p.B * p.Tq * p.H * p.D * sizeof(float);
 }
 
 cudaError_t attn_tc_fwd(const AttnProblem& p, cudaStream_t s) {

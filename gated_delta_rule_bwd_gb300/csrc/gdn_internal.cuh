@@ -222,6 +222,7 @@ cudaError_t attn_simt_fwd(const AttnProblem& p, cudaStream_t s);
 cudaError_t attn_simt_bwd(const AttnProblem& p, cudaStream_t s);
 // Tensor-core kernels: bf16, D a multiple of 8, q, k, v fit for tensor maps.
 bool attn_tc_supported(const AttnProblem& p);
+size_t attn_tc_fwd_workspace(const AttnProblem& p);  // reads sizes, cu_q != NULL and nseq
 cudaError_t attn_tc_fwd(const AttnProblem& p, cudaStream_t s);
 cudaError_t attn_tc_bwd(const AttnProblem& p, cudaStream_t s);
 // delta [B, H, Tq] = rowsum(do * o), fp32: the workspace of the backward (both

@@ -77,6 +77,13 @@ int attn_inputs(gdn::AttnProblem* p, const void* q, const void* k, const void* v
   return GDN_OK;
 }
 
+// What the tensor-core kernels would need: whether they run depends on the
+// pointers' alignment too, which a shape does not say.
+size_t fwd_workspace(const gdn::AttnProblem& p) {
+  if (!p.bf16 || p.D % 8 || p.B == 0 || p.Tq == 0 || p.Tk == 0 || p.H == 0) return 0;
+  return gdn::attn_tc_fwd_workspace(p);
+}
+
 int decode_problem(const gdn_attn_decode_shape* s, gdn::AttnDecodeProblem* p) {
   if (!s) return GDN_ERR_ARG;
   int rc = check_heads(s->H, s->Hkv, s->D, s->dtype);
@@ -110,8 +117,11 @@ int ln_problem(const gdn_norm_shape* s, float eps, gdn::LayerNormProblem* p) {
 extern "C" {
 
 size_t gdn_attn_fwd_workspace(const gdn_attn_shape* shape, int nseq) {
-  (void)shape, (void)nseq;
-  return 0;
+  gdn::AttnProblem p;
+  static const int offsets[2] = {0, 0};  // stands for packed sequences; not read
+  const int* cu = nseq > 0 ? offsets : nullptr;
+  if (attn_problem(shape, 1.f, cu, cu, nseq, &p) != GDN_OK) return 0;
+  return fwd_workspace(p);
 }
 
 int gdn_attn_fwd(const gdn_attn_shape* shape, const void* q, const void* k, const void* v, float scale,
@@ -124,7 +134,8 @@ int gdn_attn_fwd(const gdn_attn_shape* shape, const void* q, const void* k, cons
   if (any_null({o, lse})) return GDN_ERR_ARG;
   if ((rc = attn_inputs(&p, q, k, v)) != GDN_OK) return rc;
   if (!all_aligned16({o, lse, ws})) return GDN_ERR_ALIGN;
-  (void)ws_bytes;
+  const size_t need = fwd_workspace(p);
+  if (need > 0 && (!ws || ws_bytes < need)) return GDN_ERR_WORKSPACE;
   p.o = o, p.lse = lse, p.ws = ws;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return done(gdn::attn_tc_supported(p) ? gdn::attn_tc_fwd(p, st) : gdn::attn_simt_fwd(p, st));

@@ -135,6 +135,47 @@ def test_packed(lq, lk, H, Hkv, D, fused, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("lq,lk,H,Hkv,D", [
+    ([1], [4100], 2, 1, 128), ([70], [2050], 3, 3, 64), ([260], [3000], 2, 2, 80),
+    ([1400], [1400], 1, 1, 128), ([300], [2500], 4, 1, 96),
+    ([5, 130, 0, 2], [1500, 131, 70, 6000], 2, 1, 128), ([3000, 40], [1400, 40], 1, 1, 64)])
+def test_few_queries_and_many_keys(lq, lk, H, Hkv, D):
+    """Keys in parts that are joined: parts without keys for some rows, for a
+    whole short sequence, and rows that see no key in any part."""
+    q, k, v, do = inputs(1, sum(lq), sum(lk), H, Hkv, D, BF16, seed=len(lq))
+    s, *_, nseq = gdn._attn_args(q, k, v, cu(lq), cu(lk), None)
+    assert gdn.lib().gdn_attn_fwd_workspace(ctypes.byref(s), nseq) > 0
+    ref, bound = reference(q, k, v, do, lq, lk, D ** -0.5, True)
+    got = run(q, k, v, do, *((lq, lk) if len(lq) > 1 else ()))
+    check(got, ref, bound)
+    # another packed sequence's NaN reaches no row
+    for bad, rows in ((slice(lk[0]), slice(lq[0], None)), (slice(-lk[-1], None), slice(-lq[-1]))):
+        if len(lq) > 1:
+            k2, v2 = k.clone(), v.clone()
+            k2[:, bad] = v2[:, bad] = float("nan")
+            o, lse = gdn.attn_fwd(q, k2, v2, cu(lq), cu(lk))
+            assert torch.equal(o[:, rows], got["o"][:, rows])
+            assert torch.equal(lse[:, :, rows], got["lse"][:, :, rows])
+
+
+@gpu
+def test_workspace_of_parts():
+    """A workspace that is too small or missing is refused before a launch."""
+    q, k, v, _ = inputs(1, 64, 4096, 2, 2, 128, BF16)
+    s, scale, *_ = gdn._attn_args(q, k, v, None, None, None)
+    L, need = gdn.lib(), gdn.lib().gdn_attn_fwd_workspace(ctypes.byref(s), 0)
+    o, lse = torch.empty_like(q), torch.empty(1, 2, 64, device="cuda")
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    call = lambda ptr, n: L.gdn_attn_fwd(  # noqa: E731
+        ctypes.byref(s), q.data_ptr(), k.data_ptr(), v.data_ptr(), scale, None, None, 0,
+        o.data_ptr(), lse.data_ptr(), ptr, n, None)
+    assert call(None, need) == -5 and call(ws.data_ptr(), need - 1) == -5
+    given, given_lse = gdn.attn_fwd(q, k, v, workspace=ws)
+    own, own_lse = gdn.attn_fwd(q, k, v)
+    assert torch.equal(given, own) and torch.equal(given_lse, own_lse)
+
+
+@gpu
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("Tq,Tk", [(1, 700), (130, 1), (64, 0), (0, 5), (200, 460)])
 def test_other_numbers_of_keys(Tq, Tk, dtype):
