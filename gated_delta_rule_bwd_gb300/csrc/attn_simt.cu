@@ -14,15 +14,26 @@
 // consecutive rows touch all banks once.  dk and dv come from a kernel that
 // owns key tiles and sums over the queries (of all heads that share the key
 // head, in order), dq from one that owns query tiles: the scores are computed
-// twice, and nothing is added atomically, so results do not depend on the
-// order in which CTAs run.  Bound by the fp32 FMA rate.
+// twice, and nothing is added atomically, so results do not depend on the order
+// in which CTAs run.  Both are roles of one launch.
+//
+// Small problems have fewer jobs than SMs and are bound by the time of one job's
+// walk, so a cluster of up to eight CTAs shares a job: each walks a range of the
+// other side's tiles, leaves its accumulators in shared memory, and sums a slice
+// of the rows over the cluster, in the order of the ranks.  Larger ones are bound
+// by the fp32 FMA rate.
 
+#include <cooperative_groups.h>
 #include <math.h>
+
+#include <algorithm>
 
 #include "attn.cuh"
 #include "tc_common.cuh"
 
 namespace gdn {
+
+namespace cg = cooperative_groups;
 
 cudaError_t attn_simt_read_and_clear_status(int* status) {
   return tc::read_and_clear_file_status(status);
@@ -38,7 +49,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 struct Args {
   AttnSeqs sq;
   int H, Hkv, D;
+  int ranks;  // CTAs of a cluster, along x
   float scale;
+  bool vec;  // rows of q, k, v and do_ are read in fours
   long long qs[3], ks[3], vs[3];
   const void *q, *k, *v, *do_;
   void* o;
@@ -55,13 +68,34 @@ Args args_of(const AttnProblem& p) {
   a.q = p.q, a.k = p.k, a.v = p.v, a.do_ = p.do_, a.o = p.o, a.lse = p.lse;
   a.delta = static_cast<const float*>(p.ws);
   a.dq = p.dq, a.dk = p.dk, a.dv = p.dv;
+  long long odd = p.D;
+  for (int i = 0; i < 3; ++i) odd |= p.qs[i] | p.ks[i] | p.vs[i];
+  const uintptr_t at = (uintptr_t)p.q | (uintptr_t)p.k | (uintptr_t)p.v | (uintptr_t)p.do_;
+  a.vec = odd % 4 == 0 && at % (p.bf16 ? 8 : 16) == 0;
   return a;
+}
+
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                     __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
 }
 
 // 64 rows of D values (row r at src + r * stride, rows >= n zero) as fp32
 template <typename T, int DP>
-__device__ __forceinline__ void load_tile(float* dst, const T* src, long long stride, int n, int D) {
+__device__ __forceinline__ void load_tile(float* dst, const T* src, long long stride, int n, int D, bool vec) {
   constexpr int LD = DP + 4;
+  if (vec) {
+#pragma unroll
+    for (int x = 0; x < kM * DP / 4 / kThreads; ++x) {
+      const int i = threadIdx.x + x * kThreads, r = i / (DP / 4), c = i % (DP / 4) * 4;
+      *reinterpret_cast<float4*>(dst + r * LD + c) =
+          r < n && c < D ? load4(src + r * stride + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    return;
+  }
+#pragma unroll 4
   for (int i = threadIdx.x; i < kM * DP; i += kThreads) {
     const int r = i / DP, c = i % DP;
     dst[r * LD + c] = (r < n && c < D) ? to_f32(src[r * stride + c]) : 0.f;
@@ -173,20 +207,47 @@ __device__ __forceinline__ float row_sum(float v) {
 template <int DP>
 constexpr int tile_floats() { return kM * (DP + 4); }
 
+// a thread's 4 rows of an accumulator, rows first + i * step, to shared memory
+template <int DP>
+__device__ __forceinline__ void park(float* dst, const float (&acc)[4][DP / 16], int first, int step, int tx) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int u = 0; u < DP / 64; ++u)
+      *reinterpret_cast<float4*>(dst + (first + i * step) * (DP + 4) + 4 * tx + 64 * u) =
+          make_float4(acc[i][4 * u], acc[i][4 * u + 1], acc[i][4 * u + 2], acc[i][4 * u + 3]);
+}
+
+// this rank's slice of a tile's n rows, summed over the cluster's parked tiles
+template <typename T, int DP>
+__device__ __forceinline__ void join_rows(T* dst, long long stride, float* tile, float f, int n, int D, int rank,
+                                          int ranks) {
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int rows = kM / ranks;
+  for (int i = threadIdx.x; i < rows * DP; i += kThreads) {
+    const int r = rank * rows + i / DP, c = i % DP;
+    if (r >= n || c >= D) continue;
+    float sum = 0.f;
+    for (int x = 0; x < ranks; ++x) sum += cluster.map_shared_rank(tile, x)[r * (DP + 4) + c];
+    dst[r * stride + c] = from_f32<T>(sum * f);
+  }
+}
+
 template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads) attn_simt_fwd_kernel(Args a) {
   extern __shared__ float sm[];
   float *Q = sm, *K = Q + tile_floats<DP>(), *V = K + tile_floats<DP>(), *P = V + tile_floats<DP>();
+  const int rank = blockIdx.x % a.ranks;
   if (blockIdx.x == 0 && blockIdx.y == 0 && !a.sq.valid() && threadIdx.x == 0)
     atomicExch(&tc::g_file_status, GDN_ERR_SEQLENS);
   AttnTile t;
-  if (!a.sq.get<false>(blockIdx.x, kM, t)) return;
+  if (!a.sq.get<false>(blockIdx.x / a.ranks, kM, t)) return;  // the whole cluster
   const int h = blockIdx.y, hk = h / (a.H / a.Hkv), tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int r0 = t.tile * kM, nr = min(kM, t.lq - r0), shift = t.lk - t.lq;
   const T* q = static_cast<const T*>(a.q) + t.b * a.qs[0] + (long long)(t.q0 + r0) * a.qs[1] + h * a.qs[2];
   const T* k = static_cast<const T*>(a.k) + t.b * a.ks[0] + (long long)t.k0 * a.ks[1] + hk * a.ks[2];
   const T* v = static_cast<const T*>(a.v) + t.b * a.vs[0] + (long long)t.k0 * a.vs[1] + hk * a.vs[2];
-  load_tile<T, DP>(Q, q, a.qs[1], nr, a.D);
+  load_tile<T, DP>(Q, q, a.qs[1], nr, a.D, a.vec);
   float acc[4][DP / 16], m[4], l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -195,10 +256,12 @@ __global__ void __launch_bounds__(kThreads) attn_simt_fwd_kernel(Args a) {
     for (int c = 0; c < DP / 16; ++c) acc[i][c] = 0.f;
   }
   const int nk = min(t.lk, r0 + nr + shift);  // keys that the tile's last row sees
-  for (int j0 = 0; j0 < nk; j0 += kM) {
+  const int steps = (max(0, nk) + kM - 1) / kM, end = steps * (rank + 1) / a.ranks;
+  for (int step = steps * rank / a.ranks; step < end; ++step) {
+    const int j0 = step * kM;
     __syncthreads();
-    load_tile<T, DP>(K, k + (long long)j0 * a.ks[1], a.ks[1], t.lk - j0, a.D);
-    load_tile<T, DP>(V, v + (long long)j0 * a.vs[1], a.vs[1], t.lk - j0, a.D);
+    load_tile<T, DP>(K, k + (long long)j0 * a.ks[1], a.ks[1], t.lk - j0, a.D, a.vec);
+    load_tile<T, DP>(V, v + (long long)j0 * a.vs[1], a.vs[1], t.lk - j0, a.D, a.vec);
     __syncthreads();
     float s[4][4];
     dots<DP>(s, Q, K, ty, tx);
@@ -228,6 +291,35 @@ __global__ void __launch_bounds__(kThreads) attn_simt_fwd_kernel(Args a) {
     }
     __syncwarp();  // a row of P is written and read by one warp
     rows_times<DP>(acc, P, V, ty, tx);
+  }
+  if (a.ranks > 1) {
+    // o = sum_x e^(m_x - m) acc_x / l,  l = sum_x e^(m_x - m) l_x over the ranks
+    const cg::cluster_group cluster = cg::this_cluster();
+    __syncthreads();
+    park<DP>(K, acc, ty, 16, tx);
+    if (tx == 0)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) V[ty + 16 * i] = m[i], V[kM + ty + 16 * i] = l[i];
+    cluster.sync();
+    const int rows = kM / a.ranks;
+    const long long tok = (long long)t.b * a.sq.Tq + t.q0 + r0;
+    for (int i = threadIdx.x; i < rows * DP; i += kThreads) {
+      const int r = rank * rows + i / DP, c = i % DP;
+      if (r >= nr || c >= a.D) continue;
+      float mx = -INFINITY, sum = 0.f, o = 0.f;
+      for (int x = 0; x < a.ranks; ++x) mx = fmaxf(mx, cluster.map_shared_rank(V, x)[r]);
+      const float base = mx == -INFINITY ? 0.f : mx;
+      for (int x = 0; x < a.ranks; ++x) {
+        const float* ml = cluster.map_shared_rank(V, x);
+        const float f = exp2f((ml[r] - base) * kLog2e);
+        sum = fmaf(f, ml[kM + r], sum);
+        o = fmaf(f, cluster.map_shared_rank(K, x)[r * (DP + 4) + c], o);
+      }
+      static_cast<T*>(a.o)[((tok + r) * a.H + h) * a.D + c] = from_f32<T>(sum == 0.f ? 0.f : o / sum);
+      if (c == 0) a.lse[((long long)t.b * a.H + h) * a.sq.Tq + t.q0 + r0 + r] = sum == 0.f ? -INFINITY : mx + logf(sum);
+    }
+    cluster.sync();  // the others still read this CTA's shared memory
+    return;
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -276,54 +368,65 @@ __device__ __forceinline__ void grads(float (&p)[4][4], float (&ds)[4][4], const
   }
 }
 
+// dk and dv of a key tile
 template <typename T, int DP>
-__global__ void __launch_bounds__(kThreads) attn_simt_bwd_kv_kernel(Args a) {
-  extern __shared__ float sm[];
+__device__ __forceinline__ void bwd_kv(const Args& a, float* sm, int slot, int hk, int rank) {
   constexpr int n = tile_floats<DP>();
   float *K = sm, *V = K + n, *Q = V + n, *dO = Q + n, *P = dO + n, *S = P + kM * kLdP;
   float *lse = S + kM * kLdP, *delta = lse + kM;
-  if (blockIdx.x == 0 && blockIdx.y == 0 && !a.sq.valid() && threadIdx.x == 0)
-    atomicExch(&tc::g_file_status, GDN_ERR_SEQLENS);
   AttnTile t;
-  if (!a.sq.get<true>(blockIdx.x, kM, t)) return;
-  const int G = a.H / a.Hkv, hk = blockIdx.y, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  if (!a.sq.get<true>(slot, kM, t)) return;  // the whole cluster
+  const int G = a.H / a.Hkv, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int j0 = t.tile * kM, shift = t.lk - t.lq;
   load_tile<T, DP>(K, static_cast<const T*>(a.k) + t.b * a.ks[0] + (long long)(t.k0 + j0) * a.ks[1] + hk * a.ks[2],
-                   a.ks[1], t.lk - j0, a.D);
+                   a.ks[1], t.lk - j0, a.D, a.vec);
   load_tile<T, DP>(V, static_cast<const T*>(a.v) + t.b * a.vs[0] + (long long)(t.k0 + j0) * a.vs[1] + hk * a.vs[2],
-                   a.vs[1], t.lk - j0, a.D);
+                   a.vs[1], t.lk - j0, a.D, a.vec);
   float dk[4][DP / 16], dv[4][DP / 16];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int c = 0; c < DP / 16; ++c) dk[i][c] = dv[i][c] = 0.f;
-  const int first = max(0, j0 - shift);  // the first query that sees the tile
-  for (int h = hk * G; h < (hk + 1) * G; ++h) {
+  // the query tiles that see the tile, of each of the G heads
+  const int first = max(0, j0 - shift) / kM, per = max(0, (t.lq + kM - 1) / kM - first);
+  const int x0 = (int)((long long)G * per * rank / a.ranks), x1 = (int)((long long)G * per * (rank + 1) / a.ranks);
+  int h = hk * G + (per ? x0 / per : 0), tile = first + (per ? x0 % per : 0);
+  for (int x = x0; x < x1; ++x) {
     const long long st = ((long long)t.b * a.H + h) * a.sq.Tq + t.q0;
-    for (int r0 = first / kM * kM; r0 < t.lq; r0 += kM) {
-      const int nr = min(kM, t.lq - r0);
-      __syncthreads();
-      load_tile<T, DP>(Q, static_cast<const T*>(a.q) + t.b * a.qs[0] + (long long)(t.q0 + r0) * a.qs[1] + h * a.qs[2],
-                       a.qs[1], nr, a.D);
-      load_tile<T, DP>(dO, static_cast<const T*>(a.do_) + (((long long)t.b * a.sq.Tq + t.q0 + r0) * a.H + h) * a.D,
-                       (long long)a.H * a.D, nr, a.D);
-      if (threadIdx.x < nr) lse[threadIdx.x] = a.lse[st + r0 + threadIdx.x];
-      else if (threadIdx.x < kM) lse[threadIdx.x] = 0.f;
-      if (threadIdx.x < nr) delta[threadIdx.x] = a.delta[st + r0 + threadIdx.x];
-      __syncthreads();
-      float p[4][4], ds[4][4];
-      grads<DP>(p, ds, Q, K, dO, V, lse, delta, r0, nr, j0, shift, t.lk, a.scale, ty, tx);
+    const int r0 = tile * kM, nr = min(kM, t.lq - r0);
+    __syncthreads();
+    load_tile<T, DP>(Q, static_cast<const T*>(a.q) + t.b * a.qs[0] + (long long)(t.q0 + r0) * a.qs[1] + h * a.qs[2],
+                     a.qs[1], nr, a.D, a.vec);
+    load_tile<T, DP>(dO, static_cast<const T*>(a.do_) + (((long long)t.b * a.sq.Tq + t.q0 + r0) * a.H + h) * a.D,
+                     (long long)a.H * a.D, nr, a.D, a.vec);
+    if (threadIdx.x < nr) lse[threadIdx.x] = a.lse[st + r0 + threadIdx.x];
+    else if (threadIdx.x < kM) lse[threadIdx.x] = 0.f;
+    if (threadIdx.x < nr) delta[threadIdx.x] = a.delta[st + r0 + threadIdx.x];
+    __syncthreads();
+    float p[4][4], ds[4][4];
+    grads<DP>(p, ds, Q, K, dO, V, lse, delta, r0, nr, j0, shift, t.lk, a.scale, ty, tx);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          P[(ty + 16 * i) * kLdP + tx + 16 * j] = p[i][j];
-          S[(ty + 16 * i) * kLdP + tx + 16 * j] = ds[i][j];
-        }
-      __syncthreads();
-      cols_times<DP>(dv, P, dO, ty, tx);
-      cols_times<DP>(dk, S, Q, ty, tx);
-    }
+      for (int j = 0; j < 4; ++j) {
+        P[(ty + 16 * i) * kLdP + tx + 16 * j] = p[i][j];
+        S[(ty + 16 * i) * kLdP + tx + 16 * j] = ds[i][j];
+      }
+    __syncthreads();
+    cols_times<DP>(dv, P, dO, ty, tx);
+    cols_times<DP>(dk, S, Q, ty, tx);
+    if (++tile == first + per) ++h, tile = first;
+  }
+  if (a.ranks > 1) {
+    __syncthreads();
+    park<DP>(Q, dk, 4 * ty, 1, tx);
+    park<DP>(dO, dv, 4 * ty, 1, tx);
+    cg::this_cluster().sync();
+    const long long at = (((long long)t.b * a.sq.Tk + t.k0 + j0) * a.Hkv + hk) * a.D;
+    join_rows<T, DP>(static_cast<T*>(a.dk) + at, (long long)a.Hkv * a.D, Q, a.scale, t.lk - j0, a.D, rank, a.ranks);
+    join_rows<T, DP>(static_cast<T*>(a.dv) + at, (long long)a.Hkv * a.D, dO, 1.f, t.lk - j0, a.D, rank, a.ranks);
+    cg::this_cluster().sync();  // the others still read this CTA's shared memory
+    return;
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -335,21 +438,21 @@ __global__ void __launch_bounds__(kThreads) attn_simt_bwd_kv_kernel(Args a) {
   }
 }
 
+// dq of a query tile
 template <typename T, int DP>
-__global__ void __launch_bounds__(kThreads) attn_simt_bwd_q_kernel(Args a) {
-  extern __shared__ float sm[];
+__device__ __forceinline__ void bwd_q(const Args& a, float* sm, int slot, int h, int rank) {
   constexpr int n = tile_floats<DP>();
   float *K = sm, *V = K + n, *Q = V + n, *dO = Q + n, *S = dO + n;
   float *lse = S + kM * kLdP, *delta = lse + kM;
   AttnTile t;
-  if (!a.sq.get<false>(blockIdx.x, kM, t)) return;
-  const int h = blockIdx.y, hk = h / (a.H / a.Hkv), tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  if (!a.sq.get<false>(slot, kM, t)) return;  // the whole cluster
+  const int hk = h / (a.H / a.Hkv), tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int r0 = t.tile * kM, nr = min(kM, t.lq - r0), shift = t.lk - t.lq;
   const long long st = ((long long)t.b * a.H + h) * a.sq.Tq + t.q0 + r0;
   const long long tok = (long long)t.b * a.sq.Tq + t.q0 + r0;
   load_tile<T, DP>(Q, static_cast<const T*>(a.q) + t.b * a.qs[0] + (long long)(t.q0 + r0) * a.qs[1] + h * a.qs[2],
-                   a.qs[1], nr, a.D);
-  load_tile<T, DP>(dO, static_cast<const T*>(a.do_) + (tok * a.H + h) * a.D, (long long)a.H * a.D, nr, a.D);
+                   a.qs[1], nr, a.D, a.vec);
+  load_tile<T, DP>(dO, static_cast<const T*>(a.do_) + (tok * a.H + h) * a.D, (long long)a.H * a.D, nr, a.D, a.vec);
   if (threadIdx.x < nr) lse[threadIdx.x] = a.lse[st + threadIdx.x], delta[threadIdx.x] = a.delta[st + threadIdx.x];
   else if (threadIdx.x < kM) lse[threadIdx.x] = 0.f, delta[threadIdx.x] = 0.f;
   float dq[4][DP / 16];
@@ -358,12 +461,14 @@ __global__ void __launch_bounds__(kThreads) attn_simt_bwd_q_kernel(Args a) {
 #pragma unroll
     for (int c = 0; c < DP / 16; ++c) dq[i][c] = 0.f;
   const int nk = min(t.lk, r0 + nr + shift);
-  for (int j0 = 0; j0 < nk; j0 += kM) {
+  const int steps = (max(0, nk) + kM - 1) / kM, end = steps * (rank + 1) / a.ranks;
+  for (int step = steps * rank / a.ranks; step < end; ++step) {
+    const int j0 = step * kM;
     __syncthreads();
     load_tile<T, DP>(K, static_cast<const T*>(a.k) + t.b * a.ks[0] + (long long)(t.k0 + j0) * a.ks[1] + hk * a.ks[2],
-                     a.ks[1], t.lk - j0, a.D);
+                     a.ks[1], t.lk - j0, a.D, a.vec);
     load_tile<T, DP>(V, static_cast<const T*>(a.v) + t.b * a.vs[0] + (long long)(t.k0 + j0) * a.vs[1] + hk * a.vs[2],
-                     a.vs[1], t.lk - j0, a.D);
+                     a.vs[1], t.lk - j0, a.D, a.vec);
     __syncthreads();
     float p[4][4], ds[4][4];
     grads<DP>(p, ds, Q, K, dO, V, lse, delta, r0, nr, j0, shift, t.lk, a.scale, ty, tx);
@@ -374,10 +479,32 @@ __global__ void __launch_bounds__(kThreads) attn_simt_bwd_q_kernel(Args a) {
     __syncwarp();
     rows_times<DP>(dq, S, K, ty, tx);
   }
+  if (a.ranks > 1) {
+    __syncthreads();
+    park<DP>(V, dq, ty, 16, tx);
+    cg::this_cluster().sync();
+    join_rows<T, DP>(static_cast<T*>(a.dq) + (tok * a.H + h) * a.D, (long long)a.H * a.D, V, a.scale, nr, a.D, rank,
+                     a.ranks);
+    cg::this_cluster().sync();  // the others still read this CTA's shared memory
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = ty + 16 * i;
     if (r < nr) store_row<T, DP>(static_cast<T*>(a.dq) + ((tok + r) * a.H + h) * a.D, dq[i], a.scale, tx, a.D);
+  }
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreads) attn_simt_bwd_kernel(Args a, int key_slots, int query_slots) {
+  extern __shared__ __align__(16) float sm[];
+  const int slot = blockIdx.x / a.ranks, rank = blockIdx.x % a.ranks;
+  if (blockIdx.x + blockIdx.y + blockIdx.z == 0 && !a.sq.valid() && threadIdx.x == 0)
+    atomicExch(&tc::g_file_status, GDN_ERR_SEQLENS);
+  if (blockIdx.z == 0) {  // the role with more work first
+    if (slot < key_slots && blockIdx.y < a.Hkv) bwd_kv<T, DP>(a, sm, slot, blockIdx.y, rank);
+  } else if (slot < query_slots) {
+    bwd_q<T, DP>(a, sm, slot, blockIdx.y, rank);
   }
 }
 
@@ -399,39 +526,65 @@ cudaError_t attn_delta(const AttnProblem& p, cudaStream_t s) {
   return e;
 }
 
-template <typename K>
-cudaError_t launch(K kernel, dim3 grid, int smem, const Args& a, cudaStream_t s, int id) {
+template <typename K, typename... A>
+cudaError_t launch(K kernel, dim3 grid, int smem, cudaStream_t s, int id, const Args& a, A... more) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = a.ranks, attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid, cfg.blockDim = dim3(kThreads), cfg.dynamicSmemBytes = smem, cfg.stream = s;
+  cfg.attrs = &attr, cfg.numAttrs = 1;
   prof_before(s);
-  kernel<<<grid, kThreads, smem, s>>>(a);
-  e = cudaGetLastError();
+  e = cudaLaunchKernelEx(&cfg, kernel, a, more...);
   prof_after(s, id);
   return e;
+}
+
+// CTAs that share a job: as many as it takes for the longest walk (in tiles) not
+// to outlast an even share of all the walks, `work`, over the CTAs that fit (two
+// on an SM for D <= 64, one above); no more than there are tiles, plus one.
+// Measured (fp32, us with 1, 2, 4, 8 CTAs, * the choice).  Forward: 2 x 333 tokens,
+// 4 heads, D 64: 42, 30, 31*, 36; 1200 tokens, 4 heads: 114, 72, 57*, 61; 4 x 300,
+// 16 heads: 52*, 72, 86, 131.  Backward: 2 x 333, 4 heads on 2: 133, 90, 51, 53*;
+// 1200, 16 on 4: 874, 491, 371*, 424; 2048, 8 on 2, D 128: 2002, 1016, 967*, 1245.
+int ranks_of(const AttnProblem& p, float longest, float work) {
+  const float even = work / (float)(tc::sm_count() * (p.D <= 64 ? 2 : 1));
+  int ranks = 1;
+  while (ranks < 8 && longest / ranks > even && 2 * ranks <= longest + 1) ranks *= 2;
+  return ranks;
+}
+
+// the mean sequence's tiles
+float mean_tiles(const AttnProblem& p, int T) {
+  return std::max(1.f, ceilf((float)T / (p.cu_q ? std::max(1, p.nseq) : 1) / kM));
 }
 
 template <typename T, int DP>
 cudaError_t fwd(const AttnProblem& p, cudaStream_t s) {
   const int smem = (3 * tile_floats<DP>() + kM * kLdP) * 4;
-  const dim3 grid((unsigned)AttnSeqs::slots(p, kM, false), p.H);
-  return launch(attn_simt_fwd_kernel<T, DP>, grid, smem, args_of(p), s, kAttnFwd);
+  const long slots = AttnSeqs::slots(p, kM, false);
+  Args a = args_of(p);
+  // half of the tiles are seen on average; a join costs about as much as a step, so
+  // only walks of twice the even share are cut
+  const float tiles = mean_tiles(p, p.Tk);
+  a.ranks = ranks_of(p, tiles, (float)slots * p.H * tiles);
+  return launch(attn_simt_fwd_kernel<T, DP>, dim3((unsigned)(slots * a.ranks), p.H), smem, s, kAttnFwd, a);
 }
 
 template <typename T, int DP>
 cudaError_t bwd(const AttnProblem& p, cudaStream_t s) {
-  cudaError_t e = attn_delta(p, s);
-  const Args a = args_of(p);
-  if (e == cudaSuccess && p.Tk > 0) {
-    const int smem = (4 * tile_floats<DP>() + 2 * kM * kLdP + 2 * kM) * 4;
-    const dim3 grid((unsigned)AttnSeqs::slots(p, kM, true), p.Hkv);
-    e = launch(attn_simt_bwd_kv_kernel<T, DP>, grid, smem, a, s, kAttnBwdKv);
-  }
-  if (e == cudaSuccess && p.Tq > 0) {
-    const int smem = (4 * tile_floats<DP>() + kM * kLdP + 2 * kM) * 4;
-    const dim3 grid((unsigned)AttnSeqs::slots(p, kM, false), p.H);
-    e = launch(attn_simt_bwd_q_kernel<T, DP>, grid, smem, a, s, kAttnBwdQ);
-  }
-  return e;
+  const cudaError_t e = attn_delta(p, s);
+  const long keys = p.Tk > 0 ? AttnSeqs::slots(p, kM, true) : 0, queries = p.Tq > 0 ? AttnSeqs::slots(p, kM, false) : 0;
+  if (e != cudaSuccess || std::max(keys, queries) == 0) return e;
+  Args a = args_of(p);
+  // a key tile's walk is over the queries of all heads that share the key head
+  const float tk = mean_tiles(p, p.Tk), tq = mean_tiles(p, p.Tq) * p.H / p.Hkv;
+  a.ranks = ranks_of(p, std::max(tk, tq), ((float)keys * p.Hkv * tq + (float)queries * p.H * tk) / 2);
+  const int smem = (4 * tile_floats<DP>() + 2 * kM * kLdP + 2 * kM) * 4;
+  return launch(attn_simt_bwd_kernel<T, DP>, dim3((unsigned)(std::max(keys, queries) * a.ranks), p.H, 2), smem, s,
+                kAttnBwd, a, (int)keys, (int)queries);
 }
 
 }  // namespace

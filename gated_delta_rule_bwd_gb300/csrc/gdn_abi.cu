@@ -223,7 +223,7 @@ const char* kernel_name(int id) {
       "kda_tc_prep", "kda_tc_fwd", "kda_tc_states", "kda_tc_bwd", "seqlens_setup",
       "short_conv_fwd", "short_conv_bwd", "gated_rmsnorm_fwd", "gated_rmsnorm_bwd", "sum_partials",
       "attn_fwd", "attn_delta", "attn_bwd_kv", "attn_bwd_q", "attn_decode", "attn_combine",
-      "layer_norm_fwd", "layer_norm_bwd", "layer_norm_sum"};
+      "layer_norm_fwd", "layer_norm_bwd", "layer_norm_sum", "attn_bwd"};
   return (id >= 0 && id < kNumKernelIds) ? names[id] : "unknown";
 }
 

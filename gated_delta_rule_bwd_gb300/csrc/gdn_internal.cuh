@@ -297,7 +297,8 @@ enum KernelId {
   kLnFwd = 27,
   kLnBwd = 28,
   kLnSum = 29,
-  kNumKernelIds = 30
+  kAttnBwd = 30,
+  kNumKernelIds = 31
 };
 const char* kernel_name(int id);
 

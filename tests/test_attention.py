@@ -159,6 +159,15 @@ def test_few_queries_and_many_keys(lq, lk, H, Hkv, D):
 
 
 @gpu
+@pytest.mark.parametrize("dtype,D", [(F32, 64), (F32, 72), (BF16, 65)], ids=["f32", "f32-72", "bf16-65"])
+def test_more_jobs_than_fit(dtype, D):
+    """CUDA-core kernels with whole jobs to a CTA (shorter calls share them)."""
+    q, k, v, do = inputs(6, 200, 200, 16, 16, D, dtype)
+    ref, bound = reference(q, k, v, do, [200], [200], D ** -0.5, dtype == BF16)
+    check(run(q, k, v, do), ref, bound)
+
+
+@gpu
 def test_workspace_of_parts():
     """A workspace that is too small or missing is refused before a launch."""
     q, k, v, _ = inputs(1, 64, 4096, 2, 2, 128, BF16)
