@@ -30,9 +30,9 @@
 // are a single tile the kernel takes that sum, in fp32, instead of do . o with
 // o's bf16 rounding: with few keys dP and delta nearly cancel.
 //
-// Measured, 16 rows of 2048 tokens, 8 heads, D 128: q 239 us, kv 246 us, which is
-// 863 and 1118 TFLOP/s of their three and four products over the pairs seen; the
-// tensor pipe is active 39 and 51 % of the time.  What bounds both is the chain
+// Measured, 16 rows of 2048 tokens, 8 heads, D 128: q 202 us, kv 223 us, which is
+// 1021 and 1233 TFLOP/s of their three and four products over the pairs seen; the
+// tensor pipe is active about half of the time.  What bounds both is the chain
 // of an iteration (scores, exponentials, P and dS into TMEM, products) and the
 // turn of a job, some 11000 cycles for 8.5 iterations on average here.
 
@@ -69,6 +69,7 @@ struct Cfg {
 struct Args {
   AttnSeqs sq;
   int H, Hkv, D, tiles;  // tiles: 128-row tiles per batch row (0: packed)
+  int group;             // see batch_group
   float c, scale;
   const float* lse;
   float* delta;
@@ -336,7 +337,7 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             // the tiles that the most queries see first
             const int u = cta / a.Hkv;
             AttnTile t;
-            if (!a.sq.get<true>(a.tiles ? u % a.sq.B * a.tiles + u / a.sq.B : u, 128, t)) return false;
+            if (!a.sq.get<true>(a.tiles ? batch_slot(u, a.sq.B, a.tiles, a.group, false) : u, 128, t)) return false;
             const int j0 = t.tile * 128;
             j[kHead] = cta % a.Hkv, j[kB] = t.b, j[kQ0] = t.q0, j[kLq] = t.lq, j[kK0] = t.k0 + j0;
             j[kNk] = min(128, t.lk - j0), j[kJs] = j0 - (t.lk - t.lq);
@@ -644,7 +645,7 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           [&](int cta, int(&j)[12]) {
             // the tiles with the most keys first
             const int u = cta / a.H;
-            const int slot = a.tiles ? u % a.sq.B * a.tiles + a.tiles - 1 - u / a.sq.B : ctas / a.H - 1 - u;
+            const int slot = a.tiles ? batch_slot(u, a.sq.B, a.tiles, a.group, true) : ctas / a.H - 1 - u;
             AttnTile t;
             if (!a.sq.get<false>(slot, 128, t)) return false;
             const int r0 = t.tile * 128, nr = min(128, t.lq - r0);
@@ -818,6 +819,7 @@ cudaError_t run(const AttnProblem& p, cudaStream_t s) {
   a.dq = static_cast<__nv_bfloat16*>(p.dq);
   a.dk = static_cast<__nv_bfloat16*>(p.dk), a.dv = static_cast<__nv_bfloat16*>(p.dv);
   a.tiles = p.cu_q ? 0 : (p.Tq + 127) / 128;
+  a.group = batch_group(p.B, 4.0 * p.Tk * p.Hkv * p.D, (long)a.tiles * p.H);  // K and V
   prof_before(s);
   attn_tc_bwd_q_kernel<DP>
       <<<(unsigned)(AttnSeqs::slots(p, 128, false) * p.H), kThreads, C::kSmem, s>>>(mq, mk, mv, md, a);
@@ -825,6 +827,7 @@ cudaError_t run(const AttnProblem& p, cudaStream_t s) {
   prof_after(s, kAttnBwdQ);
   if (e != cudaSuccess) return e;
   a.tiles = p.cu_q ? 0 : (p.Tk + 127) / 128;
+  a.group = batch_group(p.B, 4.0 * p.Tq * p.H * p.D, (long)a.tiles * p.Hkv);  // Q and dO
   prof_before(s);
   attn_tc_bwd_kv_kernel<DP>
       <<<(unsigned)(AttnSeqs::slots(p, 128, true) * p.Hkv), kThreads, C::kSmem, s>>>(mq, mk, mv, md, a);

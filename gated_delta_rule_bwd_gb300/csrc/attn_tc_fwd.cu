@@ -28,7 +28,7 @@
 // other tile's products.  Code that runs once per job is kept rolled: its
 // instructions come from beyond the instruction cache, at some 2 cycles a byte.
 // Measured, D 128: one row of 16384 tokens, 16 heads on 2: 750 us, 1466 TFLOP/s of
-// the pairs seen; 16 rows of 2048 tokens, 8 heads: 139 us, 989 TFLOP/s, the tensor
+// the pairs seen; 16 rows of 2048 tokens, 8 heads: 138 us, 996 TFLOP/s, the tensor
 // pipe active 47 % of the time (tiles on the diagonal and the turn of the jobs).
 
 #include <math.h>
@@ -66,6 +66,7 @@ struct Cfg {
 struct Args {
   AttnSeqs sq;
   int H, G, D, tiles;  // tiles: 256-row tiles per batch row (0: packed)
+  int group;           // see batch_group
   int parts;           // of a job's keys
   float c, scale;
   __nv_bfloat16* o;
@@ -82,7 +83,7 @@ enum { kHead, kPart, kQ0, kK0, kLk, kFirst, kNr, kB, kN0, kN1, kFix, kValid };
 __device__ __forceinline__ bool decode(const Args& a, int cta, int ctas, int (&j)[12]) {
   // the tiles with the most keys first
   const int part = cta % a.parts, u = cta / a.parts / a.H;
-  const int slot = a.tiles ? u % a.sq.B * a.tiles + a.tiles - 1 - u / a.sq.B : ctas / a.parts / a.H - 1 - u;
+  const int slot = a.tiles ? batch_slot(u, a.sq.B, a.tiles, a.group, true) : ctas / a.parts / a.H - 1 - u;
   AttnTile t;
   j[kValid] = a.sq.get<false>(slot, 256, t);
   if (!j[kValid]) return false;
@@ -531,6 +532,7 @@ cudaError_t run(const AttnProblem& p, cudaStream_t s) {
   a.tiles = p.cu_q ? 0 : (p.Tq + 255) / 256;
   a.scale = p.scale, a.c = p.scale * kLog2e;
   a.o = static_cast<__nv_bfloat16*>(p.o), a.lse = p.lse;
+  a.group = batch_group(p.B, 4.0 * p.Tk * p.Hkv * p.D, (long)a.tiles * p.H);  // K and V
   a.parts = parts_of(p);
   a.po = nullptr;
   if (a.parts > 1) {

@@ -168,6 +168,14 @@ def test_more_jobs_than_fit(dtype, D):
 
 
 @gpu
+def test_batch_rows_in_groups():
+    """Batches of many rows go out in groups of rows, the last one smaller."""
+    q, k, v, do = inputs(19, 300, 300, 16, 16, 64, BF16)
+    ref, bound = reference(q, k, v, do, [300], [300], 64 ** -0.5, True)
+    check(run(q, k, v, do), ref, bound)
+
+
+@gpu
 def test_workspace_of_parts():
     """A workspace that is too small or missing is refused before a launch."""
     q, k, v, _ = inputs(1, 64, 4096, 2, 2, 128, BF16)
