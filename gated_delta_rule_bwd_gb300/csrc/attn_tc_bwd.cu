@@ -118,8 +118,9 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
   TileSlots* slots = reinterpret_cast<TileSlots*>(sm + C::kBar);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(slots + 1);
   uint64_t* v_full = k_full + 1;
-  uint64_t* kv_empty = v_full + 1;
-  uint64_t* q_full = kv_empty + 1;    // [3]
+  uint64_t* k_empty = v_full + 1;
+  uint64_t* v_empty = k_empty + 1;
+  uint64_t* q_full = v_empty + 1;     // [3]
   uint64_t* q_empty = q_full + 3;     // [3]
   uint64_t* do_full = q_empty + 3;    // [2]
   uint64_t* do_empty = do_full + 2;   // [2]
@@ -143,7 +144,7 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
   if (threadIdx.x == kCompute) {
     *dead = 0;
     slots->init(19);
-    for (uint64_t* x : {k_full, v_full, kv_empty, s_full, dp_full, acc_full, landed, fixed, drain}) mbar_init(x, 1);
+    for (uint64_t* x : {k_full, v_full, k_empty, v_empty, s_full, dp_full, acc_full, landed, fixed, drain}) mbar_init(x, 1);
     for (int i = 0; i < 3; ++i) {
       mbar_init(q_full + i, 1);
       mbar_init(q_empty + i, 1);
@@ -181,8 +182,7 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         for (int h = hk * G, first = 1; h < (hk + 1) * G && ok; ++h)
           for (int i = 0; i < ni; ++i, first = 0) {
             if (first) {
-              if (!(ok = wait_live(kv_empty, kph ^ 1, dead))) break;
-              kph ^= 1;
+              if (!(ok = wait_live(k_empty, kph ^ 1, dead))) break;
               mbar_arrive_expect_tx(k_full, C::kTile);
               load_tile<C::NH>(sm, &tm_k, k_full, hk, k0, b);
             }
@@ -191,6 +191,8 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             load_tile<C::NH>(sm + (2 + rq.i) * C::kTile, &tm_q, q_full + rq.i, h, q0 + i * 128, b);
             rq.next();
             if (first) {
+              if (!(ok = wait_live(v_empty, kph ^ 1, dead))) break;
+              kph ^= 1;
               mbar_arrive_expect_tx(v_full, C::kTile);
               load_tile<C::NH>(sm + C::kTile, &tm_v, v_full, hk, k0, b);
             }
@@ -201,6 +203,7 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
           }
       }
       if (*dead) {  // nothing may still be written at exit (bounded)
+        mbar_wait(k_full, kph, 10000);  // of a load that has only just begun, if any
         mbar_wait(k_full, kph ^ 1, 10000);
         mbar_wait(v_full, kph ^ 1, 10000);
         drain_loads(q_full, rq);
@@ -216,14 +219,18 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       bool ok = true;
       auto have_q = [&] { return wait_live(q_full + rq.i, rq.ph, dead); };
       auto have_do = [&] { return wait_live(do_full + rd.i, rd.ph, dead); };
-      auto scores = [&] {
+      // K and V are free behind a job's last scores and dP^T: the next job's are
+      // loaded while this one ends
+      auto scores = [&](bool last) {
         mma_rows<DP>(tmem + kS, rows, desc_at(rows, (2 + rq.i) * C::kTile));
         mma_commit(s_full);
+        if (last) mma_commit(k_empty);
         rq.next();
       };
-      auto dprobs = [&] {
+      auto dprobs = [&](bool last) {
         mma_rows<DP>(tmem + kDP, desc_at(rows, C::kTile), desc_at(rows, (5 + rd.i) * C::kTile));
         mma_commit(dp_full);
+        if (last) mma_commit(v_empty);
         rd.next();
       };
       while (const int* j = ok ? next_job(slots, take, false, dead) : nullptr) {
@@ -235,9 +242,9 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
           continue;
         }
         if (!(ok = wait_live(k_full, kph, dead) && have_q())) break;
-        scores();
+        scores(N == 1);
         if (!(ok = wait_live(v_full, kph, dead) && have_do())) break;
-        dprobs();
+        dprobs(N == 1);
         kph ^= 1;
         if (!(ok = wait_live(acc_empty, aph ^ 1, dead))) break;  // the job before has read its sums
         aph ^= 1;
@@ -260,7 +267,7 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
           mma_commit(do_empty + rv.i);
           rv.next();
           if (it + 1 < N) {
-            scores();  // over P^T, behind the product that reads it
+            scores(it + 2 == N);  // over P^T, behind the product that reads it
             if (!(ok = have_do())) break;
           }
           if (!(ok = wait_live(ds_full, ph, dead))) break;
@@ -270,12 +277,11 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
           mma_commit(q_empty + rk.i);
           rk.next();
           if (it + 1 < N) {
-            dprobs();
+            dprobs(it + 2 == N);
             if (it + 2 < N) ok = have_q();
           }
         }
         mma_commit(acc_full);
-        mma_commit(kv_empty);
       }
       if (*dead) {
         mma_commit(drain);
@@ -478,8 +484,9 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   TileSlots* slots = reinterpret_cast<TileSlots*>(sm + C::kBar);
   uint64_t* q_full = reinterpret_cast<uint64_t*>(slots + 1);
   uint64_t* do_full = q_full + 1;
-  uint64_t* q_empty = do_full + 1;    // Q and dO
-  uint64_t* k_full = q_empty + 1;     // [3]
+  uint64_t* q_empty = do_full + 1;
+  uint64_t* do_empty = q_empty + 1;
+  uint64_t* k_full = do_empty + 1;    // [3]
   uint64_t* k_empty = k_full + 3;     // [3]
   uint64_t* v_full = k_empty + 3;     // [2]
   uint64_t* v_empty = v_full + 2;     // [2]
@@ -503,7 +510,7 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   if (threadIdx.x == kCompute) {
     *dead = 0;
     slots->init(18);
-    for (uint64_t* x : {q_full, do_full, q_empty, s_full, s_full + 1, dp_full, acc_full, landed, fixed, drain})
+    for (uint64_t* x : {q_full, do_full, q_empty, do_empty, s_full, s_full + 1, dp_full, acc_full, landed, fixed, drain})
       mbar_init(x, 1);
     for (int i = 0; i < 3; ++i) {
       mbar_init(k_full + i, 1);
@@ -539,7 +546,6 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         job_done(slots, take, false);
         if (!N) continue;
         if (!(ok = wait_live(q_empty, qph ^ 1, dead))) break;
-        qph ^= 1;
         mbar_arrive_expect_tx(q_full, C::kTile);
         load_tile<C::NH>(sm, &tm_q, q_full, h, q0, b);
         for (int x = 0; x < N; ++x) {
@@ -548,6 +554,8 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           load_tile<C::NH>(sm + (2 + rk.i) * C::kTile, &tm_k, k_full + rk.i, hk, k0 + x * 128, b);
           rk.next();
           if (x == 0) {
+            if (!(ok = wait_live(do_empty, qph ^ 1, dead))) break;
+            qph ^= 1;
             mbar_arrive_expect_tx(do_full, C::kTile);
             load_tile<C::NH>(sm + C::kTile, &tm_do, do_full, h, q0, b);
           }
@@ -558,6 +566,7 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         }
       }
       if (*dead) {  // nothing may still be written at exit (bounded)
+        mbar_wait(q_full, qph, 10000);  // of a load that has only just begun, if any
         mbar_wait(q_full, qph ^ 1, 10000);
         mbar_wait(do_full, qph ^ 1, 10000);
         drain_loads(k_full, rk);
@@ -579,15 +588,20 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         fph ^= 1;
         return got;
       };
-      auto scores = [&] {
+      // Q and dO are free behind a job's last scores and dP (the warps that make
+      // delta from dO have read the dP before, or N is 1 and none does): the next
+      // job's are loaded while this one ends
+      auto scores = [&](bool last) {
         mma_rows<DP>(tmem + kS + 128 * ss.i, rows, desc_at(rows, (2 + rk.i) * C::kTile));
         mma_commit(s_full + ss.i);
+        if (last) mma_commit(q_empty);
         rk.next();
         ss.next();
       };
-      auto dprobs = [&] {
+      auto dprobs = [&](bool last) {
         mma_rows<DP>(tmem + kDP, desc_at(rows, C::kTile), desc_at(rows, (5 + rv.i) * C::kTile));
         mma_commit(dp_full);
+        if (last) mma_commit(do_empty);
         mma_commit(v_empty + rv.i);
         rv.next();
       };
@@ -598,7 +612,7 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         if (N <= 3) mbar_arrive(&slots->soon);  // before the scheduler is asked to clean the last tile
         if (!N) continue;
         if (!(ok = wait_live(q_full, qph, dead) && have_k(fix && N == 1))) break;
-        scores();
+        scores(N == 1);
         // the dP before (of the last job, too) has been read
         if (!(ok = wait_live(do_full, qph, dead) && wait_live(v_full + rv.i, rv.ph, dead) &&
                    wait_live(dp_read, rph ^ 1, dead)))
@@ -606,7 +620,7 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         rph ^= 1;
         qph ^= 1;
         tc_fence_after();
-        dprobs();
+        dprobs(N == 1);
         if (!(ok = wait_live(acc_empty, aph ^ 1, dead))) break;
         aph ^= 1;
         ok = N == 1 || have_k(fix && N == 2);
@@ -614,11 +628,11 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         for (int x = 0; x < N && ok; ++x) {
           if (x > 0 && x == N - 3) mbar_arrive(&slots->soon);
           if (x + 1 < N) {
-            scores();  // over the dS of tile x - 1, behind the product that reads it
+            scores(x + 2 == N);  // over the dS of tile x - 1, behind the product that reads it
             if (!(ok = wait_live(v_full + rv.i, rv.ph, dead) && wait_live(dp_read, rph ^ 1, dead))) break;
             rph ^= 1;
             tc_fence_after();
-            dprobs();
+            dprobs(x + 2 == N);
             if (x + 2 < N && !(ok = have_k(fix && x + 3 == N))) break;
           }
           if (!(ok = wait_live(ds_full + sd.i, sd.ph, dead))) break;
@@ -629,7 +643,6 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           sd.next();
         }
         mma_commit(acc_full);
-        mma_commit(q_empty);
       }
       if (*dead) {
         mma_commit(drain);
@@ -698,7 +711,8 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           ov[x] = N > 1 && row < nr && c < a.D ? *reinterpret_cast<const uint4*>(a.o + (tok * a.H + j[kHead]) * a.D + c)
                                                : make_uint4(0, 0, 0, 0);
         }
-        if (!(ok = warp_wait_live(do_full, oph, dead))) break;
+        // (for N = 1, dO may be the next job's by now, and do_full a phase further)
+        if (N > 1 && !(ok = warp_wait_live(do_full, oph, dead))) break;
         oph ^= 1;
         if (N > 1) {  // delta = do . o: a thread takes DP / 4 values of its row
 #pragma unroll
