@@ -30,8 +30,8 @@
 // are a single tile the kernel takes that sum, in fp32, instead of do . o with
 // o's bf16 rounding: with few keys dP and delta nearly cancel.
 //
-// Measured, 16 rows of 2048 tokens, 8 heads, D 128: q 202 us, kv 223 us, which is
-// 1021 and 1233 TFLOP/s of their three and four products over the pairs seen; the
+// Measured, 16 rows of 2048 tokens, 8 heads, D 128: q 192 us, kv 221 us, which is
+// 1074 and 1244 TFLOP/s of their three and four products over the pairs seen; the
 // tensor pipe is active about half of the time.  What bounds both is the chain
 // of an iteration (scores, exponentials, P and dS into TMEM, products) and the
 // turn of a job, some 11000 cycles for 8.5 iterations on average here.
@@ -698,19 +698,30 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       pph ^= 1;
       return part[row] + part[128 + row] + part[256 + row] + part[384 + row];
     };
-    while (const int* j = ok ? next_job(slots, take, true, dead) : nullptr) {
+    float lse;
+    uint4 ov[DP / 32];
+    // a job's lse and its part of o: asked for before the last job's sums are written
+    auto fetch = [&](const int* j) {
+      const bool in = j && row < j[qNr];
+      lse = in ? a.lse[((long long)j[kB] * a.H + j[kHead]) * a.sq.Tq + j[qQ0] + row] : 0.f;
+#pragma unroll
+      for (int x = 0; x < DP / 32; ++x) {
+        const int c = g * (DP / 4) + 8 * x;
+        ov[x] = make_uint4(0, 0, 0, 0);
+        if (in && j[qN] > 1 && c < a.D) {
+          const long long tok = (long long)j[kB] * a.sq.Tq + j[qQ0] + row;
+          ov[x] = *reinterpret_cast<const uint4*>(a.o + (tok * a.H + j[kHead]) * a.D + c);
+        }
+      }
+    };
+    const int* j = next_job(slots, take, true, dead);
+    fetch(j);
+    while (j) {
       const int N = j[qN], nr = j[qNr];
       const long long tok = (long long)j[kB] * a.sq.Tq + j[qQ0] + row;
-      float lse = 0.f, delta = 0.f;
-      if (row < nr) lse = a.lse[((long long)j[kB] * a.H + j[kHead]) * a.sq.Tq + j[qQ0] + row] * kLog2e;
+      float delta = 0.f;
+      lse *= kLog2e;
       if (N) {
-        uint4 ov[DP / 32];
-#pragma unroll
-        for (int x = 0; x < DP / 32; ++x) {
-          const int c = g * (DP / 4) + 8 * x;
-          ov[x] = N > 1 && row < nr && c < a.D ? *reinterpret_cast<const uint4*>(a.o + (tok * a.H + j[kHead]) * a.D + c)
-                                               : make_uint4(0, 0, 0, 0);
-        }
         // (for N = 1, dO may be the next job's by now, and do_full a phase further)
         if (N > 1 && !(ok = warp_wait_live(do_full, oph, dead))) break;
         oph ^= 1;
@@ -790,6 +801,8 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       const long long stride = (long long)a.H * a.D;
       __nv_bfloat16* dst = a.dq + ((tok - row + w0) * a.H + j[kHead]) * a.D;
       job_done(slots, take, true);
+      j = next_job(slots, take, true, dead);
+      fetch(j);
       if (N) {
         if (!(ok = warp_wait_live(acc_full, aph, dead))) break;
         aph ^= 1;
