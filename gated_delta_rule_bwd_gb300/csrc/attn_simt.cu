@@ -224,12 +224,19 @@ __device__ __forceinline__ void join_rows(T* dst, long long stride, float* tile,
                                           int ranks) {
   const cg::cluster_group cluster = cg::this_cluster();
   const int rows = kM / ranks;
-  for (int i = threadIdx.x; i < rows * DP; i += kThreads) {
-    const int r = rank * rows + i / DP, c = i % DP;
+  for (int i = threadIdx.x; i < rows * DP / 4; i += kThreads) {
+    const int r = rank * rows + i / (DP / 4), c = i % (DP / 4) * 4;
     if (r >= n || c >= D) continue;
-    float sum = 0.f;
-    for (int x = 0; x < ranks; ++x) sum += cluster.map_shared_rank(tile, x)[r * (DP + 4) + c];
-    dst[r * stride + c] = from_f32<T>(sum * f);
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int x = 0; x < ranks; ++x) {
+      const float4 y = *reinterpret_cast<const float4*>(cluster.map_shared_rank(tile, x) + r * (DP + 4) + c);
+      sum.x += y.x, sum.y += y.y, sum.z += y.z, sum.w += y.w;
+    }
+    const float o[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (c + e < D) dst[r * stride + c + e] = from_f32<T>(o[e] * f);
   }
 }
 
@@ -303,19 +310,26 @@ __global__ void __launch_bounds__(kThreads) attn_simt_fwd_kernel(Args a) {
     cluster.sync();
     const int rows = kM / a.ranks;
     const long long tok = (long long)t.b * a.sq.Tq + t.q0 + r0;
-    for (int i = threadIdx.x; i < rows * DP; i += kThreads) {
-      const int r = rank * rows + i / DP, c = i % DP;
+    for (int i = threadIdx.x; i < rows * DP / 4; i += kThreads) {
+      const int r = rank * rows + i / (DP / 4), c = i % (DP / 4) * 4;
       if (r >= nr || c >= a.D) continue;
-      float mx = -INFINITY, sum = 0.f, o = 0.f;
+      float mx = -INFINITY, sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
       for (int x = 0; x < a.ranks; ++x) mx = fmaxf(mx, cluster.map_shared_rank(V, x)[r]);
       const float base = mx == -INFINITY ? 0.f : mx;
+#pragma unroll 4
       for (int x = 0; x < a.ranks; ++x) {
         const float* ml = cluster.map_shared_rank(V, x);
         const float f = exp2f((ml[r] - base) * kLog2e);
+        const float4 y = *reinterpret_cast<const float4*>(cluster.map_shared_rank(K, x) + r * (DP + 4) + c);
         sum = fmaf(f, ml[kM + r], sum);
-        o = fmaf(f, cluster.map_shared_rank(K, x)[r * (DP + 4) + c], o);
+        o[0] = fmaf(f, y.x, o[0]), o[1] = fmaf(f, y.y, o[1]);
+        o[2] = fmaf(f, y.z, o[2]), o[3] = fmaf(f, y.w, o[3]);
       }
-      static_cast<T*>(a.o)[((tok + r) * a.H + h) * a.D + c] = from_f32<T>(sum == 0.f ? 0.f : o / sum);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + e < a.D)
+          static_cast<T*>(a.o)[((tok + r) * a.H + h) * a.D + c + e] = from_f32<T>(sum == 0.f ? 0.f : o[e] / sum);
       if (c == 0) a.lse[((long long)t.b * a.H + h) * a.sq.Tq + t.q0 + r0 + r] = sum == 0.f ? -INFINITY : mx + logf(sum);
     }
     cluster.sync();  // the others still read this CTA's shared memory
