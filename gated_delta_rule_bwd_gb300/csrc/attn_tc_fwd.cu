@@ -467,7 +467,8 @@ __global__ void __launch_bounds__(256) attn_join_kernel(Args a, __nv_bfloat16* o
   float m = l;
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-  const float w = m == -INFINITY || l == -INFINITY ? 0.f : ex2((l - m) * kLog2e);
+  // 0 for a part without keys only: a NaN (which fmaxf passes over) stays in the sum
+  const float w = l == -INFINITY ? 0.f : ex2((l - (m == -INFINITY ? 0.f : m)) * kLog2e);
   float sum = w;
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);

@@ -400,10 +400,12 @@ GDN_API int gdn_gated_rmsnorm_bwd(const gdn_norm_shape* shape, const void* o, co
  * accumulators are fp32 everywhere.  The forward needs a workspace where few
  * queries stand against many keys (the keys are then split and joined).
  *
- * Non-finite values: a NaN or infinity in a token's k or v reaches the rows
- * that see it and may reach earlier rows of its own sequence in the same tile
- * of 128 tokens (0 times it is NaN); in q or do_ likewise the gradients of
- * that tile.  Other sequences of a packed call never see it.
+ * Non-finite values: a NaN in a row of q makes that row of o and lse NaN, one
+ * in a token's k the rows that see it.  A NaN or infinity in a token's k or v
+ * reaches the rows that see it, and one in v may reach earlier rows of its own
+ * sequence in the same tile of 128 tokens (0 times it is NaN); in q, k, v or
+ * do_ likewise the gradients of that tile.  Other sequences of a packed call
+ * never see it.
  *
  * Errors: GDN_ERR_ARG (NULL pointer, scale not a positive finite number, only
  * one of cu_q and cu_k given), GDN_ERR_SHAPE, GDN_ERR_DTYPE, GDN_ERR_ALIGN (o,
