@@ -516,8 +516,9 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_mma_kernel(Args a) {
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
-        const float mp = ml[(p * 16 * MB + rl) * 2];
-        sum += mp == -INFINITY ? 0.f : ex2(mp - top) * ml[(p * 16 * MB + rl) * 2 + 1];
+        // a piece without keys adds 0; one whose scores are all NaN has m = -inf too, and adds its l
+        const float mp = ml[(p * 16 * MB + rl) * 2], base = top == -INFINITY ? 0.f : top;
+        sum = fmaf(ex2(mp - base), ml[(p * 16 * MB + rl) * 2 + 1], sum);
         const float4 y = *reinterpret_cast<const float4*>(part + (p * 16 * MB + rl) * DP + c);
         x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
       }

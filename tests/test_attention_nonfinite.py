@@ -50,3 +50,24 @@ def test_nan_in_a_prompt(B, Tq, Tk, H, Hkv, D, dtype, split):
         same_but(rows, o, clean)
         same_but(rows, lse.transpose(1, 2), clean_lse.transpose(1, 2))
     assert gdn.device_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("B,T,S,n,H,Hkv,D", [
+    (1, 1, 9000, 8000, 2, 1, 128), (2, 3, 4000, 3500, 8, 1, 64), (1, 2, 30000, 29000, 32, 1, 128),  # split
+    (300, 1, 64, 40, 2, 1, 128), (1, 2, 100, 50, 4, 2, 64), (3, 4, 128, 70, 20, 2, 80)])            # whole
+def test_nan_in_decode(B, T, S, n, H, Hkv, D, dtype):
+    q, k, v = (randn(i, B, T, h, D, dtype=dtype) for i, h in enumerate((H, Hkv, Hkv)))
+    kc, vc = (randn(i, B, S, Hkv, D, dtype=dtype) for i in (3, 4))
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    clean = gdn.attn_decode(q, k, v, kc.clone(), vc.clone(), lens)
+    for what, at in (("q", T - 1), ("q", slice(None)), ("cache", 0), ("cache", n - 1), ("cache", slice(n)), ("k", T - 1)):
+        x = {"q": q.clone(), "cache": kc.clone(), "k": k.clone()}
+        x[what][:, at] = NAN
+        rows = torch.ones(T, dtype=torch.bool, device="cuda")
+        if what in ("q", "k"):
+            rows[:] = False
+            rows[at] = True
+        same_but(rows, gdn.attn_decode(x["q"], x["k"], v, x["cache"], vc.clone(), lens), clean)
+    assert gdn.device_status() == 0
