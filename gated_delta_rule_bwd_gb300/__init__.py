@@ -229,7 +229,16 @@ def _validate(q, k, v, g, beta, kda, extra=()):
             raise GdnError(f"{name} must be contiguous")
 
 
+def _on_current(device):
+    """Refuses tensors of a device that is not the current one: the library's kernels
+    run on the current device, whatever device a stream or a pointer belongs to."""
+    if device.index != torch.cuda.current_device():
+        raise GdnError(f"the tensors are on {device}, the current device is "
+                       f"cuda:{torch.cuda.current_device()}: call inside torch.cuda.device({device.index})")
+
+
 def _stream(dev):
+    _on_current(dev)
     return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
 
 
@@ -626,6 +635,7 @@ def _same(x, dtype, device, shape):
 
 
 def _raw_stream(device):
+    _on_current(device)
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
