@@ -79,7 +79,7 @@ EXPORTS = ("gdn_fwd", "gdn_bwd", "kda_fwd", "kda_bwd", "gdn_fwd_workspace", "kda
            "mamba2_fwd_workspace", "mamba2_bwd_workspace", "mamba2_ctx_bytes",
            "gdn_decode", "kda_decode",
            "gdn_status_str", "gdn_last_cuda_error", "gdn_device_status", "gdn_uses_tensor_cores",
-           "gdn_wait_selftest", "kda_uses_tensor_cores",
+           "gdn_wait_selftest", "gdn_attn_wait_selftest", "kda_uses_tensor_cores",
            "gdn_varlen_workspace", "kda_varlen_workspace", "mamba2_varlen_workspace",
            "gdn_fwd_varlen", "gdn_bwd_varlen", "kda_fwd_varlen", "kda_bwd_varlen",
            "mamba2_fwd_varlen", "mamba2_bwd_varlen",
@@ -133,8 +133,9 @@ def lib():
             for name in ("gdn_bwd_varlen", "kda_bwd_varlen", "mamba2_bwd_varlen"):
                 getattr(L, name).argtypes = [sp, vp, ctypes.c_int] + [vp] * 14 + [vp, sz, vp]
                 getattr(L, name).restype = ctypes.c_int
-            L.gdn_wait_selftest.argtypes = [ctypes.c_int, vp]
-            L.gdn_wait_selftest.restype = ctypes.c_int
+            for name in ("gdn_wait_selftest", "gdn_attn_wait_selftest"):
+                getattr(L, name).argtypes = [ctypes.c_int, vp]
+                getattr(L, name).restype = ctypes.c_int
             for name in ("gdn_uses_tensor_cores", "kda_uses_tensor_cores"):
                 getattr(L, name).argtypes = [sp]
                 getattr(L, name).restype = ctypes.c_int
@@ -877,6 +878,11 @@ def layer_norm(x, weight, bias=None, eps=NORM_EPS):
 def wait_selftest(max_tries=5):
     """Runs the device-side timeout path once (see gdn_wait_selftest in gdn.h)."""
     _check(lib().gdn_wait_selftest(max_tries, _stream(torch.device("cuda", torch.cuda.current_device()))))
+
+
+def attn_wait_selftest(clocks=1 << 22):
+    """The same for the attention kernels' waits (see gdn_attn_wait_selftest in gdn.h)."""
+    _check(lib().gdn_attn_wait_selftest(clocks, _stream(torch.device("cuda", torch.cuda.current_device()))))
 
 
 def device_status() -> int:

@@ -40,19 +40,48 @@ __device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Bounded wait that also gives up once another warp of the CTA has
-// (*dead != 0); running out (after a second or more: a poll is tens of cycles at
-// least) sets *dead.  Kept small: it stands at every hand-over, and what does not
-// fit the instruction cache is fetched again at every turn of a job.
-__device__ __forceinline__ bool wait_live(uint64_t* bar, uint32_t parity, volatile int* dead) {
+// What the roles of a CTA tell each other about a wait that runs out.
+struct Liveness {
+  int dead;         // a wait ran out: everyone gives up
+  int progress[2];  // counted up by the issuing thread per iteration and by the scheduler per CTA it asks for
+};
+
+// Bounded wait for a hand-over within an iteration or two, which take microseconds;
+// it also gives up once another warp of the CTA has (live->dead != 0), and running
+// out of polls sets that: after about a second, as a poll that nothing answers was
+// measured to last 7800 clocks (and after 2 ms even if one lasted 20).  Kept small: it
+// stands at every hand-over, and what does not fit the instruction cache is fetched
+// again at every turn of a job.
+__device__ __forceinline__ bool wait_live(uint64_t* bar, uint32_t parity, volatile Liveness* live) {
   if (try_wait(bar, parity)) return true;
 #pragma unroll 1
-  for (uint32_t i = 0; i < (1u << 25); ++i) {
+  for (uint32_t i = 0; i < (1u << 18); ++i) {
     if (try_wait(bar, parity)) return true;
-    if (*dead) return false;
+    if (live->dead) return false;
   }
-  *dead = 1;
+  live->dead = 1;
   return false;
+}
+
+// The same for a wait that may rightly last a whole job (the scheduler's; a warp's
+// without rows in a job).  A job has no longest time, so what runs out is `patience`
+// clocks of the SM (2^31: about a second) in which nothing has moved: all roles hang
+// on the issuing thread and, between jobs, on the scheduler.
+constexpr uint32_t kPatience = 1u << 31;
+__device__ __forceinline__ bool wait_job(uint64_t* bar, uint32_t parity, volatile Liveness* live,
+                                         uint32_t patience = kPatience) {
+  uint32_t since = clock();
+  int seen = live->progress[0] + live->progress[1];
+#pragma unroll 1
+  while (!try_wait(bar, parity)) {
+    if (live->dead) return false;
+    if ((uint32_t)clock() - since <= patience) continue;
+    const int now = live->progress[0] + live->progress[1];
+    if (now == seen) live->dead = 1;
+    seen = now;
+    since = clock();
+  }
+  return true;
 }
 
 // One lane of a converged warp.  A role that one lane plays is put behind it
@@ -69,10 +98,16 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// wait_live for a whole warp: one lane polls.
-__device__ __forceinline__ bool warp_wait_live(uint64_t* bar, uint32_t parity, volatile int* dead) {
+// The waits for a whole warp: one lane polls.
+__device__ __forceinline__ bool warp_wait_live(uint64_t* bar, uint32_t parity, volatile Liveness* live) {
   int ok = 1;
-  if ((threadIdx.x & 31) == 0) ok = wait_live(bar, parity, dead);
+  if ((threadIdx.x & 31) == 0) ok = wait_live(bar, parity, live);
+  return __shfl_sync(0xffffffffu, ok, 0);
+}
+__device__ __forceinline__ bool warp_wait_job(uint64_t* bar, uint32_t parity, volatile Liveness* live,
+                                              uint32_t patience = kPatience) {
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) ok = wait_job(bar, parity, live, patience);
   return __shfl_sync(0xffffffffu, ok, 0);
 }
 
@@ -124,8 +159,8 @@ struct __align__(16) TileSlots {
 
 // The next tile's job, for one lane (whole = false) or a whole warp; NULL: none.
 // It stays in place until the taker says done.
-__device__ __forceinline__ const int* next_job(TileSlots* ts, const Ring<2>& r, bool whole, volatile int* dead) {
-  const bool ok = whole ? warp_wait_live(ts->full + r.i, r.ph, dead) : wait_live(ts->full + r.i, r.ph, dead);
+__device__ __forceinline__ const int* next_job(TileSlots* ts, const Ring<2>& r, bool whole, volatile Liveness* live) {
+  const bool ok = whole ? warp_wait_job(ts->full + r.i, r.ph, live) : wait_job(ts->full + r.i, r.ph, live);
   const int* j = ts->job[r.i];
   return ok && j[11] ? j : nullptr;
 }
@@ -156,8 +191,8 @@ inline int batch_group(int B, double bytes, long jobs) {
 }
 
 // Scheduler warp: puts a job into the next slot.
-__device__ __forceinline__ bool put_job(TileSlots* ts, Ring<2>& r, const int (&j)[12], volatile int* dead) {
-  if (!warp_wait_live(ts->empty + r.i, r.ph ^ 1, dead)) return false;
+__device__ __forceinline__ bool put_job(TileSlots* ts, Ring<2>& r, const int (&j)[12], volatile Liveness* live) {
+  if (!warp_wait_live(ts->empty + r.i, r.ph ^ 1, live)) return false;
   if ((threadIdx.x & 31) == 0) {
 #pragma unroll
     for (int i = 0; i < 12; i += 4)
@@ -171,7 +206,7 @@ __device__ __forceinline__ bool put_job(TileSlots* ts, Ring<2>& r, const int (&j
 
 // Scheduler warp: takes over a CTA that has not started; its index in x, or
 // false if there is none left (after which this must not be called again).
-__device__ __forceinline__ bool next_cta(TileSlots* ts, uint32_t& ph, int& x, volatile int* dead) {
+__device__ __forceinline__ bool next_cta(TileSlots* ts, uint32_t& ph, int& x, volatile Liveness* live) {
   if ((threadIdx.x & 31) == 0) {
     mbar_arrive_expect_tx(&ts->response_full, 16);
     asm volatile(
@@ -181,7 +216,10 @@ __device__ __forceinline__ bool next_cta(TileSlots* ts, uint32_t& ph, int& x, vo
         : "memory");
   }
   __syncwarp();
-  if (!warp_wait_live(&ts->response_full, ph, dead)) return false;
+  if (!warp_wait_live(&ts->response_full, ph, live)) {
+    mbar_wait(&ts->response_full, ph, 10000);  // nothing may still be written at exit (bounded)
+    return false;
+  }
   ph ^= 1;
   uint32_t got, at = 0;
   asm volatile(
@@ -204,26 +242,28 @@ __device__ __forceinline__ bool next_cta(TileSlots* ts, uint32_t& ph, int& x, vo
 // warp, before and after the next job is put out (they read it from its slot,
 // which is rewritten only by the job after the next).
 template <class Decode, class Early, class Late>
-__device__ __forceinline__ void schedule(TileSlots* slots, volatile int* dead, Decode decode, Early early, Late late) {
+__device__ __forceinline__ void schedule(TileSlots* slots, volatile Liveness* live, Decode decode, Early early, Late late) {
   Ring<2> put;
   int cta = blockIdx.x, j[12];
   uint32_t ph = 0, soon_ph = 0;
   bool left = true, fresh = true;
+  int asked = 0;
   const volatile int* now = nullptr;
   for (;;) {
     if (now) {
-      if (!early(now) || !warp_wait_live(&slots->soon, soon_ph, dead)) break;
+      if (!early(now) || !warp_wait_job(&slots->soon, soon_ph, live)) break;
       soon_ph ^= 1;
     }
     bool more = false;
     while (left && !more) {  // the next CTA whose tile is not empty
-      if (!fresh) left = next_cta(slots, ph, cta, dead);
+      if (!fresh) left = next_cta(slots, ph, cta, live);
       fresh = false;
+      live->progress[1] = ++asked;  // thousands of empty packed sequences may lie in a row
       if (left) more = decode(cta, j);
     }
     j[11] = more;
     const volatile int* next = slots->job[put.i];
-    if (!put_job(slots, put, j, dead)) break;
+    if (!put_job(slots, put, j, live)) break;
     if (now && !late(now)) break;
     if (!more) break;
     now = next;

@@ -136,13 +136,13 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
   uint64_t* fixed = landed + 1;
   uint64_t* drain = fixed + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-  volatile int* dead = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile Liveness* live = reinterpret_cast<volatile Liveness*>(tmem_slot + 1);
   constexpr uint32_t kS = 0, kDP = 128, kAcc = 256;  // TMEM columns; dV, then dK
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.H / a.Hkv;
 
   if (!aligned_smem(sm)) return;
   if (threadIdx.x == kCompute) {
-    *dead = 0;
+    live->dead = live->progress[0] = live->progress[1] = 0;
     slots->init(19);
     for (uint64_t* x : {k_full, v_full, k_empty, v_empty, s_full, dp_full, acc_full, landed, fixed, drain}) mbar_init(x, 1);
     for (int i = 0; i < 3; ++i) {
@@ -176,33 +176,33 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       Ring<2> rd;
       uint32_t kph = 0;
       bool ok = true;
-      while (const int* j = ok ? next_job(slots, take, false, dead) : nullptr) {
+      while (const int* j = ok ? next_job(slots, take, false, live) : nullptr) {
         const int hk = j[kHead], b = j[kB], k0 = j[kK0], i0 = j[kI0], ni = j[kNi], q0 = j[kQ0] + i0 * 128;
         job_done(slots, take, false);
         for (int h = hk * G, first = 1; h < (hk + 1) * G && ok; ++h)
           for (int i = 0; i < ni; ++i, first = 0) {
             if (first) {
-              if (!(ok = wait_live(k_empty, kph ^ 1, dead))) break;
+              if (!(ok = wait_live(k_empty, kph ^ 1, live))) break;
               mbar_arrive_expect_tx(k_full, C::kTile);
               load_tile<C::NH>(sm, &tm_k, k_full, hk, k0, b);
             }
-            if (!(ok = wait_live(q_empty + rq.i, rq.ph ^ 1, dead))) break;
+            if (!(ok = wait_live(q_empty + rq.i, rq.ph ^ 1, live))) break;
             mbar_arrive_expect_tx(q_full + rq.i, C::kTile);
             load_tile<C::NH>(sm + (2 + rq.i) * C::kTile, &tm_q, q_full + rq.i, h, q0 + i * 128, b);
             rq.next();
             if (first) {
-              if (!(ok = wait_live(v_empty, kph ^ 1, dead))) break;
+              if (!(ok = wait_live(v_empty, kph ^ 1, live))) break;
               kph ^= 1;
               mbar_arrive_expect_tx(v_full, C::kTile);
               load_tile<C::NH>(sm + C::kTile, &tm_v, v_full, hk, k0, b);
             }
-            if (!(ok = wait_live(do_empty + rd.i, rd.ph ^ 1, dead))) break;
+            if (!(ok = wait_live(do_empty + rd.i, rd.ph ^ 1, live))) break;
             mbar_arrive_expect_tx(do_full + rd.i, C::kTile);
             load_tile<C::NH>(sm + (5 + rd.i) * C::kTile, &tm_do, do_full + rd.i, h, q0 + i * 128, b);
             rd.next();
           }
       }
-      if (*dead) {  // nothing may still be written at exit (bounded)
+      if (live->dead) {  // nothing may still be written at exit (bounded)
         mbar_wait(k_full, kph, 10000);  // of a load that has only just begun, if any
         mbar_wait(k_full, kph ^ 1, 10000);
         mbar_wait(v_full, kph ^ 1, 10000);
@@ -216,9 +216,10 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       Ring<3> rq, rk;   // Q for S^T (an iteration ahead) and for dK
       Ring<2> rd, rv;   // dO for dP^T (an iteration ahead) and for dV
       uint32_t kph = 0, ph = 0, fph = 0, aph = 0;
+      int turns = 0;
       bool ok = true;
-      auto have_q = [&] { return wait_live(q_full + rq.i, rq.ph, dead); };
-      auto have_do = [&] { return wait_live(do_full + rd.i, rd.ph, dead); };
+      auto have_q = [&] { return wait_live(q_full + rq.i, rq.ph, live); };
+      auto have_do = [&] { return wait_live(do_full + rd.i, rd.ph, live); };
       // K and V are free behind a job's last scores and dP^T: the next job's are
       // loaded while this one ends
       auto scores = [&](bool last) {
@@ -233,7 +234,7 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         if (last) mma_commit(v_empty);
         rd.next();
       };
-      while (const int* j = ok ? next_job(slots, take, false, dead) : nullptr) {
+      while (const int* j = ok ? next_job(slots, take, false, live) : nullptr) {
         const int ni = j[kNi], N = ni * G;
         const bool fix = packed && j[kLq] % 128;
         job_done(slots, take, false);
@@ -241,27 +242,28 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
           mbar_arrive(&slots->soon);
           continue;
         }
-        if (!(ok = wait_live(k_full, kph, dead) && have_q())) break;
+        if (!(ok = wait_live(k_full, kph, live) && have_q())) break;
         scores(N == 1);
-        if (!(ok = wait_live(v_full, kph, dead) && have_do())) break;
+        if (!(ok = wait_live(v_full, kph, live) && have_do())) break;
         dprobs(N == 1);
         kph ^= 1;
-        if (!(ok = wait_live(acc_empty, aph ^ 1, dead))) break;  // the job before has read its sums
+        if (!(ok = wait_live(acc_empty, aph ^ 1, live))) break;  // the job before has read its sums
         aph ^= 1;
         int left = ni;  // iterations of the head
         ok = N == 1 || have_q();
 #pragma unroll 1
         for (int it = 0; it < N && ok; ++it) {
+          live->progress[0] = ++turns;
           if (it == max(0, N - 3)) mbar_arrive(&slots->soon);
           if (--left == 0) {
             left = ni;
             if (fix) {
               mbar_arrive(landed);
-              if (!(ok = wait_live(fixed, fph, dead))) break;
+              if (!(ok = wait_live(fixed, fph, live))) break;
               fph ^= 1;
             }
           }
-          if (!(ok = wait_live(p_full, ph, dead))) break;
+          if (!(ok = wait_live(p_full, ph, live))) break;
           tc_fence_after();
           mma_sum<DP, 8, 2, 32>(tmem + kAcc, tmem + kS, desc_at(cols, (5 + rv.i) * C::kTile), it > 0);
           mma_commit(do_empty + rv.i);
@@ -270,7 +272,7 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             scores(it + 2 == N);  // over P^T, behind the product that reads it
             if (!(ok = have_do())) break;
           }
-          if (!(ok = wait_live(ds_full, ph, dead))) break;
+          if (!(ok = wait_live(ds_full, ph, live))) break;
           ph ^= 1;
           tc_fence_after();
           mma_sum<DP, 8, 2, 32>(tmem + kAcc + DP, tmem + kDP, desc_at(cols, (2 + rk.i) * C::kTile), it > 0);
@@ -283,7 +285,7 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         }
         mma_commit(acc_full);
       }
-      if (*dead) {
+      if (live->dead) {
         mma_commit(drain);
         mbar_wait(drain, 0, 10000);
       }
@@ -291,7 +293,7 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       // ------------------------------------------------------------ lse, delta
       Ring<2> rs;
       bool ok = true;
-      while (const int* j = ok ? next_job(slots, take, true, dead) : nullptr) {
+      while (const int* j = ok ? next_job(slots, take, true, live) : nullptr) {
         const int lq = j[kLq], i0 = j[kI0], ni = j[kNi];
         long long at = ((long long)j[kB] * a.H + j[kHead] * G) * a.sq.Tq + j[kQ0];
         job_done(slots, take, true);
@@ -308,7 +310,7 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         if (ni) fetch(i0);
         for (int g = 0; g < G && ok; ++g)
           for (int i = i0; i < i0 + ni; ++i) {
-            if (!(ok = warp_wait_live(st_empty + rs.i, rs.ph ^ 1, dead))) break;
+            if (!(ok = warp_wait_live(st_empty + rs.i, rs.ph ^ 1, live))) break;
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               stats[rs.i * 256 + lane + 32 * x] = ls[x];
@@ -328,7 +330,7 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       uint32_t ph = 0;
       auto clean = [&](const volatile int* j) {
         if (!packed || j[kLq] % 128 == 0 || !j[kNi]) return true;
-        if (!warp_wait_live(landed, ph, dead)) return false;
+        if (!warp_wait_job(landed, ph, live)) return false;
         ph ^= 1;
         const int x = it + ++head * j[kNi] - 1;
         zero_rows<C::NH>(sm + (2 + x % 3) * C::kTile, j[kLq] % 128, lane);
@@ -338,7 +340,7 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         return true;
       };
       schedule(
-          slots, dead,
+          slots, live,
           [&](int cta, int(&j)[12]) {
             // the tiles that the most queries see first
             const int u = cta / a.Hkv;
@@ -373,17 +375,17 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     Ring<2> rs;
     uint32_t ph = 0, aph = 0;
     bool ok = true;
-    while (const int* j = ok ? next_job(slots, take, true, dead) : nullptr) {
+    while (const int* j = ok ? next_job(slots, take, true, live) : nullptr) {
       const int ni = j[kNi], N = ni * G, lq = j[kLq], js = j[kJs];
       int r = j[kI0] * 128, left = ni;
 #pragma unroll 1
       for (int it = 0; it < N; ++it) {
         const float *lse = stats + rs.i * 256 + 32 * g, *delta = lse + 128;
-        if (!(ok = warp_wait_live(st_full + rs.i, rs.ph, dead))) break;
+        if (!(ok = warp_wait_live(st_full + rs.i, rs.ph, live))) break;
         float p[32], n[32];
 #pragma unroll
         for (int x = 0; x < 32; x += 4) *reinterpret_cast<float4*>(n + x) = *reinterpret_cast<const float4*>(lse + x);
-        if (!(ok = warp_wait_live(s_full, ph, dead))) break;
+        if (!(ok = warp_wait_live(s_full, ph, live))) break;
         tc_fence_after();
         tmem_ld32_start(ts, p);
         tmem_ld_wait();
@@ -410,7 +412,7 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
 
 #pragma unroll
         for (int x = 0; x < 32; x += 4) *reinterpret_cast<float4*>(n + x) = *reinterpret_cast<const float4*>(delta + x);
-        if (!(ok = warp_wait_live(dp_full, ph, dead))) break;
+        if (!(ok = warp_wait_live(dp_full, ph, live))) break;
         ph ^= 1;
         tc_fence_after();
         float d[32];
@@ -447,7 +449,7 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       __nv_bfloat16* dst = (which ? a.dk : a.dv) + (((long long)j[kB] * a.sq.Tk + j[kK0] + w0) * a.Hkv + j[kHead]) * a.D;
       job_done(slots, take, true);
       if (N) {
-        if (!(ok = warp_wait_live(acc_full, aph, dead))) break;
+        if (!(ok = warp_wait_live(acc_full, aph, live))) break;
         aph ^= 1;
         tc_fence_after();
         store_acc<DP / 2>(tmem + lanes + kAcc + DP * which + half, which ? a.scale : 1.f, dst, stride, rows, half, a.D);
@@ -462,7 +464,7 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (threadIdx.x == 0 && *dead) report_timeout();
+  if (threadIdx.x == 0 && live->dead) report_timeout();
   if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
@@ -501,14 +503,14 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   uint64_t* fixed = landed + 1;
   uint64_t* drain = fixed + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-  volatile int* dead = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile Liveness* live = reinterpret_cast<volatile Liveness*>(tmem_slot + 1);
   constexpr uint32_t kS = 0, kDP = 256, kDQ = 384;  // TMEM columns; S has two buffers
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.H / a.Hkv;
 
   if (!aligned_smem(sm)) return;
   if (blockIdx.x == 0 && !a.sq.valid() && threadIdx.x == 0) atomicExch(&g_file_status, GDN_ERR_SEQLENS);
   if (threadIdx.x == kCompute) {
-    *dead = 0;
+    live->dead = live->progress[0] = live->progress[1] = 0;
     slots->init(18);
     for (uint64_t* x : {q_full, do_full, q_empty, do_empty, s_full, s_full + 1, dp_full, acc_full, landed, fixed, drain})
       mbar_init(x, 1);
@@ -541,31 +543,31 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       Ring<2> rv;
       uint32_t qph = 0;
       bool ok = true;
-      while (const int* j = ok ? next_job(slots, take, false, dead) : nullptr) {
+      while (const int* j = ok ? next_job(slots, take, false, live) : nullptr) {
         const int h = j[kHead], hk = h / G, b = j[kB], q0 = j[qQ0], k0 = j[qK0], N = j[qN];
         job_done(slots, take, false);
         if (!N) continue;
-        if (!(ok = wait_live(q_empty, qph ^ 1, dead))) break;
+        if (!(ok = wait_live(q_empty, qph ^ 1, live))) break;
         mbar_arrive_expect_tx(q_full, C::kTile);
         load_tile<C::NH>(sm, &tm_q, q_full, h, q0, b);
         for (int x = 0; x < N; ++x) {
-          if (!(ok = wait_live(k_empty + rk.i, rk.ph ^ 1, dead))) break;
+          if (!(ok = wait_live(k_empty + rk.i, rk.ph ^ 1, live))) break;
           mbar_arrive_expect_tx(k_full + rk.i, C::kTile);
           load_tile<C::NH>(sm + (2 + rk.i) * C::kTile, &tm_k, k_full + rk.i, hk, k0 + x * 128, b);
           rk.next();
           if (x == 0) {
-            if (!(ok = wait_live(do_empty, qph ^ 1, dead))) break;
+            if (!(ok = wait_live(do_empty, qph ^ 1, live))) break;
             qph ^= 1;
             mbar_arrive_expect_tx(do_full, C::kTile);
             load_tile<C::NH>(sm + C::kTile, &tm_do, do_full, h, q0, b);
           }
-          if (!(ok = wait_live(v_empty + rv.i, rv.ph ^ 1, dead))) break;
+          if (!(ok = wait_live(v_empty + rv.i, rv.ph ^ 1, live))) break;
           mbar_arrive_expect_tx(v_full + rv.i, C::kTile);
           load_tile<C::NH>(sm + (5 + rv.i) * C::kTile, &tm_v, v_full + rv.i, hk, k0 + x * 128, b);
           rv.next();
         }
       }
-      if (*dead) {  // nothing may still be written at exit (bounded)
+      if (live->dead) {  // nothing may still be written at exit (bounded)
         mbar_wait(q_full, qph, 10000);  // of a load that has only just begun, if any
         mbar_wait(q_full, qph ^ 1, 10000);
         mbar_wait(do_full, qph ^ 1, 10000);
@@ -579,12 +581,13 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       Ring<3> rk, rd;   // K for S (a tile ahead) and for dQ
       Ring<2> rv, ss, sd;  // V; S buffer written, dS buffer read
       uint32_t qph = 0, fph = 0, aph = 0, rph = 0;
+      int turns = 0;
       bool ok = true;
       auto have_k = [&](bool last) {
-        if (!wait_live(k_full + rk.i, rk.ph, dead)) return false;
+        if (!wait_live(k_full + rk.i, rk.ph, live)) return false;
         if (!last) return true;
         mbar_arrive(landed);
-        const bool got = wait_live(fixed, fph, dead);
+        const bool got = wait_live(fixed, fph, live);
         fph ^= 1;
         return got;
       };
@@ -605,37 +608,38 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         mma_commit(v_empty + rv.i);
         rv.next();
       };
-      while (const int* j = ok ? next_job(slots, take, false, dead) : nullptr) {
+      while (const int* j = ok ? next_job(slots, take, false, live) : nullptr) {
         const int N = j[qN];
         const bool fix = packed && N * 128 > j[qLk];
         job_done(slots, take, false);
         if (N <= 3) mbar_arrive(&slots->soon);  // before the scheduler is asked to clean the last tile
         if (!N) continue;
-        if (!(ok = wait_live(q_full, qph, dead) && have_k(fix && N == 1))) break;
+        if (!(ok = wait_live(q_full, qph, live) && have_k(fix && N == 1))) break;
         scores(N == 1);
         // the dP before (of the last job, too) has been read
-        if (!(ok = wait_live(do_full, qph, dead) && wait_live(v_full + rv.i, rv.ph, dead) &&
-                   wait_live(dp_read, rph ^ 1, dead)))
+        if (!(ok = wait_live(do_full, qph, live) && wait_live(v_full + rv.i, rv.ph, live) &&
+                   wait_live(dp_read, rph ^ 1, live)))
           break;
         rph ^= 1;
         qph ^= 1;
         tc_fence_after();
         dprobs(N == 1);
-        if (!(ok = wait_live(acc_empty, aph ^ 1, dead))) break;
+        if (!(ok = wait_live(acc_empty, aph ^ 1, live))) break;
         aph ^= 1;
         ok = N == 1 || have_k(fix && N == 2);
 #pragma unroll 1
         for (int x = 0; x < N && ok; ++x) {
+          live->progress[0] = ++turns;
           if (x > 0 && x == N - 3) mbar_arrive(&slots->soon);
           if (x + 1 < N) {
             scores(x + 2 == N);  // over the dS of tile x - 1, behind the product that reads it
-            if (!(ok = wait_live(v_full + rv.i, rv.ph, dead) && wait_live(dp_read, rph ^ 1, dead))) break;
+            if (!(ok = wait_live(v_full + rv.i, rv.ph, live) && wait_live(dp_read, rph ^ 1, live))) break;
             rph ^= 1;
             tc_fence_after();
             dprobs(x + 2 == N);
             if (x + 2 < N && !(ok = have_k(fix && x + 3 == N))) break;
           }
-          if (!(ok = wait_live(ds_full + sd.i, sd.ph, dead))) break;
+          if (!(ok = wait_live(ds_full + sd.i, sd.ph, live))) break;
           tc_fence_after();
           mma_sum<DP, 8, 2, 32>(tmem + kDQ, tmem + kS + 128 * sd.i, desc_at(cols, (2 + rd.i) * C::kTile), x > 0);
           mma_commit(k_empty + rd.i);
@@ -644,7 +648,7 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         }
         mma_commit(acc_full);
       }
-      if (*dead) {
+      if (live->dead) {
         mma_commit(drain);
         mbar_wait(drain, 0, 10000);
       }
@@ -654,7 +658,7 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       uint32_t ph = 0;
       const int ctas = gridDim.x;
       schedule(
-          slots, dead,
+          slots, live,
           [&](int cta, int(&j)[12]) {
             // the tiles with the most keys first
             const int u = cta / a.H;
@@ -670,7 +674,7 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           [&](const volatile int* j) {
             it += j[qN];
             if (!packed || j[qN] * 128 <= j[qLk]) return true;
-            if (!warp_wait_live(landed, ph, dead)) return false;
+            if (!warp_wait_live(landed, ph, live)) return false;
             ph ^= 1;
             zero_rows<C::NH>(sm + (2 + (it - 1) % 3) * C::kTile, j[qLk] - (j[qN] - 1) * 128, lane);
             if (lane == 0) mbar_arrive(fixed);
@@ -694,7 +698,7 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       part[g * 128 + row] = x;
       __syncwarp();
       if (lane == 0) mbar_arrive(part_full);
-      ok = warp_wait_live(part_full, pph, dead);
+      ok = warp_wait_live(part_full, pph, live);
       pph ^= 1;
       return part[row] + part[128 + row] + part[256 + row] + part[384 + row];
     };
@@ -714,7 +718,7 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         }
       }
     };
-    const int* j = next_job(slots, take, true, dead);
+    const int* j = next_job(slots, take, true, live);
     fetch(j);
     while (j) {
       const int N = j[qN], nr = j[qNr];
@@ -723,7 +727,7 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       lse *= kLog2e;
       if (N) {
         // (for N = 1, dO may be the next job's by now, and do_full a phase further)
-        if (N > 1 && !(ok = warp_wait_live(do_full, oph, dead))) break;
+        if (N > 1 && !(ok = warp_wait_live(do_full, oph, live))) break;
         oph ^= 1;
         if (N > 1) {  // delta = do . o: a thread takes DP / 4 values of its row
 #pragma unroll
@@ -748,7 +752,7 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       for (int x = 0; x < N; ++x) {
         const int buf = rs.i;
         const uint32_t ts = tmem + lanes + kS + 128 * buf + 32 * g;
-        if (!(ok = warp_wait_live(s_full + buf, rs.ph, dead))) break;
+        if (!(ok = warp_wait_live(s_full + buf, rs.ph, live))) break;
         rs.next();
         tc_fence_after();
         float p[32], d[32];
@@ -760,7 +764,7 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           const float2 e = unpack(fma2(f2(p[y], p[y + 1]), cc, ls));
           p[y] = ex2(e.x), p[y + 1] = ex2(e.y);
         }
-        if (!(ok = warp_wait_live(dp_full, dph, dead))) break;
+        if (!(ok = warp_wait_live(dp_full, dph, live))) break;
         dph ^= 1;
         tc_fence_after();
         tmem_ld32_start(td, d);
@@ -801,10 +805,10 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       const long long stride = (long long)a.H * a.D;
       __nv_bfloat16* dst = a.dq + ((tok - row + w0) * a.H + j[kHead]) * a.D;
       job_done(slots, take, true);
-      j = next_job(slots, take, true, dead);
+      j = next_job(slots, take, true, live);
       fetch(j);
       if (N) {
-        if (!(ok = warp_wait_live(acc_full, aph, dead))) break;
+        if (!(ok = warp_wait_live(acc_full, aph, live))) break;
         aph ^= 1;
         tc_fence_after();
         if (g * kPart < DP)
@@ -820,7 +824,7 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (threadIdx.x == 0 && *dead) report_timeout();
+  if (threadIdx.x == 0 && live->dead) report_timeout();
   if (warp == 17) tmem_dealloc(tmem, 512);
 }
 

@@ -122,13 +122,13 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   uint64_t* kv_full = drain + 1;              // [kStages]
   uint64_t* kv_empty = kv_full + C::kStages;  // [kStages]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(kv_empty + C::kStages);
-  volatile int* dead = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile Liveness* live = reinterpret_cast<volatile Liveness*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (!aligned_smem(sm)) return;
   if (blockIdx.x == 0 && !a.sq.valid() && threadIdx.x == 0) atomicExch(&g_file_status, GDN_ERR_SEQLENS);
   if (threadIdx.x == kSoftmax) {
-    *dead = 0;
+    live->dead = live->progress[0] = live->progress[1] = 0;
     slots->init(18);
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full + i, 1);
@@ -166,20 +166,20 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       Ring<C::kStages> kv;
       uint32_t qph[2] = {0, 0};
       bool ok = true;
-      while (const int* j = ok ? next_job(slots, take, false, dead) : nullptr) {
+      while (const int* j = ok ? next_job(slots, take, false, live) : nullptr) {
         const int h = j[kHead], hk = h / a.G, b = j[kB], q0 = j[kQ0], k0 = j[kK0], n[2] = {j[kN0], j[kN1]};
         const int nmax = max(n[0], n[1]);
         job_done(slots, take, false);
         auto load_q = [&](int i) {
           if (!n[i]) return;
-          ok = ok && wait_live(q_empty + i, qph[i] ^ 1, dead);
+          ok = ok && wait_live(q_empty + i, qph[i] ^ 1, live);
           if (!ok) return;
           qph[i] ^= 1;
           mbar_arrive_expect_tx(q_full + i, C::kTile);
           load_tile<C::NH>(sm + i * C::kTile, &tm_q, q_full + i, h, q0 + 128 * i, b);
         };
         auto load_kv = [&](const CUtensorMap* tm, int x) {
-          ok = ok && wait_live(kv_empty + kv.i, kv.ph ^ 1, dead);
+          ok = ok && wait_live(kv_empty + kv.i, kv.ph ^ 1, live);
           if (!ok) return;
           mbar_arrive_expect_tx(kv_full + kv.i, C::kTile);
           load_tile<C::NH>(sm + (2 + kv.i) * C::kTile, tm, kv_full + kv.i, hk, k0 + x * 128, b);
@@ -193,7 +193,7 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           load_kv(&tm_v, x);
         }
       }
-      if (*dead) {
+      if (live->dead) {
         for (int i = 0; i < 2; ++i) mbar_wait(q_full + i, qph[i] ^ 1, 10000);
         drain_loads(kv_full, kv);
       }
@@ -203,6 +203,7 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       const uint64_t dv = sw128_desc(smem_u32(sm), 16384, 1024);  // MN-major, 64-column blocks 16 KB apart
       Ring<C::kStages> kv;  // the next tile to wait for
       uint32_t qph0 = 0, qph1 = 0, pph0 = 0, pph1 = 0, oph0 = 0, oph1 = 0, fph = 0;
+      int turns = 0;
       bool ok = true;
       auto qk = [&](int i, int stage) {
         mma_rows<DP>(tmem + C::kS + 128 * i, desc_at(dq, i * C::kTile), desc_at(dq, (2 + stage) * C::kTile));
@@ -212,16 +213,16 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       auto turn = [&](int i, int x, int n, int vs, int ks, uint32_t& pph, uint32_t& oph) {
         if (x >= n) return true;
         if (x == 0) {  // the job before has read O
-          if (!wait_live(o_empty + i, oph ^ 1, dead)) return false;
+          if (!wait_live(o_empty + i, oph ^ 1, live)) return false;
           oph ^= 1;
         }
         // the first 64 keys' products run while the others' exponentials are made
         const uint32_t o = tmem + C::kO + DP * i, p = tmem + C::kS + 128 * i;
         const uint64_t v = desc_at(dv, (2 + vs) * C::kTile);
-        if (!wait_live(p_full + 2 * i, pph, dead)) return false;
+        if (!wait_live(p_full + 2 * i, pph, live)) return false;
         tc_fence_after();
         mma_sum<DP, 4>(o, p, v, x > 0);
-        if (!wait_live(p_full + 2 * i + 1, pph, dead)) return false;
+        if (!wait_live(p_full + 2 * i + 1, pph, live)) return false;
         pph ^= 1;
         tc_fence_after();
         mma_sum<DP, 4>(o, p + 32, desc_at(v, 8192), true);
@@ -233,7 +234,7 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         return true;
       };
-      while (const int* j = ok ? next_job(slots, take, false, dead) : nullptr) {
+      while (const int* j = ok ? next_job(slots, take, false, live) : nullptr) {
         const int n0 = j[kN0], n1 = j[kN1], nmax = max(n0, n1);
         const bool fix = j[kFix];
         job_done(slots, take, false);
@@ -241,15 +242,15 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           mbar_arrive(&slots->soon);
           continue;
         }
-        if (!(ok = wait_live(kv_full + kv.i, kv.ph, dead))) break;
+        if (!(ok = wait_live(kv_full + kv.i, kv.ph, live))) break;
         if (n0) {
-          if (!(ok = wait_live(q_full, qph0, dead))) break;
+          if (!(ok = wait_live(q_full, qph0, live))) break;
           qph0 ^= 1;
           qk(0, kv.i);
           if (n0 == 1) mma_commit(q_empty);
         }
         if (n1) {
-          if (!(ok = wait_live(q_full + 1, qph1, dead))) break;
+          if (!(ok = wait_live(q_full + 1, qph1, live))) break;
           qph1 ^= 1;
           qk(1, kv.i);
           if (n1 == 1) mma_commit(q_empty + 1);
@@ -257,19 +258,20 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         mma_commit(kv_empty + kv.i);
         kv.next();
         int vs = kv.i, ks = 0;  // V of key tile x, K of x + 1
-        if (!(ok = wait_live(kv_full + vs, kv.ph, dead))) break;
+        if (!(ok = wait_live(kv_full + vs, kv.ph, live))) break;
         kv.next();
         if (nmax > 1) {
           ks = kv.i;
-          if (!(ok = wait_live(kv_full + ks, kv.ph, dead))) break;
+          if (!(ok = wait_live(kv_full + ks, kv.ph, live))) break;
           kv.next();
         }
 #pragma unroll 1
         for (int x = 0; x < nmax; ++x) {
+          live->progress[0] = ++turns;
           if (x == max(0, nmax - 2)) mbar_arrive(&slots->soon);
           if (fix && x + 1 == nmax) {
             mbar_arrive(v_landed);
-            if (!(ok = wait_live(v_fixed, fph, dead))) break;
+            if (!(ok = wait_live(v_fixed, fph, live))) break;
             fph ^= 1;
           }
           if (!(ok = turn(0, x, n0, vs, ks, pph0, oph0))) break;
@@ -277,12 +279,12 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           int vn = 0, kn = 0;
           if (x + 1 < nmax) {
             vn = kv.i;
-            if (!(ok = wait_live(kv_full + vn, kv.ph, dead))) break;
+            if (!(ok = wait_live(kv_full + vn, kv.ph, live))) break;
             kv.next();
           }
           if (x + 2 < nmax) {
             kn = kv.i;
-            if (!(ok = wait_live(kv_full + kn, kv.ph, dead))) break;
+            if (!(ok = wait_live(kv_full + kn, kv.ph, live))) break;
             kv.next();
           }
           if (!(ok = turn(1, x, n1, vs, ks, pph1, oph1))) break;
@@ -291,7 +293,7 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           vs = vn, ks = kn;
         }
       }
-      if (*dead) {
+      if (live->dead) {
         mma_commit(drain);
         mbar_wait(drain, 0, 10000);
       }
@@ -301,13 +303,13 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       uint32_t ph = 0;
       const int ctas = gridDim.x;
       schedule(
-          slots, dead, [&](int cta, int(&j)[12]) { return decode(a, cta, ctas, j); },
+          slots, live, [&](int cta, int(&j)[12]) { return decode(a, cta, ctas, j); },
           [](const volatile int*) { return true; },
           [&](const volatile int* j) {
             const int n = max(j[kN0], j[kN1]);
             it += 2 * n;
             if (!j[kFix]) return true;
-            if (!warp_wait_live(v_landed, ph, dead)) return false;
+            if (!warp_wait_live(v_landed, ph, live)) return false;
             ph ^= 1;
             zero_rows<C::NH>(sm + (2 + (it - 1) % C::kStages) * C::kTile, j[kLk] - (n - 1) * 128, lane);
             if (lane == 0) mbar_arrive(v_fixed);
@@ -326,14 +328,14 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     const F2 cc = f2(c, c);
     uint32_t sph = 0, oph = 0;
     bool ok = true;
-    while (const int* j = ok ? next_job(slots, take, true, dead) : nullptr) {
+    while (const int* j = ok ? next_job(slots, take, true, live) : nullptr) {
       const int n = j[kN0 + i], lk = j[kLk];
       const int first = min(j[kFirst] + 128 * i + w0, lk - 1);  // last key that the warp's first row sees
       float m[2] = {-INFINITY, -INFINITY};
       F2 l[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll 1
       for (int x = 0; x < n; ++x) {
-        if (!(ok = warp_wait_live(s_full + i, sph, dead))) break;
+        if (!(ok = warp_wait_live(s_full + i, sph, live))) break;
         sph ^= 1;
         tc_fence_after();
         float s[64];
@@ -400,7 +402,7 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
       }
       if (ok && n) {
-        ok = warp_wait_live(o_full + i, oph, dead);
+        ok = warp_wait_live(o_full + i, oph, live);
         oph ^= 1;
         tc_fence_after();
       }
@@ -451,7 +453,7 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (threadIdx.x == 0 && *dead) report_timeout();
+  if (threadIdx.x == 0 && live->dead) report_timeout();
   if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
@@ -487,6 +489,35 @@ __global__ void __launch_bounds__(256) attn_join_kernel(Args a, __nv_bfloat16* o
   }
   if (4 * lane < a.D)
     *reinterpret_cast<uint2*>(o + r * a.D + 4 * lane) = make_uint2(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]));
+}
+
+// One warp waits for an arrival that comes after eight times its patience, with
+// signs of progress all the while, then for one that never comes; the other warp
+// gives the signs.  Nothing else is in flight.
+__global__ void __launch_bounds__(64) attn_wait_selftest_kernel(uint32_t patience) {
+  __shared__ uint64_t late, never;
+  __shared__ Liveness state;
+  volatile Liveness* live = &state;
+  if (threadIdx.x == 0) {
+    mbar_init(&late, 1);
+    mbar_init(&never, 1);
+    live->dead = live->progress[0] = live->progress[1] = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const bool came = warp_wait_job(&late, 0, live, patience) && !live->dead;
+    const bool ran_out = !warp_wait_job(&never, 0, live, patience) && live->dead;
+    if (threadIdx.x == 0) atomicExch(&g_file_status, came && ran_out ? GDN_ERR_DEVICE_TIMEOUT : GDN_ERR_ARG);
+  } else if (threadIdx.x == 32) {
+    for (int i = 1; i <= 32; ++i) {
+      const uint32_t since = clock();  // a turn takes a clock at least
+      for (uint32_t k = 0; k < patience && (uint32_t)clock() - since < patience / 4; ++k) {
+      }
+      live->progress[0] = i;
+    }
+    mbar_arrive(&late);
+  }
 }
 
 // Parts of a job's keys, from the sizes alone (a packed sequence's own length is
@@ -555,6 +586,11 @@ cudaError_t run(const AttnProblem& p, cudaStream_t s) {
 }
 
 }  // namespace
+
+cudaError_t attn_wait_selftest(int clocks, cudaStream_t s) {
+  attn_wait_selftest_kernel<<<1, 64, 0, s>>>((uint32_t)clocks);
+  return cudaGetLastError();
+}
 
 bool attn_tc_supported(const AttnProblem& p) {
   return p.bf16 && p.Tq > 0 && p.Tk > 0 && attn_map_ok(p.q, p.B, p.Tq, p.H, p.D, p.qs) &&

@@ -202,7 +202,7 @@ cudaError_t gated_rmsnorm_fwd(const NormProblem& p, cudaStream_t s);
 cudaError_t gated_rmsnorm_bwd(const NormProblem& p, cudaStream_t s);
 cudaError_t nb_read_and_clear_status(int* status);
 
-// Causal attention over whole prompts (attn_simt.cu, attn_tc.cu); see
+// Causal attention over whole prompts (attn_simt.cu, attn_tc_fwd.cu, attn_tc_bwd.cu); see
 // include/gdn.h.  Strides are batch, token, head, in elements.
 struct AttnProblem {
   int B = 0, Tq = 0, Tk = 0, H = 0, Hkv = 0, D = 0;
@@ -225,6 +225,7 @@ bool attn_tc_supported(const AttnProblem& p);
 size_t attn_tc_fwd_workspace(const AttnProblem& p);  // reads sizes, cu_q != NULL and nseq
 cudaError_t attn_tc_fwd(const AttnProblem& p, cudaStream_t s);
 cudaError_t attn_tc_bwd(const AttnProblem& p, cudaStream_t s);
+cudaError_t attn_wait_selftest(int clocks, cudaStream_t s);
 // delta [B, H, Tq] = rowsum(do * o), fp32: the workspace of the backward (both
 // kernel families).
 size_t attn_bwd_workspace(const AttnProblem& p);

@@ -166,6 +166,11 @@ int gdn_attn_bwd(const gdn_attn_shape* shape, const void* q, const void* k, cons
   return done(gdn::attn_tc_supported(p) ? gdn::attn_tc_bwd(p, st) : gdn::attn_simt_bwd(p, st));
 }
 
+int gdn_attn_wait_selftest(int clocks, void* stream) {
+  if (clocks < 1 || clocks > (1 << 26)) return GDN_ERR_ARG;
+  return done(gdn::attn_wait_selftest(clocks, static_cast<cudaStream_t>(stream)));
+}
+
 size_t gdn_attn_decode_workspace(const gdn_attn_decode_shape* shape) {
   gdn::AttnDecodeProblem p;
   if (decode_problem(shape, &p) != GDN_OK || decode_empty(p)) return 0;

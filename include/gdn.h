@@ -501,6 +501,15 @@ GDN_API int gdn_device_status(void);
  * max_tries must be in [1, 1000] (GDN_ERR_ARG otherwise). */
 GDN_API int gdn_wait_selftest(int max_tries, void* stream);
 
+/* The same for the waits of the attention kernels, which give up after a number
+ * of SM clocks (2^31 in the kernels, about a second; `clocks` here, in [1, 2^26],
+ * GDN_ERR_ARG otherwise) in which no part of the CTA has moved.  One CTA on
+ * `stream` waits eight times that long for an arrival while another warp shows
+ * progress, and gets it; then it waits for one that never comes and gives up,
+ * with nothing in flight.  A following gdn_device_status() returns
+ * GDN_ERR_DEVICE_TIMEOUT, or GDN_ERR_ARG if either wait ended otherwise. */
+GDN_API int gdn_attn_wait_selftest(int clocks, void* stream);
+
 /* 1 if the tensor-core kernels would run for this shape, else 0 (GDN / KDA).
  * For KDA this is the kernel family of the shape; a sequence whose gates
  * decay too fast for it inside some chunk is still computed by the CUDA-core
