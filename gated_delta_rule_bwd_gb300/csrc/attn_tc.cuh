@@ -98,16 +98,27 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// The waits for a whole warp: one lane polls.
+// The waits for a whole warp: one lane polls.  That orders the polling lane's accesses
+// behind the barrier, and the other lanes' only with the __syncwarp of warp_wait_data
+// and warp_wait_job, which shared memory read or written next asks for.  What follows
+// warp_wait_live is a tcgen05.ld of the whole warp, or nothing (the __syncwarp costs
+// the forward 5 % at its hand-over of S).
 __device__ __forceinline__ bool warp_wait_live(uint64_t* bar, uint32_t parity, volatile Liveness* live) {
   int ok = 1;
   if ((threadIdx.x & 31) == 0) ok = wait_live(bar, parity, live);
+  return __shfl_sync(0xffffffffu, ok, 0);
+}
+__device__ __forceinline__ bool warp_wait_data(uint64_t* bar, uint32_t parity, volatile Liveness* live) {
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) ok = wait_live(bar, parity, live);
+  __syncwarp();
   return __shfl_sync(0xffffffffu, ok, 0);
 }
 __device__ __forceinline__ bool warp_wait_job(uint64_t* bar, uint32_t parity, volatile Liveness* live,
                                               uint32_t patience = kPatience) {
   int ok = 1;
   if ((threadIdx.x & 31) == 0) ok = wait_job(bar, parity, live, patience);
+  __syncwarp();
   return __shfl_sync(0xffffffffu, ok, 0);
 }
 
@@ -216,7 +227,7 @@ __device__ __forceinline__ bool next_cta(TileSlots* ts, uint32_t& ph, int& x, vo
         : "memory");
   }
   __syncwarp();
-  if (!warp_wait_live(&ts->response_full, ph, live)) {
+  if (!warp_wait_data(&ts->response_full, ph, live)) {
     mbar_wait(&ts->response_full, ph, 10000);  // nothing may still be written at exit (bounded)
     return false;
   }

@@ -310,7 +310,7 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         if (ni) fetch(i0);
         for (int g = 0; g < G && ok; ++g)
           for (int i = i0; i < i0 + ni; ++i) {
-            if (!(ok = warp_wait_live(st_empty + rs.i, rs.ph ^ 1, live))) break;
+            if (!(ok = warp_wait_data(st_empty + rs.i, rs.ph ^ 1, live))) break;
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               stats[rs.i * 256 + lane + 32 * x] = ls[x];
@@ -381,7 +381,7 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
 #pragma unroll 1
       for (int it = 0; it < N; ++it) {
         const float *lse = stats + rs.i * 256 + 32 * g, *delta = lse + 128;
-        if (!(ok = warp_wait_live(st_full + rs.i, rs.ph, live))) break;
+        if (!(ok = warp_wait_data(st_full + rs.i, rs.ph, live))) break;
         float p[32], n[32];
 #pragma unroll
         for (int x = 0; x < 32; x += 4) *reinterpret_cast<float4*>(n + x) = *reinterpret_cast<const float4*>(lse + x);
@@ -674,7 +674,7 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           [&](const volatile int* j) {
             it += j[qN];
             if (!packed || j[qN] * 128 <= j[qLk]) return true;
-            if (!warp_wait_live(landed, ph, live)) return false;
+            if (!warp_wait_data(landed, ph, live)) return false;
             ph ^= 1;
             zero_rows<C::NH>(sm + (2 + (it - 1) % 3) * C::kTile, j[qLk] - (j[qN] - 1) * 128, lane);
             if (lane == 0) mbar_arrive(fixed);
@@ -698,7 +698,7 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       part[g * 128 + row] = x;
       __syncwarp();
       if (lane == 0) mbar_arrive(part_full);
-      ok = warp_wait_live(part_full, pph, live);
+      ok = warp_wait_data(part_full, pph, live);
       pph ^= 1;
       return part[row] + part[128 + row] + part[256 + row] + part[384 + row];
     };
@@ -727,7 +727,7 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       lse *= kLog2e;
       if (N) {
         // (for N = 1, dO may be the next job's by now, and do_full a phase further)
-        if (N > 1 && !(ok = warp_wait_live(do_full, oph, live))) break;
+        if (N > 1 && !(ok = warp_wait_data(do_full, oph, live))) break;
         oph ^= 1;
         if (N > 1) {  // delta = do . o: a thread takes DP / 4 values of its row
 #pragma unroll

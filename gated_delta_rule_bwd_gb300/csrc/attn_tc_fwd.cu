@@ -309,7 +309,7 @@ attn_tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const int n = max(j[kN0], j[kN1]);
             it += 2 * n;
             if (!j[kFix]) return true;
-            if (!warp_wait_live(v_landed, ph, live)) return false;
+            if (!warp_wait_data(v_landed, ph, live)) return false;
             ph ^= 1;
             zero_rows<C::NH>(sm + (2 + (it - 1) % C::kStages) * C::kTile, j[kLk] - (n - 1) * 128, lane);
             if (lane == 0) mbar_arrive(v_fixed);
