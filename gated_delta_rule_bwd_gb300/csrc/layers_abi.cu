@@ -112,6 +112,18 @@ int ln_problem(const gdn_norm_shape* s, float eps, gdn::LayerNormProblem* p) {
   return GDN_OK;
 }
 
+// Rows that are whole 16-byte vectors are read and written in vectors and start on
+// one; other rows, and the fp32 vectors and statistics always, go value by value.
+bool ln_aligned(const gdn::LayerNormProblem& p, std::initializer_list<const void*> rows,
+                std::initializer_list<const void*> values) {
+  const size_t e = p.bf16 ? 2 : 4, a = p.D * e % 16 == 0 ? 16 : e;
+  for (const void* x : rows)
+    if (!aligned(x, a)) return false;
+  for (const void* x : values)
+    if (!aligned(x, 4)) return false;
+  return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -202,7 +214,7 @@ int gdn_layer_norm_fwd(const gdn_norm_shape* shape, const void* x, const float* 
   int rc = ln_problem(shape, eps, &p);
   if (rc != GDN_OK || p.rows == 0) return rc;
   if (any_null({x, weight, y})) return GDN_ERR_ARG;
-  if (!all_aligned16({x, y, weight, bias})) return GDN_ERR_ALIGN;
+  if (!ln_aligned(p, {x, y}, {weight, bias, mean, rstd})) return GDN_ERR_ALIGN;
   p.x = x, p.weight = weight, p.bias = bias, p.y = y, p.mean = mean, p.rstd = rstd;
   return done(gdn::layer_norm_fwd(p, static_cast<cudaStream_t>(stream)));
 }
@@ -228,7 +240,7 @@ int gdn_layer_norm_bwd(const gdn_norm_shape* shape, const void* x, const float* 
     return done(e);
   }
   if (any_null({x, weight, mean, rstd, dy, dx})) return GDN_ERR_ARG;
-  if (!all_aligned16({x, dy, dx, weight, dweight, dbias, ws})) return GDN_ERR_ALIGN;
+  if (!ln_aligned(p, {x, dy, dx}, {weight, mean, rstd, dweight, dbias}) || !aligned(ws, 16)) return GDN_ERR_ALIGN;
   const size_t need = gdn::layer_norm_bwd_workspace(p);
   if (!ws || ws_bytes < need) return GDN_ERR_WORKSPACE;
   p.x = x, p.weight = weight, p.mean = const_cast<float*>(mean), p.rstd = const_cast<float*>(rstd);

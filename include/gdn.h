@@ -465,7 +465,9 @@ GDN_API int gdn_attn_decode(const gdn_attn_decode_shape* shape, const void* q, c
  * mean and rstd ([rows], fp32) are written for the backward unless NULL.  The
  * backward writes dx (layout and dtype of x) and dweight, dbias [D] (fp32,
  * overwritten, summed over the rows in a fixed order; dbias may be NULL) from
- * x, weight, mean, rstd and dy.  x, y, dy, dx contiguous and 16-byte aligned,
+ * x, weight, mean, rstd and dy.  x, y, dy, dx contiguous, and 16-byte aligned
+ * where a row is a whole number of 16-byte vectors (aligned to their element
+ * otherwise, as everything else but ws, which is 16-byte aligned);
  * D in [1, 65536], rows >= 0; dtype GDN_F32 or GDN_BF16.  Errors as for the
  * gated RMS norm. */
 GDN_API int gdn_layer_norm_fwd(const gdn_norm_shape* shape, const void* x, const float* weight,
