@@ -644,6 +644,13 @@ def _addr(x):
     return None if x is None else x.data_ptr()
 
 
+def _dense(x):
+    """x, contiguous and 16-byte aligned: a gradient may be a slice of another's
+    memory (of a concatenation's) that starts anywhere."""
+    x = x.contiguous()
+    return x if x.data_ptr() % 16 == 0 else x.clone()
+
+
 def _call(rc):
     if rc:
         _check(rc)
@@ -844,7 +851,7 @@ class Attention(torch.autograd.Function):
     @staticmethod
     def backward(ctx, do):
         q, k, v, o, lse, cu, cuk = ctx.saved_tensors
-        return (*attn_bwd(q, k, v, o, lse, do.contiguous(), cu, cuk, ctx.scale), None, None, None)
+        return (*attn_bwd(q, k, v, o, lse, _dense(do), cu, cuk, ctx.scale), None, None, None)
 
 
 def attention(q, k, v, cu_seqlens=None, cu_seqlens_k=None, scale=None):
@@ -857,7 +864,7 @@ class LayerNorm(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, weight, bias, eps):
-        x = x.contiguous()
+        x = _dense(x)
         y, mean, rstd = layer_norm_fwd(x, weight, bias, eps)
         ctx.save_for_backward(x, weight, mean, rstd)
         ctx.has_bias = bias is not None
@@ -866,7 +873,7 @@ class LayerNorm(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
-        dx, dw, db = layer_norm_bwd(x, weight, mean, rstd, dy.contiguous())
+        dx, dw, db = layer_norm_bwd(x, weight, mean, rstd, _dense(dy))
         return dx, dw, db if ctx.has_bias else None, None
 
 
@@ -937,8 +944,8 @@ class GatedDeltaRule(torch.autograd.Function):
     @staticmethod
     def backward(ctx, do, dht):
         q, k, v, g, beta, h0 = ctx.saved_tensors
-        gr = _bwd(ctx.kda, q, k, v, g, beta, h0, do.contiguous(),
-                  None if dht is None else dht.contiguous(), ctx.chunk, h0 is not None,
+        gr = _bwd(ctx.kda, q, k, v, g, beta, h0, _dense(do),
+                  None if dht is None else _dense(dht), ctx.chunk, h0 is not None,
                   ctx=ctx.saved, delta=ctx.delta)
         ctx.saved = None
         return (gr["dq"], gr["dk"], gr["dv"], gr["dg"], gr["dbeta"], gr["dh0"], None, None,
