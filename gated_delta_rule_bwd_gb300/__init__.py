@@ -29,6 +29,7 @@ import os
 import threading
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdn.so")
@@ -849,6 +850,7 @@ class Attention(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do):
         q, k, v, o, lse, cu, cuk = ctx.saved_tensors
         return (*attn_bwd(q, k, v, o, lse, _dense(do), cu, cuk, ctx.scale), None, None, None)
@@ -871,6 +873,7 @@ class LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         dx, dw, db = layer_norm_bwd(x, weight, mean, rstd, _dense(dy))

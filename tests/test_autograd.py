@@ -47,3 +47,15 @@ def test_gradient_between_boundaries(make, dtype):
 def test_layer_norm_input_between_boundaries(dtype):
     x, w = rand(0, 1 + 5 * 64, dtype=dtype), rand(1, 64)
     assert torch.equal(gdn.layer_norm(x[1:].view(5, 64), w), gdn.layer_norm(x[1:].clone().view(5, 64), w))
+
+
+@gpu
+@pytest.mark.parametrize("make", [attention, layer_norm])
+def test_second_derivatives_are_refused(make):
+    """The gradients have no gradient of their own: a loss that holds one raises
+    instead of going on without its share."""
+    f, x = make(F32)
+    x = [t.requires_grad_() for t in x]
+    first, *_ = torch.autograd.grad(f(*x).square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="differentiate twice"):
+        (first.square().sum() + x[0].sum()).backward()
