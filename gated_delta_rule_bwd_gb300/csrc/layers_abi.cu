@@ -166,7 +166,16 @@ int gdn_attn_bwd(const gdn_attn_shape* shape, const void* q, const void* k, cons
   gdn::AttnProblem p;
   int rc = attn_problem(shape, scale, cu_q, cu_k, nseq, &p);
   if (rc != GDN_OK) return rc;
-  if (p.B == 0 || p.H == 0 || (p.Tq == 0 && p.Tk == 0)) return GDN_OK;
+  if (p.B == 0 || (p.Tq == 0 && p.Tk == 0)) return GDN_OK;
+  if (p.H == 0) {  // key heads without query heads
+    const size_t n = (size_t)p.B * p.Tk * p.Hkv * p.D * (p.bf16 ? 2 : 4);
+    if (n == 0) return GDN_OK;
+    if (any_null({dk, dv})) return GDN_ERR_ARG;
+    if (!all_aligned16({dk, dv})) return GDN_ERR_ALIGN;
+    cudaError_t e = cudaMemsetAsync(dk, 0, n, static_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess) e = cudaMemsetAsync(dv, 0, n, static_cast<cudaStream_t>(stream));
+    return done(e);
+  }
   if ((p.Tq > 0 && any_null({o, lse, do_, dq})) || (p.Tk > 0 && any_null({dk, dv}))) return GDN_ERR_ARG;
   if ((rc = attn_inputs(&p, q, k, v)) != GDN_OK) return rc;
   if (!all_aligned16({o, lse, do_, dq, dk, dv, ws})) return GDN_ERR_ALIGN;
