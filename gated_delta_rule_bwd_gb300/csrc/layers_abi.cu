@@ -2,6 +2,7 @@
 // kernel selection, launch.  The operations, layouts and error rules are
 // stated in include/gdn.h.
 
+#include <limits.h>
 #include <math.h>
 
 #include <initializer_list>
@@ -65,6 +66,10 @@ int attn_problem(const gdn_attn_shape* s, float scale, const int* cu_q, const in
   p->B = s->B, p->Tq = s->Tq, p->Tk = s->Tk, p->H = s->H, p->Hkv = s->Hkv, p->D = s->D;
   p->bf16 = s->dtype == GDN_BF16;
   p->scale = scale;
+  // A grid has at most 2^31 - 1 CTAs: one per tile of 64 rows (or more) and head,
+  // empty packed sequences among them, and one per eight (row, head) pairs.
+  const long long T = s->Tq > s->Tk ? s->Tq : s->Tk, tiles = cu_q ? T / 64 + nseq : s->B * ((T + 63) / 64);
+  if (tiles * s->H > INT_MAX || (long long)s->B * s->Tq * s->H > 8LL * INT_MAX) return GDN_ERR_SHAPE;
   return GDN_OK;
 }
 

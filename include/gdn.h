@@ -379,7 +379,9 @@ GDN_API int gdn_gated_rmsnorm_bwd(const gdn_norm_shape* shape, const void* o, co
  * in elements: q, k and v may be views of one fused projection.  o, do_ and
  * dq are [B, Tq, H, D], dk and dv [B, Tk, Hkv, D], all contiguous; lse is
  * [B, H, Tq] fp32, contiguous.  D in [1, 128]; dtype GDN_F32 or GDN_BF16;
- * H a multiple of Hkv.
+ * H a multiple of Hkv.  Limits: H <= 65535; B Tq and B Tk <= 2^30; with T the
+ * larger of Tq and Tk, B ceil(T / 64) H (packed: (T / 64 + nseq) H) < 2^31 and
+ * B Tq H < 2^34.
  *
  * Packed sequences: cu_q and cu_k non-NULL, B = 1, each a DEVICE array of
  * nseq + 1 int32 offsets (sequence s is queries [cu_q[s], cu_q[s+1]) and keys

@@ -32,3 +32,30 @@ def test_key_heads_without_query_heads_refusals():
     call = lambda dk, dv: gdn.lib().gdn_attn_bwd(  # noqa: E731
         ctypes.byref(s), None, fake, fake, 0.5, None, None, 0, None, None, None, None, dk, dv, None, 0, None)
     assert call(None, fake) == -1 and call(fake, None) == -1 and call(odd, fake) == -4 and call(fake, odd) == -4
+
+
+def call(name, packed=False, nseq=0, **sizes):
+    """An entry point on made-up pointers: for calls that are refused before a launch."""
+    fake = ctypes.c_void_p(0x10000)
+    n = dict(B=1, Tq=8, Tk=8, H=16, Hkv=16, D=8) | sizes
+    s = gdn.AttnShape(*n.values(), 1, (0, 0, 0), (0, 0, 0), (0, 0, 0))
+    cu = fake if packed else None
+    f = getattr(gdn.lib(), name)
+    if name == "gdn_attn_fwd":
+        return f(ctypes.byref(s), fake, fake, fake, 0.5, cu, cu, nseq, fake, fake, fake, 1 << 62, None)
+    return f(ctypes.byref(s), fake, fake, fake, 0.5, cu, cu, nseq, *[fake] * 7, 1 << 62, None)
+
+
+@pytest.mark.parametrize("name", ["gdn_attn_fwd", "gdn_attn_bwd"])
+@pytest.mark.parametrize("sizes", [dict(packed=True, nseq=1 << 30, H=16), dict(packed=True, nseq=1 << 27, H=16, Hkv=1),
+                                   dict(B=1 << 24, Tq=1, Tk=1, H=128), dict(B=1 << 24, Tq=0, Tk=1, H=128),
+                                   dict(Tq=1 << 30, H=17, Hkv=1), dict(Tq=1, Tk=1 << 30, H=128, Hkv=1)])
+def test_more_jobs_than_a_grid_has(name, sizes):
+    assert call(name, **sizes) == -2
+
+
+def test_sizes_below_the_limits_have_a_workspace():
+    for n in (dict(B=1 << 24, Tq=1, Tk=1, H=127), dict(Tq=1 << 30, H=15, Hkv=1), dict(Tq=8, Tk=1 << 30, H=64, Hkv=1)):
+        n = dict(B=1, Tq=8, Tk=8, H=16, Hkv=n["H"], D=8) | n
+        s = gdn.AttnShape(*n.values(), 1, (0, 0, 0), (0, 0, 0), (0, 0, 0))
+        assert gdn.lib().gdn_attn_bwd_workspace(ctypes.byref(s), 0) == 4 * n["B"] * n["H"] * n["Tq"], n
