@@ -5,6 +5,7 @@
 #include <limits.h>
 #include <math.h>
 
+#include <algorithm>
 #include <initializer_list>
 
 #include "gdn.h"
@@ -134,11 +135,13 @@ bool ln_aligned(const gdn::LayerNormProblem& p, std::initializer_list<const void
 extern "C" {
 
 size_t gdn_attn_fwd_workspace(const gdn_attn_shape* shape, int nseq) {
+  // as a batch and, where nseq and B allow, as packed sequences: the query has no
+  // offsets that would tell the two apart
   gdn::AttnProblem p;
   static const int offsets[2] = {0, 0};  // stands for packed sequences; not read
-  const int* cu = nseq > 0 ? offsets : nullptr;
-  if (attn_problem(shape, 1.f, cu, cu, nseq, &p) != GDN_OK) return 0;
-  return fwd_workspace(p);
+  size_t need = attn_problem(shape, 1.f, nullptr, nullptr, 0, &p) == GDN_OK ? fwd_workspace(p) : 0;
+  if (nseq > 0 && attn_problem(shape, 1.f, offsets, offsets, nseq, &p) == GDN_OK) need = std::max(need, fwd_workspace(p));
+  return need;
 }
 
 int gdn_attn_fwd(const gdn_attn_shape* shape, const void* q, const void* k, const void* v, float scale,

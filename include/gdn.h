@@ -389,7 +389,9 @@ GDN_API int gdn_gated_rmsnorm_bwd(const gdn_norm_shape* shape, const void* o, co
  * rise from 0 to Tq / Tk give unspecified outputs (every access stays inside
  * the arrays) and gdn_device_status() returns GDN_ERR_SEQLENS.  With both
  * NULL, nseq is ignored and each of the B rows is one sequence of Tq queries
- * and Tk keys.
+ * and Tk keys.  The workspace queries take the nseq of the call; what they
+ * return is enough for a batch whatever nseq, and for packed sequences with
+ * that nseq.
  *
  * The backward returns the gradients of q, k and v from o and lse of the
  * forward and do_; heads that share a key head are summed into its gradient

@@ -59,3 +59,15 @@ def test_sizes_below_the_limits_have_a_workspace():
         n = dict(B=1, Tq=8, Tk=8, H=16, Hkv=n["H"], D=8) | n
         s = gdn.AttnShape(*n.values(), 1, (0, 0, 0), (0, 0, 0), (0, 0, 0))
         assert gdn.lib().gdn_attn_bwd_workspace(ctypes.byref(s), 0) == 4 * n["B"] * n["H"] * n["Tq"], n
+
+
+@pytest.mark.parametrize("B,Tq,Tk,H,D", [(1, 64, 4096, 2, 128), (2, 64, 4096, 2, 128), (1, 1400, 1400, 1, 64)])
+def test_workspace_of_a_batch_whatever_nseq(B, Tq, Tk, H, D):
+    """A batch call ignores nseq; so does what its workspace query returns at least."""
+    s = gdn.AttnShape(B, Tq, Tk, H, 1, D, 1, *[(1 << 20, 1 << 10, 128)] * 3)
+    need = lambda nseq: gdn.lib().gdn_attn_fwd_workspace(ctypes.byref(s), nseq)  # noqa: E731
+    assert need(0) > 0
+    for nseq in (-3, 1, 7, 100000, 1 << 30):
+        assert need(nseq) >= need(0), nseq
+    if B > 1:
+        assert need(7) == need(0)
