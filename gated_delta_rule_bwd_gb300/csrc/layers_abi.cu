@@ -96,6 +96,7 @@ int decode_problem(const gdn_attn_decode_shape* s, gdn::AttnDecodeProblem* p) {
   if (rc != GDN_OK) return rc;
   if (s->B < 0 || s->T < 0 || s->S < 0) return GDN_ERR_SHAPE;
   if (s->S > (1 << 30) || (s->T > s->S && s->B > 0)) return GDN_ERR_SHAPE;
+  if (s->H == 0 && s->Hkv > 0) return GDN_ERR_SHAPE;  // the cache's rows go out with the queries' work
   // every CTA sums the rows' lengths; 8 query rows per CTA in grid.y
   if ((long long)s->B * s->Hkv > 65535 || (s->Hkv > 0 && (long long)s->H / s->Hkv * s->T > 65535LL * 8))
     return GDN_ERR_SHAPE;

@@ -71,3 +71,12 @@ def test_workspace_of_a_batch_whatever_nseq(B, Tq, Tk, H, D):
         assert need(nseq) >= need(0), nseq
     if B > 1:
         assert need(7) == need(0)
+
+
+def test_decode_of_key_heads_without_query_heads_is_refused():
+    """It would have to extend the caches, and wrote nothing."""
+    fake = ctypes.c_void_p(0x10000)
+    s = lambda Hkv: gdn.AttnDecodeShape(1, 1, 8, 0, Hkv, 16, 1, (256, 32, 16), (256, 32, 16))  # noqa: E731
+    call = lambda Hkv: gdn.lib().gdn_attn_decode(  # noqa: E731
+        ctypes.byref(s(Hkv)), *[fake] * 6, 0.5, fake, None, 0, None)
+    assert call(2) == -2 and call(0) == 0
