@@ -272,6 +272,8 @@ def ctx_bytes(q, v, chunk=64, kda=False, delta=True) -> int:
 
 
 def _workspace(need, given, device):
+    if given is not None and (given.device != device or not given.is_contiguous()):
+        raise GdnError(f"workspace must be contiguous and on {device}, got one on {given.device}")
     if given is not None and given.numel() >= need:
         return given
     return torch.empty(max(need, 16), dtype=torch.uint8, device=device)

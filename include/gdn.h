@@ -449,7 +449,8 @@ GDN_API int gdn_attn_bwd(const gdn_attn_shape* shape, const void* q, const void*
  * unaligned caches).  The batch's keys are dealt out evenly over the GPU in
  * pieces of 64, whatever the rows' lengths, and a second kernel joins what is
  * split, through the workspace.  Limits: S <= 2^30, B Hkv <= 65535, no key heads
- * without query heads (H = 0 < Hkv).  Errors as above (GDN_ERR_ALIGN: q, k, v, o or ws not 16-byte aligned). */
+ * without query heads (H = 0 < Hkv).  Errors as above (GDN_ERR_ALIGN: q, k, v,
+ * o or ws not 16-byte aligned). */
 typedef struct {
   int B, T, S;        /* batch rows, new tokens per row, cache slots per row   */
   int H, Hkv, D;

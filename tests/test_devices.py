@@ -12,6 +12,17 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
             stream(torch.device("cuda", 1))
 
 
+def test_a_workspace_elsewhere_is_refused():
+    """The kernels would write to its address."""
+    cpu, cuda = torch.device("cpu"), torch.device("cuda", 0)
+    given = torch.empty(64, dtype=torch.uint8)
+    for x, device in ((given, cuda), (given[::2], cpu)):
+        with pytest.raises(gdn.GdnError, match="workspace"):
+            gdn._workspace(16, x, device)
+    assert gdn._workspace(16, given, cpu) is given
+    assert gdn._workspace(65, given, cpu) is not given
+
+
 @pytest.mark.gpu
 def test_calls_refuse_another_current_device(monkeypatch):
     """Every call asks for its stream, and that refuses; nothing is launched."""
