@@ -19,8 +19,8 @@
 // exp(m_p - m) l_p.  No atomics: the order of every sum is fixed.
 //
 // Measured: 64 rows of 1638 to 8191 tokens, 16 heads on 4, D 128, bf16: 110 us the
-// call, 5.9 TB/s (102 us and 6.3 TB/s the first kernel); one row of 1M slots, 95 %
-// full, 16 heads on 2: 174 us, 6.0 TB/s.
+// call, 5.9 TB/s (104 us and 6.2 TB/s the first kernel); one row of 1M slots, 95 %
+// full, 16 heads on 2: 171 us, 6.1 TB/s.
 //
 // The new tokens' k and v are read from the call's inputs, never from the
 // cache; the CTA that has their keys writes them there.  No CTA reads a slot

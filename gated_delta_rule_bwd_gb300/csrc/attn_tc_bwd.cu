@@ -342,7 +342,7 @@ attn_tc_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       schedule(
           slots, live,
           [&](int cta, int(&j)[12]) {
-            // the tiles that the most queries see first
+            // the tiles that the most queries see first (packed: of a sequence)
             const int u = cta / a.Hkv;
             AttnTile t;
             if (!a.sq.get<true>(a.tiles ? batch_slot(u, a.sq.B, a.tiles, a.group, false) : u, 128, t)) return false;
@@ -660,7 +660,7 @@ attn_tc_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       schedule(
           slots, live,
           [&](int cta, int(&j)[12]) {
-            // the tiles with the most keys first
+            // the tiles with the most keys first (packed: of a sequence, the last sequence first)
             const int u = cta / a.H;
             const int slot = a.tiles ? batch_slot(u, a.sq.B, a.tiles, a.group, true) : ctas / a.H - 1 - u;
             AttnTile t;

@@ -81,7 +81,7 @@ enum { kHead, kPart, kQ0, kK0, kLk, kFirst, kNr, kB, kN0, kN1, kFix, kValid };
 // 128-row tile sees; kFix: the last one holds rows of the next packed sequence.
 
 __device__ __forceinline__ bool decode(const Args& a, int cta, int ctas, int (&j)[12]) {
-  // the tiles with the most keys first
+  // the tiles with the most keys first (packed: of a sequence, the last sequence first)
   const int part = cta % a.parts, u = cta / a.parts / a.H;
   const int slot = a.tiles ? batch_slot(u, a.sq.B, a.tiles, a.group, true) : ctas / a.parts / a.H - 1 - u;
   AttnTile t;
