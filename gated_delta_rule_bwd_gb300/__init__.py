@@ -669,6 +669,8 @@ def _attn_tensor(name, x, dtype, device):
         raise GdnError(f"{name}: expected a [B, T, H, D] {dtype} tensor on {device}, got "
                        f"{tuple(x.shape)} {x.dtype} on {x.device}")
     st = x.stride()
+    if x.shape[3] == 0:
+        raise GdnError(f"{name}: a head has no values (D = 0)")
     if st[3] != 1 and x.shape[3] > 1:
         raise GdnError(f"{name}: the D values of a head must be contiguous")
     return st[:3]

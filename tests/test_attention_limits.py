@@ -80,3 +80,12 @@ def test_decode_of_key_heads_without_query_heads_is_refused():
     call = lambda Hkv: gdn.lib().gdn_attn_decode(  # noqa: E731
         ctypes.byref(s(Hkv)), *[fake] * 6, 0.5, fake, None, 0, None)
     assert call(2) == -2 and call(0) == 0
+
+
+@gpu
+def test_heads_without_values_are_refused():
+    x, lens = torch.zeros(1, 4, 2, 0, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(gdn.GdnError, match="D = 0"):
+        gdn.attn_fwd(x, x, x)
+    with pytest.raises(gdn.GdnError, match="D = 0"):
+        gdn.attn_decode(x, x, x, x, x, lens)
