@@ -442,7 +442,9 @@ GDN_API int gdn_attn_bwd(const gdn_attn_shape* shape, const void* q, const void*
  * changed; the caller adds T.  Everything is contiguous but the caches, whose
  * batch, token and head strides (in elements) the shape gives.  A row whose
  * lens[b] is negative or leaves less than T free slots gets o = 0 and no cache
- * write, and gdn_device_status() returns GDN_ERR_SEQLENS.
+ * write, and gdn_device_status() returns GDN_ERR_SEQLENS.  A NaN in a row of q,
+ * or in the k of a slot that it sees, makes that row NaN; a NaN or infinity in
+ * a new token's v may also reach the row's earlier new tokens of this call.
  *
  * The H / Hkv heads that share a key head and the T tokens are the rows of
  * one pass over the used part of the caches (per 32 of them; 8 for fp32 or
@@ -492,7 +494,8 @@ GDN_API int gdn_last_cuda_error(void);
 
 /* Reads and clears the device status word of the current device: GDN_OK,
  * GDN_ERR_DEVICE_TIMEOUT, GDN_ERR_SEQLENS, or GDN_ERR_ALIGN (an attention
- * kernel found its shared memory unaligned and did nothing).  Synchronises the
+ * kernel found its shared memory unaligned and did nothing); GDN_ERR_ARG only
+ * from gdn_attn_wait_selftest.  Synchronises the
  * current device.  Returns GDN_ERR_CUDA if the read itself fails. */
 GDN_API int gdn_device_status(void);
 
