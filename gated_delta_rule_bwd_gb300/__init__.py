@@ -18,6 +18,9 @@ L2 norm for q and k) and ``gated_rmsnorm_fwd`` / ``gated_rmsnorm_bwd``.  The
 softmax attention layers between the mixers: ``attn_fwd`` / ``attn_bwd`` (causal,
 grouped heads, packed sequences), ``attn_decode`` (a few tokens against a cache
 that the call extends), and the pre-norm ``layer_norm_fwd`` / ``layer_norm_bwd``.
+In front of them ``qk_norm_rope_fwd`` / ``qk_norm_rope_bwd`` (norm of the query and
+key heads and rotation by position), and for serving from pages of 16-bit, fp32 or
+4-bit keys and values ``kv_append``, ``attn_paged`` and ``kv_gather``.
 Token tensors are ``[B, T, H, D]`` (fp32 or bf16, all the same dtype), ``g``
 is ``[B, T, H]`` (GDN) or ``[B, T, H, dk]`` (KDA) fp32, ``beta`` ``[B, T, H]``
 fp32, states ``[B, H, dk, dv]`` fp32.
@@ -27,6 +30,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple, Optional
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -67,6 +71,35 @@ class AttnDecodeShape(ctypes.Structure):
                 ("vc_stride", ctypes.c_longlong * 3)]
 
 
+class QkRopeShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int),
+                ("Hkv", ctypes.c_int), ("D", ctypes.c_int), ("R", ctypes.c_int),
+                ("P", ctypes.c_int), ("interleaved", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("q_stride", ctypes.c_longlong * 3), ("k_stride", ctypes.c_longlong * 3)]
+
+
+class PagedCacheDesc(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int), ("page", ctypes.c_int), ("Hkv", ctypes.c_int),
+                ("D", ctypes.c_int), ("format", ctypes.c_int), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("k_stride", ctypes.c_longlong * 3), ("v_stride", ctypes.c_longlong * 3),
+                ("k_scale_stride", ctypes.c_longlong * 3), ("v_scale_stride", ctypes.c_longlong * 3)]
+
+
+class KvAppendShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int), ("R", ctypes.c_int),
+                ("P", ctypes.c_int), ("interleaved", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("rows", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("table_stride", ctypes.c_longlong), ("q_stride", ctypes.c_longlong * 3),
+                ("k_stride", ctypes.c_longlong * 3), ("v_stride", ctypes.c_longlong * 3)]
+
+
+class AttnPagedShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("table_stride", ctypes.c_longlong)]
+
+
 class GdnError(RuntimeError):
     pass
 
@@ -89,6 +122,8 @@ EXPORTS = ("gdn_fwd", "gdn_bwd", "kda_fwd", "kda_bwd", "gdn_fwd_workspace", "kda
            "gdn_attn_fwd_workspace", "gdn_attn_fwd", "gdn_attn_bwd_workspace", "gdn_attn_bwd",
            "gdn_attn_decode_workspace", "gdn_attn_decode",
            "gdn_layer_norm_fwd", "gdn_layer_norm_bwd", "gdn_layer_norm_bwd_workspace",
+           "gdn_qk_norm_rope_fwd", "gdn_qk_norm_rope_bwd", "gdn_qk_norm_rope_bwd_workspace",
+           "gdn_kv_append", "gdn_kv_gather", "gdn_attn_paged", "gdn_attn_paged_workspace",
            "gdn_profile_begin", "gdn_profile_end", "gdn_profile_read", "gdn_kernel_name")
 
 
@@ -173,6 +208,22 @@ def lib():
             L.gdn_layer_norm_bwd_workspace.restype = sz
             L.gdn_layer_norm_bwd.argtypes = [ns] + [vp] * 9 + [sz, vp]
             L.gdn_layer_norm_bwd.restype = ctypes.c_int
+            qs, pc, ks, ps = (ctypes.POINTER(QkRopeShape), ctypes.POINTER(PagedCacheDesc),
+                              ctypes.POINTER(KvAppendShape), ctypes.POINTER(AttnPagedShape))
+            L.gdn_qk_norm_rope_fwd.argtypes = [qs] + [vp] * 4 + [f32] + [vp] * 6
+            L.gdn_qk_norm_rope_fwd.restype = i32
+            L.gdn_qk_norm_rope_bwd_workspace.argtypes = [qs]
+            L.gdn_qk_norm_rope_bwd_workspace.restype = sz
+            L.gdn_qk_norm_rope_bwd.argtypes = [qs] + [vp] * 4 + [f32] + [vp] * 10 + [sz, vp]
+            L.gdn_qk_norm_rope_bwd.restype = i32
+            L.gdn_kv_append.argtypes = [ks, pc] + [vp] * 10
+            L.gdn_kv_append.restype = i32
+            L.gdn_kv_gather.argtypes = [pc, vp, i32, i32, ctypes.c_longlong, vp, i32, i32, vp, vp, vp]
+            L.gdn_kv_gather.restype = i32
+            L.gdn_attn_paged_workspace.argtypes = [ps, pc]
+            L.gdn_attn_paged_workspace.restype = sz
+            L.gdn_attn_paged.argtypes = [ps, pc, vp, vp, vp, f32, vp, vp, sz, vp]
+            L.gdn_attn_paged.restype = i32
             L.gdn_profile_begin.argtypes = [ctypes.c_int]
             L.gdn_profile_begin.restype = ctypes.c_int
             L.gdn_profile_end.argtypes = []
@@ -843,6 +894,285 @@ def layer_norm_bwd(x, weight, mean, rstd, dy, workspace=None):
     return dx, dweight, dbias
 
 
+# ---------------------------------------------------------------- positions and pages
+
+def rope_table(n, R, base=10000.0, device="cuda"):
+    """``(cos, sin)`` fp32 ``[n, R / 2]`` of the angles ``position * base ** (-2 i / R)``,
+    made in 64 bits (an fp32 angle of a far position is off by more than its cosine
+    may be).  Any other tables of that shape serve as well."""
+    if R < 0 or R % 2:
+        raise GdnError(f"R = {R}: an even number of rotated values")
+    f = float(base) ** (-torch.arange(0, R, 2, dtype=torch.float64, device=device) / max(R, 1))
+    angle = torch.arange(n, dtype=torch.float64, device=device)[:, None] * f
+    return angle.cos().float(), angle.sin().float()
+
+
+def _f32(name, x, device, shape):
+    if not _same(x, torch.float32, device, shape):
+        _nb_check(name, x, torch.float32, device, shape)
+
+
+def _tables(cos, sin, D, device):
+    """R and P of the tables (0, 0: none)."""
+    if cos is None and sin is None:
+        return 0, 0
+    if cos is None or sin is None or cos.dim() != 2:
+        raise GdnError("cos and sin must be fp32 tables [positions, R / 2], both or neither")
+    _f32("cos", cos, device, cos.shape)
+    _f32("sin", sin, device, cos.shape)
+    P, half = cos.shape
+    if not 0 < 2 * half <= D:
+        raise GdnError(f"tables of {half} pairs for heads of {D} values")
+    return 2 * half, P
+
+
+def _qk_args(q, k, q_weight, k_weight, cos, sin, positions, interleaved):
+    if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPES:
+        raise GdnError("q must be a fp32 or bf16 tensor")
+    dtype, device = q.dtype, q.device
+    qs, ks = _attn_tensor("q", q, dtype, device), _attn_tensor("k", k, dtype, device)
+    B, T, H, D = q.shape
+    if k.shape[0] != B or k.shape[1] != T or k.shape[3] != D:
+        raise GdnError(f"k: expected [{B}, {T}, Hkv, {D}], got {tuple(k.shape)}")
+    if (q_weight is None) != (k_weight is None):
+        raise GdnError("q_weight and k_weight: both or neither")
+    if q_weight is not None:
+        _f32("q_weight", q_weight, device, (D,))
+        _f32("k_weight", k_weight, device, (D,))
+    R, P = _tables(cos, sin, D, device)
+    if R == 0 and q_weight is None:
+        raise GdnError("neither weights nor tables: nothing to do")
+    if positions is not None:
+        if R == 0:
+            raise GdnError("positions need cos and sin")
+        if not _same(positions, torch.int32, device, (B, T)):
+            _nb_check("positions", positions, torch.int32, device, (B, T))
+    return QkRopeShape(B, T, H, k.shape[2], D, R, P, int(bool(interleaved)), _DTYPES[dtype], qs, ks)
+
+
+def qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None,
+                     interleaved=False, eps=NORM_EPS):
+    """RMS norm of every head of ``q [B, T, H, D]`` and ``k [B, T, Hkv, D]`` (views of
+    one projection are taken as they are) with weights ``[D]`` fp32, then rotation of
+    its first R values by position: ``cos``, ``sin`` ``[P, R / 2]`` fp32 (see
+    ``rope_table``), ``positions`` int32 ``[B, T]`` (default: token t has position t).
+    Pairs are ``(i, i + R / 2)``, or ``(2 i, 2 i + 1)`` with ``interleaved``.  Weights
+    or tables may be left out.  Returns ``(qo, ko)``, contiguous."""
+    s = _qk_args(q, k, q_weight, k_weight, cos, sin, positions, interleaved)
+    device = q.device
+    qo = torch.empty(q.shape, dtype=q.dtype, device=device)
+    ko = torch.empty(k.shape, dtype=q.dtype, device=device)
+    _call(lib().gdn_qk_norm_rope_fwd(ctypes.byref(s), q.data_ptr(), k.data_ptr(), _addr(q_weight),
+                                     _addr(k_weight), float(eps), _addr(cos), _addr(sin),
+                                     _addr(positions), qo.data_ptr(), ko.data_ptr(),
+                                     _raw_stream(device)))
+    return qo, ko
+
+
+def qk_norm_rope_bwd(q, k, dqo, dko, q_weight=None, k_weight=None, cos=None, sin=None,
+                     positions=None, interleaved=False, eps=NORM_EPS, workspace=None):
+    """Gradients of ``qk_norm_rope_fwd`` from its inputs and those of its outputs:
+    returns ``(dq, dk, dq_weight, dk_weight)`` (contiguous; the last two fp32,
+    reproducible sums over all tokens and heads, None without weights)."""
+    s = _qk_args(q, k, q_weight, k_weight, cos, sin, positions, interleaved)
+    dtype, device, L, sp = q.dtype, q.device, lib(), ctypes.byref(s)
+    if not (_same(dqo, dtype, device, q.shape) and _same(dko, dtype, device, k.shape)):
+        _nb_check("dqo", dqo, dtype, device, q.shape)
+        _nb_check("dko", dko, dtype, device, k.shape)
+    dq = torch.empty(q.shape, dtype=dtype, device=device)
+    dk = torch.empty(k.shape, dtype=dtype, device=device)
+    dwq = dwk = ws = None
+    need = 0
+    if q_weight is not None:
+        dwq, dwk = torch.empty_like(q_weight), torch.empty_like(k_weight)
+        need = L.gdn_qk_norm_rope_bwd_workspace(sp)
+        ws = _workspace(need, workspace, device)
+    _call(L.gdn_qk_norm_rope_bwd(sp, q.data_ptr(), k.data_ptr(), _addr(q_weight), _addr(k_weight),
+                                 float(eps), _addr(cos), _addr(sin), _addr(positions),
+                                 dqo.data_ptr(), dko.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+                                 _addr(dwq), _addr(dwk), _addr(ws), need, _raw_stream(device)))
+    return dq, dk, dwq, dwk
+
+
+class PagedCache(NamedTuple):
+    """Pages of keys and values: ``k``, ``v`` ``[pages, page, Hkv, D]`` in fp32 or bf16,
+    or in 4 bits, codes ``[pages, page, Hkv, D / 2]`` uint8 and the steps of every 32
+    values ``[pages, page, Hkv, D / 32]`` bf16 (see gdn.h).  The calls take any tuple of
+    these two or four tensors, with any strides between tokens, heads and pages."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: Optional[torch.Tensor] = None
+    v_scale: Optional[torch.Tensor] = None
+
+
+def new_paged_cache(pages, page, Hkv, D, dtype=torch.bfloat16, bits=None, device="cuda"):
+    """An empty cache of ``pages`` pages of ``page`` tokens (a power of two), in
+    ``dtype`` or with ``bits=4`` in 4 bits.  A page's tokens of one head lie together
+    in memory, which is how attention reads them."""
+    if bits not in (None, 4):
+        raise GdnError(f"bits = {bits}: None (the dtype's own) or 4")
+    if page < 1 or page & (page - 1):
+        raise GdnError(f"a page of {page} tokens: not a power of two")
+    if dtype not in _DTYPES:
+        raise GdnError(f"unsupported dtype {dtype}")
+
+    def make(n, dt):
+        return torch.zeros(pages, Hkv, page, n, dtype=dt, device=device).transpose(1, 2)
+    if bits is None:
+        return PagedCache(make(D, dtype), make(D, dtype))
+    if D % 32:
+        raise GdnError(f"4 bits: heads of {D} values are no multiple of 32")
+    return PagedCache(make(D // 2, torch.uint8), make(D // 2, torch.uint8),
+                      make(D // 32, torch.bfloat16), make(D // 32, torch.bfloat16))
+
+
+def _cache_args(cache, device):
+    """The ABI's view of a cache."""
+    cache = tuple(x for x in cache if x is not None)
+    if len(cache) not in (2, 4) or not all(isinstance(x, torch.Tensor) and x.dim() == 4
+                                           and x.device == device for x in cache):
+        raise GdnError(f"the cache must be (k, v) or (k, v, k_scale, v_scale), [pages, page, Hkv, .] "
+                       f"tensors on {device}")
+    k, v = cache[0], cache[1]
+    shape = k.shape
+    if v.shape != shape or v.dtype is not k.dtype:
+        raise GdnError(f"the cache's k and v differ: {tuple(shape)} {k.dtype}, {tuple(v.shape)} {v.dtype}")
+    kst, vst = k.stride(), v.stride()
+    pages, page, Hkv, D = shape
+    if D == 0:
+        raise GdnError("the cache's heads have no values (D = 0)")
+    if (kst[3] != 1 or vst[3] != 1) and D > 1:
+        raise GdnError("the values of a head must be contiguous in the cache")
+    if len(cache) == 2:
+        if k.dtype not in _DTYPES:
+            raise GdnError(f"a cache of {k.dtype}: fp32, bf16, or uint8 codes with scales")
+        return PagedCacheDesc(pages, page, Hkv, D, _DTYPES[k.dtype], k.data_ptr(), v.data_ptr(),
+                              None, None, kst[:3], vst[:3])
+    ks, vs = cache[2], cache[3]
+    steps = (pages, page, Hkv, D // 16)
+    if (k.dtype is not torch.uint8 or D % 16 or ks.dtype is not torch.bfloat16
+            or vs.dtype is not torch.bfloat16 or ks.shape != steps or vs.shape != steps):
+        raise GdnError(f"a 4-bit cache: uint8 codes [pages, page, Hkv, D / 2] and bf16 scales [pages, page, "
+                       f"Hkv, D / 32], D a multiple of 32, got {[(tuple(x.shape), x.dtype) for x in cache]}")
+    kss, vss = ks.stride(), vs.stride()
+    if (kss[3] != 1 or vss[3] != 1) and steps[3] > 1:
+        raise GdnError("the scales of a head must be contiguous in the cache")
+    return PagedCacheDesc(pages, page, Hkv, 2 * D, 2, k.data_ptr(), v.data_ptr(), ks.data_ptr(),
+                          vs.data_ptr(), kst[:3], vst[:3], kss[:3], vss[:3])
+
+
+def _block_table(table, rows, device):
+    if (not isinstance(table, torch.Tensor) or table.dtype is not torch.int32 or table.dim() != 2
+            or table.device != device or (rows is not None and table.shape[0] != rows)
+            or (table.shape[1] > 1 and table.stride(1) != 1)):
+        raise GdnError(f"block_table must be int32 [{'rows' if rows is None else rows}, max_pages] on "
+                       f"{device}, the entries of a row contiguous")
+    return table.shape[1], table.stride(0)
+
+
+def kv_append(k, v, cache, block_table, lens, q=None, cos=None, sin=None, interleaved=False,
+              cu_seqlens=None):
+    """Stores new keys and values ``[B, T, Hkv, D]`` in a paged cache: token t of row b
+    in slot ``lens[b] + t`` (``lens`` int32, on the device, left to the caller), which
+    is place ``slot % page`` of page ``block_table[b, slot // page]`` (int32).  With
+    ``cos``, ``sin`` (see ``qk_norm_rope_fwd``) k is rotated by its slot on the way,
+    and so is ``q [B, T, H, D]``, if given; returns the rotated q, or None.
+
+    Packed new tokens: ``k``, ``v``, ``q`` ``[1, T, ...]`` and ``cu_seqlens`` int32
+    ``[rows + 1]``; tokens behind ``cu_seqlens[-1]`` belong to no row.  A row whose
+    ``lens`` is negative is not in use: its tokens are not stored, and their q is 0."""
+    if not isinstance(k, torch.Tensor) or k.dtype not in _DTYPES:
+        raise GdnError("k must be a fp32 or bf16 tensor")
+    dtype, device = k.dtype, k.device
+    kst, vst = _attn_tensor("k", k, dtype, device), _attn_tensor("v", v, dtype, device)
+    B, T, Hkv, D = k.shape
+    if v.shape != k.shape:
+        raise GdnError(f"k and v differ: {tuple(k.shape)}, {tuple(v.shape)}")
+    H, qst = 0, (0, 0, 0)
+    if q is not None:
+        qst = _attn_tensor("q", q, dtype, device)
+        H = q.shape[2]
+        if q.shape[0] != B or q.shape[1] != T or q.shape[3] != D:
+            raise GdnError(f"q: expected [{B}, {T}, H, {D}], got {tuple(q.shape)}")
+    c = _cache_args(cache, device)
+    if c.Hkv != Hkv or c.D != D or c.format not in (2, _DTYPES[dtype]):
+        raise GdnError(f"the cache holds {c.Hkv} heads of {c.D} values ({cache[0].dtype}), k is "
+                       f"{tuple(k.shape)} {dtype}")
+    R, P = _tables(cos, sin, D, device)
+    rows = B
+    if cu_seqlens is not None:
+        _attn_cu("cu_seqlens", cu_seqlens, device)
+        if B != 1:
+            raise GdnError("packed sequences: the token tensors must be [1, T, H, D]")
+        rows = cu_seqlens.numel() - 1
+    if not _same(lens, torch.int32, device, (rows,)):
+        _nb_check("lens", lens, torch.int32, device, (rows,))
+    most, stride = _block_table(block_table, rows, device)
+    s = KvAppendShape(B, T, H, R, P, int(bool(interleaved)), _DTYPES[dtype], rows, most, stride, qst,
+                      kst, vst)
+    qo = None if q is None else torch.empty(q.shape, dtype=dtype, device=device)
+    _call(lib().gdn_kv_append(ctypes.byref(s), ctypes.byref(c), k.data_ptr(), v.data_ptr(), _addr(q),
+                              _addr(cos), _addr(sin), block_table.data_ptr(), lens.data_ptr(),
+                              _addr(cu_seqlens), _addr(qo), _raw_stream(device)))
+    return qo
+
+
+def kv_gather(cache, block_table, cu_seqlens, total, dtype=None):
+    """Reads rows of a paged cache back as packed ``k``, ``v`` ``[1, total, Hkv, D]``,
+    as ``attn_fwd`` takes them with ``cu_seqlens_k``: the first ``cu_seqlens[b + 1] -
+    cu_seqlens[b]`` tokens of row b.  ``total`` is ``cu_seqlens[-1]``, known to the
+    host.  ``dtype`` is the cache's own; a 4-bit cache gives bf16 (exact) or fp32."""
+    device = cache[0].device
+    if device.type != "cuda":
+        raise GdnError("the cache must be CUDA tensors (the library has no CPU path)")
+    c = _cache_args(cache, device)
+    if dtype is None:
+        dtype = torch.bfloat16 if c.format == 2 else cache[0].dtype
+    if dtype not in _DTYPES or c.format not in (2, _DTYPES[dtype]):
+        raise GdnError(f"a cache of {cache[0].dtype} does not give {dtype}")
+    _attn_cu("cu_seqlens", cu_seqlens, device)
+    rows = cu_seqlens.numel() - 1
+    most, stride = _block_table(block_table, rows, device)
+    k = torch.empty((1, total, c.Hkv, c.D), dtype=dtype, device=device)
+    v = torch.empty_like(k)
+    _call(lib().gdn_kv_gather(ctypes.byref(c), block_table.data_ptr(), rows, most, stride,
+                              cu_seqlens.data_ptr(), total, _DTYPES[dtype], k.data_ptr(),
+                              v.data_ptr(), _raw_stream(device)))
+    return k, v
+
+
+def attn_paged(q, cache, block_table, lens, scale=None, workspace=None):
+    """Attention of T new tokens per row, ``q [B, T, H, D]``, against a paged cache
+    that holds them already (``kv_append`` with the same ``lens``, the tokens before
+    the new ones): token t sees the slots up to ``lens[b] + t``.  ``scale`` defaults
+    to ``D ** -0.5``.  A row whose ``lens`` is negative is not in use and gets 0.
+    Returns ``o [B, T, H, D]``."""
+    if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPES:
+        raise GdnError("q must be a fp32 or bf16 tensor")
+    dtype, device = q.dtype, q.device
+    _attn_tensor("q", q, dtype, device)
+    if not q.is_contiguous():
+        raise GdnError("q must be contiguous")
+    B, T, H, D = q.shape
+    c = _cache_args(cache, device)
+    if c.D != D or c.format not in (2, _DTYPES[dtype]):
+        raise GdnError(f"the cache holds heads of {c.D} values ({cache[0].dtype}), q is {tuple(q.shape)} {dtype}")
+    if H > 0 and (c.Hkv == 0 or H % c.Hkv):
+        raise GdnError(f"{c.Hkv} key heads do not divide the {H} query heads")
+    if not _same(lens, torch.int32, device, (B,)):
+        _nb_check("lens", lens, torch.int32, device, (B,))
+    most, stride = _block_table(block_table, B, device)
+    s = AttnPagedShape(B, T, H, _DTYPES[dtype], most, stride)
+    L, sp, cp = lib(), ctypes.byref(s), ctypes.byref(c)
+    o = torch.empty_like(q)
+    need = L.gdn_attn_paged_workspace(sp, cp)
+    ws = _workspace(need, workspace, device) if need else None
+    _call(L.gdn_attn_paged(sp, cp, q.data_ptr(), block_table.data_ptr(), lens.data_ptr(),
+                           D ** -0.5 if scale is None else float(scale), o.data_ptr(), _addr(ws), need,
+                           _raw_stream(device)))
+    return o
+
+
 class Attention(torch.autograd.Function):
     """Autograd wrapper of ``attn_fwd`` / ``attn_bwd``."""
 
@@ -863,6 +1193,29 @@ class Attention(torch.autograd.Function):
 def attention(q, k, v, cu_seqlens=None, cu_seqlens_k=None, scale=None):
     """Differentiable ``attn_fwd``: returns ``o``."""
     return Attention.apply(q, k, v, cu_seqlens, cu_seqlens_k, scale)
+
+
+class QkNormRope(torch.autograd.Function):
+    """Autograd wrapper of ``qk_norm_rope_fwd`` / ``qk_norm_rope_bwd``."""
+
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, cos, sin, positions, interleaved, eps):
+        ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin, positions)
+        ctx.interleaved, ctx.eps = interleaved, eps
+        return qk_norm_rope_fwd(q, k, q_weight, k_weight, cos, sin, positions, interleaved, eps)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dqo, dko):
+        q, k, wq, wk, cos, sin, positions = ctx.saved_tensors
+        return (*qk_norm_rope_bwd(q, k, _dense(dqo), _dense(dko), wq, wk, cos, sin, positions,
+                                  ctx.interleaved, ctx.eps), None, None, None, None, None)
+
+
+def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None,
+                 interleaved=False, eps=NORM_EPS):
+    """Differentiable ``qk_norm_rope_fwd`` (in q, k and the weights): returns ``(qo, ko)``."""
+    return QkNormRope.apply(q, k, q_weight, k_weight, cos, sin, positions, interleaved, eps)
 
 
 class LayerNorm(torch.autograd.Function):

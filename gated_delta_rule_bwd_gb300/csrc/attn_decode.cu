@@ -8,15 +8,8 @@
 // rows of one product with the cache.  Bound by the cache's bytes: 2 Hkv D
 // (old + T) elements per row, read once per block of 16 or 32 rows.
 //
-// Work split.  The (row b, key head, unit of 64 keys) triples of the whole
-// batch, in that order, are dealt out evenly: CTA c takes the units [c U / N,
-// (c + 1) U / N), whatever the rows' lengths are.  A CTA thus walks segments:
-// runs of units of one (b, key head).  A segment that covers all of a row's
-// keys writes the output; of the others each CTA has at most one that goes on
-// from the CTA before it (slot 2 c of the workspace) and one that starts a row
-// that the next CTA goes on with (slot 2 c + 1).  A second kernel joins the
-// slots of each such row: m = max m_p, o = sum exp(m_p - m) acc_p / sum
-// exp(m_p - m) l_p.  No atomics: the order of every sum is fixed.
+// Work split: the batch's units of 64 keys evenly over the CTAs, and a second
+// kernel that joins what is split (attn_split.cuh).
 //
 // Measured: 64 rows of 1638 to 8191 tokens, 16 heads on 4, D 128, bf16: 110 us the
 // call, 5.9 TB/s (104 us and 6.2 TB/s the first kernel); one row of 1M slots, 95 %
@@ -30,7 +23,7 @@
 
 #include <algorithm>
 
-#include "attn_tc.cuh"
+#include "attn_split.cuh"
 
 namespace gdn {
 
@@ -41,10 +34,7 @@ cudaError_t attn_decode_read_and_clear_status(int* status) {
 namespace {
 
 using namespace tc;
-
-constexpr int kUnit = 64;      // keys per unit
-constexpr int kMinUnits = 2;   // per CTA: fewer CTAs rather than shorter pieces
-constexpr int kThreads = 128;
+using namespace split;
 
 struct Args {
   int B, T, S, H, Hkv, D, G, R;  // R = G T rows per key head
@@ -55,109 +45,24 @@ struct Args {
   void *kc, *vc;
   const int* lens;
   void* o;
-  int4* starts;      // [grid.y][grid.x]: the row that CTA c starts and does not end (x = b or -1, y = hk, z = last CTA)
-  float *ml, *acc;   // [grid.y][2 grid.x][rows][2] (maximum in exponents, sum) and [..][D]
-};
-
-// Row b's tokens after the call (0: bad length, nothing is done).
-__device__ __forceinline__ int row_keys(const Args& a, int b) {
-  const int n = a.lens[b];
-  return n < 0 || n > a.S - a.T ? 0 : n + a.T;
-}
-__device__ __forceinline__ int row_units(const Args& a, int b) { return (row_keys(a, b) + kUnit - 1) / kUnit; }
-
-// One CTA's walk through its units.
-struct Walk {
-  long u, end, U, base;  // next unit, end, all units, first unit of row b
-  int N, b, units;       // CTAs that share the work; row and its units
-  int hk, keys, k0, k1;  // the segment: key head, the row's keys, keys [k0, k1)
-  bool starts, whole;    // it begins its row; it is all of it
-  long row0;             // first unit of (b, hk)
-
-  // All 128 threads; false if the CTA has no units.
-  __device__ bool init(const Args& a) {
-    __shared__ long sums[kThreads + 1];
-    __shared__ long at[2];
-    const int per = (a.B + kThreads - 1) / kThreads, b0 = min(a.B, (int)threadIdx.x * per), b1 = min(a.B, b0 + per);
-    long mine = 0;
-    for (int i = b0; i < b1; ++i) mine += (long)row_units(a, i) * a.Hkv;
-    sums[threadIdx.x + 1] = mine;
-    __syncthreads();
-    if (threadIdx.x < 32) {  // prefix sums, four per lane
-      const int l = threadIdx.x;
-      long s[4], x = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] = x += sums[4 * l + i + 1];
-      long y = x;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long z = __shfl_up_sync(0xffffffffu, y, o);
-        if (l >= o) y += z;
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sums[4 * l + i + 1] = y - x + s[i];
-      if (l == 0) sums[0] = 0;
-    }
-    __syncthreads();
-    U = sums[kThreads];
-    N = (int)min((long)gridDim.x, max(1L, U / kMinUnits));
-    u = (long)blockIdx.x * U / N, end = ((long)blockIdx.x + 1) * U / N;
-    if ((int)blockIdx.x >= N || u == end) return false;
-    if (u >= sums[threadIdx.x] && u < sums[threadIdx.x + 1]) {
-      long s = sums[threadIdx.x];
-      int i = b0;
-      for (;; ++i) {
-        const long n = (long)row_units(a, i) * a.Hkv;
-        if (u < s + n) break;
-        s += n;
-      }
-      at[0] = i, at[1] = s;
-    }
-    __syncthreads();
-    b = (int)at[0], base = at[1];
-    units = row_units(a, b);
-    return true;
+  int4* starts;
+  float *ml, *acc;
+  // Row b's tokens after the call (0: bad length, nothing is done).
+  __device__ __forceinline__ int keys(int b) const {
+    const int n = lens[b];
+    return n < 0 || n > S - T ? 0 : n + T;
   }
-  __device__ bool segment(const Args& a) {
-    if (u == end) return false;
-    while (u >= base + (long)units * a.Hkv) {
-      base += (long)units * a.Hkv;
-      units = row_units(a, ++b);
-    }
-    hk = (int)((u - base) / units);
-    const int unit = (int)((u - base) % units), n = (int)min(end - u, (long)(units - unit));
-    row0 = u - unit;
-    keys = row_keys(a, b);
-    k0 = unit * kUnit, k1 = min(keys, (unit + n) * kUnit);
-    starts = unit == 0, whole = starts && n == units;
-    u += n;
-    return true;
-  }
-  // the CTA that has unit x
-  __device__ int owner(long x) const { return (int)(((x + 1) * N - 1) / U); }
 };
 
 // Rows with a bad length: o = 0, and the status word says so.
 template <typename T>
 __device__ void bad_rows(const Args& a) {
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-    if (row_keys(a, b) || blockIdx.y) continue;
+    if (a.keys(b) || blockIdx.y) continue;
     const long long n = (long long)a.T * a.H * a.D;
     for (long long i = threadIdx.x; i < n; i += kThreads) static_cast<T*>(a.o)[b * n + i] = from_f32<T>(0.f);
     if (threadIdx.x == 0) atomicExch(&g_file_status, GDN_ERR_SEQLENS);
   }
-}
-
-// Workspace slot of this CTA's piece, and the note for the joining kernel.
-__device__ __forceinline__ long slot_of(const Args& a, const Walk& w) {
-  if (w.starts && threadIdx.x == 0)
-    a.starts[(long)blockIdx.y * gridDim.x + blockIdx.x] = make_int4(w.b, w.hk, w.owner(w.row0 + w.units - 1), 0);
-  return (long)blockIdx.y * 2 * gridDim.x + 2 * blockIdx.x + (w.starts ? 1 : 0);
-}
-
-// Element offset of row r (token r / G, head hk G + r % G) in q and o.
-__device__ __forceinline__ long long row_at(const Args& a, int b, int hk, int r) {
-  return (((long long)b * a.T + r / a.G) * a.H + hk * a.G + r % a.G) * a.D;
 }
 
 // ---------------------------------------------------------------- CUDA cores
@@ -175,7 +80,7 @@ __global__ void __launch_bounds__(kThreads) attn_decode_simt_kernel(Args a) {
   grid_dep_launch();
   bad_rows<T>(a);
   if (threadIdx.x == 0) a.starts[(long)blockIdx.y * gridDim.x + blockIdx.x].x = -1;
-  Walk wk;
+  Walk<Args> wk;
   if (!wk.init(a)) return;
   while (wk.segment(a)) {
     const int b = wk.b, hk = wk.hk, old = wk.keys - a.T;
@@ -332,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_mma_kernel(Args a) {
   grid_dep_launch();
   bad_rows<__nv_bfloat16>(a);
   if (threadIdx.x == 0) a.starts[(long)blockIdx.y * gridDim.x + blockIdx.x].x = -1;
-  Walk wk;
+  Walk<Args> wk;
   if (!wk.init(a)) return;
   while (wk.segment(a)) {
     const int b = wk.b, hk = wk.hk, old = wk.keys - a.T, k1 = wk.k1;
@@ -535,49 +440,6 @@ __global__ void __launch_bounds__(kThreads, 2) attn_decode_mma_kernel(Args a) {
   }
 }
 
-// ---------------------------------------------------------------- joining the pieces
-
-// One CTA of 128 threads per (row of a block, CTA that starts a row it does
-// not end): slots 2 c + 1, 2 (c + 1), 2 (c + 2), ... of the row.
-constexpr int kMaxCtas = 2048;
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) attn_combine_kernel(Args a, int ctas, int rows) {
-  __shared__ float f[kMaxCtas];
-  __shared__ float red[8];
-  grid_dep_wait();
-  const int c0 = blockIdx.x, r = blockIdx.z * rows + blockIdx.y, d = threadIdx.x;
-  const int4 st = a.starts[(long)blockIdx.z * ctas + c0];
-  if (st.x < 0 || r >= a.R) return;
-  const int n = st.z - c0 + 1;
-  auto at = [&](int i) {
-    return ((long)blockIdx.z * 2 * ctas + (i ? 2 * (c0 + i) : 2 * c0 + 1)) * rows + blockIdx.y;
-  };
-  float m = -INFINITY;
-  for (int i = d; i < n; i += kThreads) m = fmaxf(m, a.ml[2 * at(i)]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((d & 31) == 0) red[d >> 5] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  float sum = 0.f;
-  for (int i = d; i < n; i += kThreads) {
-    const float mi = a.ml[2 * at(i)], e = mi == -INFINITY ? 0.f : exp2f(mi - m);
-    f[i] = e;
-    sum = fmaf(e, a.ml[2 * at(i) + 1], sum);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if ((d & 31) == 0) red[4 + (d >> 5)] = sum;
-  __syncthreads();
-  sum = red[4] + red[5] + red[6] + red[7];
-  if (d >= a.D) return;
-  float x = 0.f;
-#pragma unroll 8
-  for (int i = 0; i < n; ++i) x = fmaf(f[i], a.acc[at(i) * a.D + d], x);
-  static_cast<T*>(a.o)[row_at(a, st.x, st.y, r) + d] = from_f32<T>(sum == 0.f ? 0.f : x / sum);
-}
-
 // ---------------------------------------------------------------- host
 
 bool use_mma(const AttnDecodeProblem& p) {
@@ -594,28 +456,18 @@ struct Plan {
   int rows, blocks, ctas;  // query rows per CTA, row blocks (grid.y), CTAs that share the units (grid.x)
 };
 
-// At most as many CTAs as run at once (mma: two per SM; CUDA cores: four), and
-// no more than there are pieces of kMinUnits units in full caches.
+// Two CTAs per SM (mma), four (CUDA cores).
 Plan plan_of(const AttnDecodeProblem& p, bool mma) {
   Plan q;
   const int R = p.H / p.Hkv * p.T;
   q.mma = mma;
   q.rows = !mma ? kRows : R <= 16 ? 16 : 32;
   q.blocks = (R + q.rows - 1) / q.rows;
-  const long units = (long)p.B * p.Hkv * ((p.S + kUnit - 1) / kUnit);
-  const long most = std::max(1L, std::min(units / kMinUnits, (long)kMaxCtas));
-  const long fit = std::max(1L, (mma ? 2L : 4L) * sm_count() / q.blocks);
-  q.ctas = (int)std::min(most, fit);
+  q.ctas = ctas_for(p.B, p.Hkv, p.S, q.blocks, mma ? 2 : 4);
   return q;
 }
 
-size_t ws_starts(const Plan& q) { return align_up((size_t)q.blocks * q.ctas * sizeof(int4), 256); }
-size_t ws_ml(const Plan& q) {
-  return align_up((size_t)q.blocks * 2 * q.ctas * q.rows * 2 * sizeof(float), 256);
-}
-size_t ws_bytes(const Plan& q, int D) {
-  return ws_starts(q) + ws_ml(q) + (size_t)q.blocks * 2 * q.ctas * q.rows * D * sizeof(float);
-}
+size_t need(const Plan& q, int D) { return ws_bytes(q.blocks, q.ctas, q.rows, D); }
 
 template <typename T>
 cudaError_t run(const AttnDecodeProblem& p, cudaStream_t s) {
@@ -631,8 +483,8 @@ cudaError_t run(const AttnDecodeProblem& p, cudaStream_t s) {
   a.q = p.q, a.k = p.k, a.v = p.v, a.kc = p.kc, a.vc = p.vc, a.lens = p.lens, a.o = p.o;
   unsigned char* ws = static_cast<unsigned char*>(p.ws);
   a.starts = reinterpret_cast<int4*>(ws);
-  a.ml = reinterpret_cast<float*>(ws + ws_starts(pl));
-  a.acc = reinterpret_cast<float*>(ws + ws_starts(pl) + ws_ml(pl));
+  a.ml = reinterpret_cast<float*>(ws + ws_starts(pl.blocks, pl.ctas));
+  a.acc = reinterpret_cast<float*>(ws + ws_starts(pl.blocks, pl.ctas) + ws_ml(pl.blocks, pl.ctas, pl.rows));
   const dim3 grid(pl.ctas, pl.blocks);
   cudaError_t e = cudaSuccess;
   auto mma = [&](auto kernel, int smem) {
@@ -661,7 +513,7 @@ cudaError_t run(const AttnDecodeProblem& p, cudaStream_t s) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr, cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attn_combine_kernel<T>, a, pl.ctas, pl.rows);
+  e = cudaLaunchKernelEx(&cfg, attn_combine_kernel<T, Args>, a, pl.ctas, pl.rows);
   prof_after(s, kAttnCombine);
   return e;
 }
@@ -671,7 +523,7 @@ cudaError_t run(const AttnDecodeProblem& p, cudaStream_t s) {
 // The larger of the two kernels' needs: which one runs depends on the caches'
 // alignment, which a shape does not say.
 size_t attn_decode_workspace(const AttnDecodeProblem& p) {
-  return std::max(ws_bytes(plan_of(p, true), p.D), ws_bytes(plan_of(p, false), p.D));
+  return std::max(need(plan_of(p, true), p.D), need(plan_of(p, false), p.D));
 }
 
 cudaError_t attn_decode(const AttnDecodeProblem& p, cudaStream_t s) {

@@ -223,7 +223,9 @@ const char* kernel_name(int id) {
       "kda_tc_prep", "kda_tc_fwd", "kda_tc_states", "kda_tc_bwd", "seqlens_setup",
       "short_conv_fwd", "short_conv_bwd", "gated_rmsnorm_fwd", "gated_rmsnorm_bwd", "sum_partials",
       "attn_fwd", "attn_delta", "attn_bwd_kv", "attn_bwd_q", "attn_decode", "attn_combine",
-      "layer_norm_fwd", "layer_norm_bwd", "layer_norm_sum", "attn_bwd"};
+      "layer_norm_fwd", "layer_norm_bwd", "layer_norm_sum", "attn_bwd",
+      "qk_norm_rope_fwd", "qk_norm_rope_bwd", "qk_norm_rope_sum", "kv_append", "kv_gather", "attn_paged",
+      "attn_paged_combine"};
   return (id >= 0 && id < kNumKernelIds) ? names[id] : "unknown";
 }
 
@@ -583,6 +585,7 @@ const char* gdn_status_str(int status) {
     case GDN_ERR_DEVICE_TIMEOUT: return "GDN_ERR_DEVICE_TIMEOUT: a device-side wait ran out";
     case GDN_ERR_SEQLENS:
       return "GDN_ERR_SEQLENS: cu_seqlens does not rise from 0 to T (packed sequences)";
+    case GDN_ERR_PAGE: return "GDN_ERR_PAGE: a block table names a page that the cache does not have";
     default: return "unknown gdn_status";
   }
 }

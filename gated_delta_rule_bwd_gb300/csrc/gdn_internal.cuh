@@ -261,7 +261,77 @@ struct LayerNormProblem {
 size_t layer_norm_bwd_workspace(const LayerNormProblem& p);
 cudaError_t layer_norm_fwd(const LayerNormProblem& p, cudaStream_t s);
 cudaError_t layer_norm_bwd(const LayerNormProblem& p, cudaStream_t s);
+
+// Norm and rotation of query and key heads (qk_rope.cu).  Strides are batch,
+// token, head, in elements; wq and wk are both given or both NULL, R = 0 without
+// cos and sin.
+struct QkRopeProblem {
+  int B = 0, T = 0, H = 0, Hkv = 0, D = 0, R = 0, P = 0;
+  bool bf16 = true, interleaved = false;
+  float eps = 1e-6f;
+  long long qs[3] = {}, ks[3] = {};
+  const void *q = nullptr, *k = nullptr;
+  const float *wq = nullptr, *wk = nullptr, *cos = nullptr, *sin = nullptr;
+  const int* pos = nullptr;
+  void *qo = nullptr, *ko = nullptr;
+  const void *dqo = nullptr, *dko = nullptr;
+  void *dq = nullptr, *dk = nullptr;
+  float *dwq = nullptr, *dwk = nullptr;
+  void* ws = nullptr;
+};
+size_t qk_rope_bwd_workspace(const QkRopeProblem& p);
+cudaError_t qk_rope_fwd(const QkRopeProblem& p, cudaStream_t s);
+cudaError_t qk_rope_bwd(const QkRopeProblem& p, cudaStream_t s);
+
+// Pages of keys and values.  Strides are page, token, head, in elements (4-bit
+// codes: bytes); ks, vs: the steps of 4-bit codes.
+struct PagedCache {
+  int pages = 0, page = 0, Hkv = 0, D = 0, format = 0;
+  void *k = nullptr, *v = nullptr, *k_scale = nullptr, *v_scale = nullptr;
+  long long ks[3] = {}, vs[3] = {}, kss[3] = {}, vss[3] = {};
+};
+// The pages of nseq rows: row b's are table[b stride .. + max_pages).
+struct PageTable {
+  const int* table = nullptr;
+  int rows = 0, max_pages = 0;
+  long long stride = 0;
+};
+struct KvAppendProblem {
+  int B = 0, T = 0, H = 0, R = 0, P = 0;
+  bool bf16 = true, interleaved = false;
+  long long qs[3] = {}, ks[3] = {}, vs[3] = {};
+  const void *q = nullptr, *k = nullptr, *v = nullptr;
+  const float *cos = nullptr, *sin = nullptr;
+  const int *lens = nullptr, *cu = nullptr;  // cu: packed new tokens, or NULL
+  void* qo = nullptr;
+  PageTable pt;
+};
+cudaError_t kv_append(const KvAppendProblem& p, const PagedCache& c, cudaStream_t s);
+struct KvGatherProblem {
+  int total = 0;
+  bool bf16 = true;
+  const int* cu = nullptr;
+  void *k = nullptr, *v = nullptr;
+  PageTable pt;
+};
+cudaError_t kv_gather(const KvGatherProblem& p, const PagedCache& c, cudaStream_t s);
+struct AttnPagedProblem {
+  int B = 0, T = 0, H = 0;
+  bool bf16 = true;
+  float scale = 1.f;
+  const void* q = nullptr;
+  const int* lens = nullptr;
+  void* o = nullptr;
+  void* ws = nullptr;
+  PageTable pt;
+};
+size_t attn_paged_workspace(const AttnPagedProblem& p, const PagedCache& c);
+cudaError_t attn_paged(const AttnPagedProblem& p, const PagedCache& c, cudaStream_t s);
+
 cudaError_t attn_simt_read_and_clear_status(int* status);
+cudaError_t qk_rope_read_and_clear_status(int* status);
+cudaError_t kv_cache_read_and_clear_status(int* status);
+cudaError_t attn_paged_read_and_clear_status(int* status);
 cudaError_t attn_tc_fwd_read_and_clear_status(int* status);
 cudaError_t attn_tc_bwd_read_and_clear_status(int* status);
 cudaError_t attn_decode_read_and_clear_status(int* status);
@@ -299,7 +369,14 @@ enum KernelId {
   kLnBwd = 28,
   kLnSum = 29,
   kAttnBwd = 30,
-  kNumKernelIds = 31
+  kQkRopeFwd = 31,
+  kQkRopeBwd = 32,
+  kQkRopeSum = 33,
+  kKvAppend = 34,
+  kKvGather = 35,
+  kAttnPaged = 36,
+  kAttnPagedCombine = 37,
+  kNumKernelIds = 38
 };
 const char* kernel_name(int id);
 

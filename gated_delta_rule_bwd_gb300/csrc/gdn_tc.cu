@@ -44,14 +44,15 @@
 
 namespace gdn {
 
-// The status words of the bounded device-side waits: this file's and the KDA
-// kernels'; a timeout recorded in either is reported.
+// The status words of the kernel files: the first that is set is reported.
 cudaError_t read_and_clear_device_status(int* status) {
   int a = GDN_OK;
   cudaError_t e = tc::read_and_clear_file_status(&a);
   for (auto read : {kda_read_and_clear_status, nb_read_and_clear_status,
                     attn_simt_read_and_clear_status, attn_tc_fwd_read_and_clear_status,
-                    attn_tc_bwd_read_and_clear_status, attn_decode_read_and_clear_status}) {
+                    attn_tc_bwd_read_and_clear_status, attn_decode_read_and_clear_status,
+                    qk_rope_read_and_clear_status, kv_cache_read_and_clear_status,
+                    attn_paged_read_and_clear_status}) {
     int b = GDN_OK;
     if (e == cudaSuccess) e = read(&b);
     if (a == GDN_OK) a = b;

@@ -1,0 +1,350 @@
+// Pages of keys and values: new tokens in (kv_append, rotating keys and queries
+// by position on the way) and rows out again (kv_gather).
+//
+// Append: token t of row b goes to slot n = lens[b] + t, that is place n % page of
+// page table[b][n / page].  A warp takes a token and walks its heads of q (if
+// given), k and v as the norm-and-rotation kernel does (rope.cuh): the angles and
+// the page are looked up once per token.  4-bit rows pass through shared memory
+// to bring 8 neighbouring values into a lane (a pair's halves lie R / 2 apart).
+// Gather: a CTA takes a run of packed tokens, looks up their pages once, and
+// copies (or widens) 16-byte vectors.  Both are bound by memory: each byte is
+// read and written once.
+
+#include "paged.cuh"
+#include "rope.cuh"
+
+namespace gdn {
+
+cudaError_t kv_cache_read_and_clear_status(int* status) { return tc::read_and_clear_file_status(status); }
+
+namespace {
+
+using namespace paged;
+using namespace rope;
+using tc::sm_count;
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+
+struct Pages {
+  int pages, shift, max_pages, nseq;
+  long long table_stride;
+  const int* table;
+  void *k, *v, *k_scale, *v_scale;
+  long long ks[3], vs[3], kss[3], vss[3];  // page, token, head
+};
+
+Pages pages_of(const PagedCache& c, const PageTable& t) {
+  Pages p = {};
+  p.pages = c.pages, p.shift = page_shift(c.page), p.max_pages = t.max_pages, p.nseq = t.rows;
+  p.table_stride = t.stride, p.table = t.table;
+  p.k = c.k, p.v = c.v, p.k_scale = c.k_scale, p.v_scale = c.v_scale;
+  for (int i = 0; i < 3; ++i) p.ks[i] = c.ks[i], p.vs[i] = c.vs[i], p.kss[i] = c.kss[i], p.vss[i] = c.vss[i];
+  return p;
+}
+
+__device__ __forceinline__ void report(int status) { atomicExch(&tc::g_file_status, status); }
+
+// Whether the packed offsets rise from 0 to at most (or, `all`, exactly) total.
+// All threads of the CTA call.
+__device__ bool rises(const int* cu, int nseq, int total, bool all) {
+  int bad = 0;
+  if (threadIdx.x == 0) bad = cu[0] != 0 || cu[nseq] > total || (all && cu[nseq] != total);
+  for (int s = threadIdx.x; s < nseq; s += blockDim.x) bad |= cu[s + 1] < cu[s];
+  return !__syncthreads_or(bad);
+}
+
+// The page that holds a row's slot, or -1 (reported).
+__device__ __forceinline__ int page_of(const Pages& p, int row, long long slot) {
+  const int n = p.table[row * p.table_stride + (slot >> p.shift)];
+  if ((unsigned)n < (unsigned)p.pages) return n;
+  report(GDN_ERR_PAGE);
+  return -1;
+}
+
+// ---------------------------------------------------------------- append
+
+struct AppendArgs {
+  Pages c;
+  int T, H, Hkv, rows, D, R, P, split, interleaved;  // rows = H + 2 Hkv
+  long tokens;
+  long long qs[3], ks[3], vs[3];
+  const void *q, *k, *v;
+  const float *cos, *sin;
+  const int *lens, *cu;
+  void* qo;
+};
+
+// What becomes of a token: its slot's page and place, its position.
+struct Place {
+  int page, at, n;
+  bool turn, keep;  // its queries and keys are rotated (q is zeros otherwise); k and v are stored
+};
+
+__device__ __forceinline__ Place place_of(const AppendArgs& a, long tok) {
+  Place p = {0, 0, 0, false, false};
+  int row = (int)(tok / a.T), t = (int)(tok % a.T), fresh = a.T;
+  if (a.cu) {
+    if (a.c.nseq == 0) return p;
+    row = sequence_of(a.cu, a.c.nseq, (int)tok);
+    t = (int)tok - a.cu[row], fresh = a.cu[row + 1] - a.cu[row];
+    if (t < 0 || t >= fresh) return p;  // behind the last sequence
+  }
+  const int used = a.lens[row];
+  if (used < 0) return p;  // a row that is not in use
+  const long long n = (long long)used + t;
+  if ((long long)used + fresh > ((long long)a.c.max_pages << a.c.shift) || (a.R && n >= a.P)) {
+    report(GDN_ERR_SEQLENS);
+    return p;
+  }
+  p.n = (int)n, p.at = (int)n & ((1 << a.c.shift) - 1);
+  p.turn = true;
+  p.page = page_of(a.c, row, n);
+  p.keep = p.page >= 0;
+  return p;
+}
+
+template <typename T, int V, int NP, int LR, bool IL, bool I4>
+__global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a) {
+  constexpr int GW = 32 / LR, U = V == 4 ? 4 : 1, RB = V == 4 ? LR * 8 : 128;  // RB: a row's place in shared memory
+  __shared__ __align__(16) float rows[I4 ? kWarps * GW * RB : 1];
+  if (a.cu && blockIdx.x == 0 && !rises(a.cu, a.c.nseq, (int)a.tokens, false) && threadIdx.x == 0)
+    report(GDN_ERR_SEQLENS);
+  const int lane = threadIdx.x & 31, grp = lane / LR, l = lane % LR;
+  const long job = (long)blockIdx.x * kWarps + (threadIdx.x >> 5), tok = job / a.split;
+  if (tok >= a.tokens) return;
+  Slot<V> slot[NP];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) slot[i].template set<IL>((l + i * LR) * V, a.D, a.R);
+  const int b = (int)(tok / a.T), t = (int)(tok % a.T), step = a.split * GW;
+  Raw<T, V> x[U][NP];
+  auto fetch = [&](int r0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * step + grp, h = r - a.H;
+      const T* p = r < a.H        ? static_cast<const T*>(a.q) + b * a.qs[0] + t * a.qs[1] + r * a.qs[2]
+                   : h < a.Hkv    ? static_cast<const T*>(a.k) + b * a.ks[0] + t * a.ks[1] + h * a.ks[2]
+                                  : static_cast<const T*>(a.v) + b * a.vs[0] + t * a.vs[1] + (h - a.Hkv) * a.vs[2];
+#pragma unroll
+      for (int i = 0; i < NP; ++i) x[u][i] = r < a.rows ? load(p, slot[i]) : Raw<T, V>{};
+    }
+  };
+  int r0 = (int)(job % a.split) * GW;
+  fetch(r0);
+  const Place at = place_of(a, tok);
+  float c[NP][V], s[NP][V];
+#pragma unroll
+  for (int i = 0; i < NP; ++i)
+    angles<V>(a.cos, a.sin, (long long)at.n * (a.R / 2), (l + i * LR) * V, slot[i].rot && at.turn, c[i], s[i]);
+  for (; r0 < a.rows; r0 += U * step) {
+    float xa[U][NP][V], xb[U][NP][V];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < NP; ++i) widen<IL>(x[u][i], xa[u][i], xb[u][i]);
+    if (r0 + U * step < a.rows) fetch(r0 + U * step);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * step + grp, h = r - a.H;
+      if (r0 + u * step >= a.rows) break;  // the same for the whole warp
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+        if (slot[i].rot && h < a.Hkv) rotate<V>(c[i], s[i], xa[u][i], xb[u][i]);
+      if (r < a.H) {
+        T* y = static_cast<T*>(a.qo) + (tok * a.H + r) * a.D;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          if (!at.turn) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) xa[u][i][e] = xb[u][i][e] = 0.f;
+          }
+          store<IL>(y, slot[i], xa[u][i], xb[u][i]);
+        }
+      }
+      const bool isk = h < a.Hkv, keep = h >= 0 && r < a.rows && at.keep;
+      const int hk = isk ? h : h - a.Hkv;
+      const long long* st = isk ? a.c.ks : a.c.vs;
+      const long long to = at.page * st[0] + at.at * st[1] + hk * st[2];
+      if constexpr (!I4) {
+        if (!keep) continue;
+        T* y = static_cast<T*>(isk ? a.c.k : a.c.v) + to;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) store<IL>(y, slot[i], xa[u][i], xb[u][i]);
+      } else {
+        if (r0 + u * step + GW <= a.H) continue;  // only queries: the same for the whole warp
+        float* row = rows + ((threadIdx.x >> 5) * GW + grp) * RB;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < NP; ++i) store<IL>(row, slot[i], xa[u][i], xb[u][i]);
+        __syncwarp();
+        float y[8], step8;
+        const bool in = l < a.D / 8;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = in ? row[8 * l + e] : 0.f;
+        const uint32_t w = quantise8(y, step8);
+        if (!keep || !in) continue;
+        const long long* ss = isk ? a.c.kss : a.c.vss;
+        *reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(isk ? a.c.k : a.c.v) + to + 4 * l) = w;
+        if (l % 4 == 0)
+          static_cast<__nv_bfloat16*>(isk ? a.c.k_scale : a.c.v_scale)[at.page * ss[0] + at.at * ss[1] + hk * ss[2] + l / 4] =
+              __float2bfloat16_rn(step8);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- gather
+
+constexpr int kTokens = 256;  // most tokens of a CTA
+
+struct GatherArgs {
+  Pages c;
+  int total, Hkv, D, tokens;  // tokens per CTA
+  const int* cu;
+  void *k, *v;
+};
+
+// V values of type S from x as type O to y; a row's step for 4-bit codes.
+template <typename O, int N>
+struct alignas(16) Vec {
+  O x[N];
+};
+
+template <typename O, bool I4, int V>
+__global__ void __launch_bounds__(kThreads) kv_gather_kernel(GatherArgs a) {
+  __shared__ long long from[kTokens], step_from[I4 ? kTokens : 1];
+  const bool isv = blockIdx.y;
+  const int t0 = blockIdx.x * a.tokens, n = min(a.tokens, a.total - t0);
+  if (blockIdx.x == 0 && !isv && !rises(a.cu, a.c.nseq, a.total, true) && threadIdx.x == 0) report(GDN_ERR_SEQLENS);
+  const long long* st = isv ? a.c.vs : a.c.ks;
+  const long long* ss = isv ? a.c.vss : a.c.kss;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    long long at = -1;  // not of any row: left as it is
+    if (a.c.nseq > 0) {
+      const int tok = t0 + i, row = sequence_of(a.cu, a.c.nseq, tok);
+      const long long slot = (long long)tok - a.cu[row];
+      if (slot >= 0 && tok < a.cu[row + 1]) {
+        at = -2;  // without a page: zeros
+        if (slot < ((long long)a.c.max_pages << a.c.shift)) {
+          const int page = page_of(a.c, row, slot);
+          const int place = (int)slot & ((1 << a.c.shift) - 1);
+          if (page >= 0) {
+            at = page * st[0] + place * st[1];
+            if constexpr (I4) step_from[i] = page * ss[0] + place * ss[1];
+          }
+        } else {
+          report(GDN_ERR_SEQLENS);
+        }
+      }
+    }
+    from[i] = at;
+  }
+  __syncthreads();
+  const int nv = a.D / V, per = a.Hkv * nv, all = n * per;
+  O* out = static_cast<O*>(isv ? a.v : a.k) + (long long)t0 * a.Hkv * a.D;
+  constexpr int U = 4;
+  for (int i0 = threadIdx.x; i0 < all; i0 += U * kThreads) {
+    Vec<O, V> y[U];
+    long long to[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kThreads;
+      to[u] = -1;
+      if (i >= all) continue;
+      const int t = i / per, h = i % per / nv, d = i % nv * V;
+      const long long at = from[t];
+      if (at == -1) continue;
+      to[u] = (long long)i * V;
+      if (at < 0) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) y[u].x[e] = from_f32<O>(0.f);
+      } else if constexpr (I4) {
+        const unsigned char* p = static_cast<const unsigned char*>(isv ? a.c.v : a.c.k) + at + h * st[2] + d / 2;
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+        const float s = __bfloat162float(
+            static_cast<const __nv_bfloat16*>(isv ? a.c.v_scale : a.c.k_scale)[step_from[t] + h * ss[2] + d / kStepGroup]);
+#pragma unroll
+        for (int e = 0; e < V; ++e) y[u].x[e] = from_f32<O>((float)((int)(w >> (4 * e) & 15) - 8) * s);
+      } else {
+        const O* p = static_cast<const O*>(isv ? a.c.v : a.c.k) + at + h * st[2] + d;
+        if constexpr (V > 1) y[u] = *reinterpret_cast<const Vec<O, V>*>(p);
+        else y[u].x[0] = p[0];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (to[u] < 0) continue;
+      if constexpr (V > 1) *reinterpret_cast<Vec<O, V>*>(out + to[u]) = y[u];
+      else out[to[u]] = y[u].x[0];
+    }
+  }
+}
+
+// ---------------------------------------------------------------- host
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+template <typename T, int V, int NP, int LR>
+cudaError_t append(AppendArgs a, bool i4, cudaStream_t s) {
+  constexpr int GW = 32 / LR;
+  const long want = (16L * sm_count() + a.tokens - 1) / a.tokens;  // warps per token, as for the norm
+  a.split = (int)std::max(1L, std::min(want, (long)(a.rows + GW - 1) / GW));
+  const unsigned ctas = (unsigned)((a.tokens * a.split + kWarps - 1) / kWarps);
+  prof_before(s);
+  if (a.interleaved)
+    i4 ? kv_append_kernel<T, V, NP, LR, true, true><<<ctas, kThreads, 0, s>>>(a)
+       : kv_append_kernel<T, V, NP, LR, true, false><<<ctas, kThreads, 0, s>>>(a);
+  else
+    i4 ? kv_append_kernel<T, V, NP, LR, false, true><<<ctas, kThreads, 0, s>>>(a)
+       : kv_append_kernel<T, V, NP, LR, false, false><<<ctas, kThreads, 0, s>>>(a);
+  prof_after(s, kKvAppend);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t append(const KvAppendProblem& p, const PagedCache& c, cudaStream_t s) {
+  AppendArgs a = {};
+  a.c = pages_of(c, p.pt);
+  a.T = p.T, a.H = p.H, a.Hkv = c.Hkv, a.rows = p.H + 2 * c.Hkv, a.D = c.D, a.R = p.R, a.P = p.P;
+  a.tokens = (long)p.B * p.T, a.interleaved = p.interleaved;
+  for (int i = 0; i < 3; ++i) a.qs[i] = p.qs[i], a.ks[i] = p.ks[i], a.vs[i] = p.vs[i];
+  a.q = p.q, a.k = p.k, a.v = p.v, a.cos = p.cos, a.sin = p.sin, a.lens = p.lens, a.cu = p.cu, a.qo = p.qo;
+  const bool i4 = c.format == GDN_CACHE_I4;
+  bool vec = a.D % 8 == 0 && a.R % 8 == 0 && vectors(p.k, p.ks, sizeof(T)) && vectors(p.v, p.vs, sizeof(T)) &&
+             (p.H == 0 || (vectors(p.q, p.qs, sizeof(T)))) && aligned16(p.cos) && aligned16(p.sin);
+  if (!i4) vec = vec && vectors(c.k, c.ks, sizeof(T)) && vectors(c.v, c.vs, sizeof(T));
+  if (!vec) return append<T, 1, 2, 32>(a, i4, s);
+  return a.D <= 64 ? append<T, 4, 1, 8>(a, i4, s) : append<T, 4, 1, 16>(a, i4, s);
+}
+
+template <typename O, bool I4, int V>
+cudaError_t gather(GatherArgs a, cudaStream_t s) {
+  // about four vectors per thread
+  a.tokens = std::max(1, std::min(kTokens, 4 * kThreads / (a.Hkv * (a.D / V))));
+  prof_before(s);
+  kv_gather_kernel<O, I4, V><<<dim3((a.total + a.tokens - 1) / a.tokens, 2), kThreads, 0, s>>>(a);
+  prof_after(s, kKvGather);
+  return cudaGetLastError();
+}
+
+template <typename O>
+cudaError_t gather(const KvGatherProblem& p, const PagedCache& c, cudaStream_t s) {
+  GatherArgs a = {};
+  a.c = pages_of(c, p.pt);
+  a.total = p.total, a.Hkv = c.Hkv, a.D = c.D, a.cu = p.cu, a.k = p.k, a.v = p.v;
+  constexpr int V = 16 / (int)sizeof(O);
+  if (c.format == GDN_CACHE_I4) return gather<O, true, 8>(a, s);
+  if (a.D % V == 0 && vectors(c.k, c.ks, sizeof(O)) && vectors(c.v, c.vs, sizeof(O))) return gather<O, false, V>(a, s);
+  return gather<O, false, 1>(a, s);
+}
+
+}  // namespace
+
+cudaError_t kv_append(const KvAppendProblem& p, const PagedCache& c, cudaStream_t s) {
+  return p.bf16 ? append<__nv_bfloat16>(p, c, s) : append<float>(p, c, s);
+}
+
+cudaError_t kv_gather(const KvGatherProblem& p, const PagedCache& c, cudaStream_t s) {
+  return p.bf16 ? gather<__nv_bfloat16>(p, c, s) : gather<float>(p, c, s);
+}
+
+}  // namespace gdn

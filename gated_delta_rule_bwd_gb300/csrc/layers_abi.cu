@@ -1,4 +1,4 @@
-// C ABI of the attention layers' operators and layer norm: argument checks,
+// C ABI of the attention layers' operators, their paged caches and layer norm: argument checks,
 // kernel selection, launch.  The operations, layouts and error rules are
 // stated in include/gdn.h.
 
@@ -131,6 +131,144 @@ bool ln_aligned(const gdn::LayerNormProblem& p, std::initializer_list<const void
   return true;
 }
 
+// Strides of dimensions that have one entry at most do not matter: 0, so that an
+// arbitrary one does not decide how rows are read.
+void set_strides(long long (&dst)[3], const long long (&src)[3], int n0, int n1, int n2) {
+  const int n[3] = {n0, n1, n2};
+  for (int i = 0; i < 3; ++i) dst[i] = n[i] > 1 ? src[i] : 0;
+}
+bool any_negative(std::initializer_list<const long long*> strides) {
+  for (const long long* x : strides)
+    for (int i = 0; i < 3; ++i)
+      if (x[i] < 0) return true;
+  return false;
+}
+
+// Rotated values, tables and dtype of a call with angles.
+int check_rotation(int D, int R, int P, int dtype) {
+  if (dtype != GDN_F32 && dtype != GDN_BF16) return GDN_ERR_DTYPE;
+  if (D < 1 || D > 128 || R < 0 || R > D || R % 2 || P < 0) return GDN_ERR_SHAPE;
+  return GDN_OK;
+}
+
+int rope_problem(const gdn_qk_rope_shape* s, const float* wq, const float* wk, float eps, const float* cos,
+                 const float* sin, const int* pos, gdn::QkRopeProblem* p) {
+  if (!s) return GDN_ERR_ARG;
+  int rc = check_rotation(s->D, s->R, s->P, s->dtype);
+  if (rc != GDN_OK) return rc;
+  if (s->B < 0 || s->T < 0 || s->H < 0 || s->Hkv < 0 || s->H > 65535 || s->Hkv > 65535) return GDN_ERR_SHAPE;
+  const long long tokens = (long long)s->B * s->T;
+  if (tokens > (1LL << 30) || tokens * (s->H + s->Hkv) >= (1LL << 40)) return GDN_ERR_SHAPE;
+  if (any_negative({s->q_stride, s->k_stride})) return GDN_ERR_SHAPE;
+  if (!(eps >= 0.f) || !isfinite(eps) || !wq != !wk || (s->R > 0) != (cos != nullptr) ||
+      (s->R > 0) != (sin != nullptr) || (s->R == 0 && (pos || !wq)))
+    return GDN_ERR_ARG;
+  for (const void* x : {(const void*)wq, (const void*)wk, (const void*)cos, (const void*)sin, (const void*)pos})
+    if (!aligned(x, 4)) return GDN_ERR_ALIGN;
+  *p = gdn::QkRopeProblem{};
+  p->B = s->B, p->T = s->T, p->H = s->H, p->Hkv = s->Hkv, p->D = s->D, p->R = s->R, p->P = s->P;
+  p->bf16 = s->dtype == GDN_BF16, p->interleaved = s->interleaved != 0, p->eps = eps;
+  set_strides(p->qs, s->q_stride, s->B, s->T, s->H);
+  set_strides(p->ks, s->k_stride, s->B, s->T, s->Hkv);
+  p->wq = wq, p->wk = wk, p->cos = cos, p->sin = sin, p->pos = pos;
+  return GDN_OK;
+}
+
+// q and k: present where they hold data, aligned to their element
+int rope_inputs(gdn::QkRopeProblem* p, const void* q, const void* k) {
+  const size_t e = p->bf16 ? 2 : 4;
+  if ((p->H > 0 && !q) || (p->Hkv > 0 && !k)) return GDN_ERR_ARG;
+  if (!aligned(q, e) || !aligned(k, e)) return GDN_ERR_ALIGN;
+  p->q = q, p->k = k;
+  return GDN_OK;
+}
+
+bool rope_empty(const gdn::QkRopeProblem& p) { return p.B == 0 || p.T == 0 || p.H + p.Hkv == 0; }
+
+int paged_cache(const gdn_paged_cache* c, gdn::PagedCache* p) {
+  if (!c) return GDN_ERR_ARG;
+  if (c->format < GDN_CACHE_F32 || c->format > GDN_CACHE_I4) return GDN_ERR_DTYPE;
+  const bool i4 = c->format == GDN_CACHE_I4;
+  if (c->pages < 0 || c->page < 1 || c->page > (1 << 30) || (c->page & (c->page - 1)) || c->Hkv < 0 ||
+      c->Hkv > 65535 || c->D < 1 || c->D > 128 || (i4 && c->D % 32))
+    return GDN_ERR_SHAPE;
+  if (any_negative({c->k_stride, c->v_stride})) return GDN_ERR_SHAPE;
+  if (i4 && any_negative({c->k_scale_stride, c->v_scale_stride})) return GDN_ERR_SHAPE;
+  *p = gdn::PagedCache{};
+  p->pages = c->pages, p->page = c->page, p->Hkv = c->Hkv, p->D = c->D, p->format = c->format;
+  set_strides(p->ks, c->k_stride, c->pages, c->page, c->Hkv);
+  set_strides(p->vs, c->v_stride, c->pages, c->page, c->Hkv);
+  if (c->pages > 0 && c->Hkv > 0 && (any_null({c->k, c->v}) || (i4 && any_null({c->k_scale, c->v_scale}))))
+    return GDN_ERR_ARG;
+  p->k = c->k, p->v = c->v;
+  const size_t e = i4 ? 16 : c->format == GDN_CACHE_BF16 ? 2 : 4;
+  if (!aligned(c->k, e) || !aligned(c->v, e)) return GDN_ERR_ALIGN;
+  if (!i4) return GDN_OK;
+  set_strides(p->kss, c->k_scale_stride, c->pages, c->page, c->Hkv);
+  set_strides(p->vss, c->v_scale_stride, c->pages, c->page, c->Hkv);
+  if (!all_aligned16({c->k_scale, c->v_scale})) return GDN_ERR_ALIGN;
+  for (int i = 0; i < 3; ++i)
+    if (p->ks[i] % 16 || p->vs[i] % 16 || p->kss[i] % (c->D / 32) || p->vss[i] % (c->D / 32)) return GDN_ERR_ALIGN;
+  p->k_scale = c->k_scale, p->v_scale = c->v_scale;
+  return GDN_OK;
+}
+
+// dtype against a cache's format: the same, or 4 bits
+int check_format(const gdn::PagedCache& c, int dtype) {
+  if (dtype != GDN_F32 && dtype != GDN_BF16) return GDN_ERR_DTYPE;
+  return c.format == GDN_CACHE_I4 || c.format == (dtype == GDN_BF16 ? GDN_CACHE_BF16 : GDN_CACHE_F32) ? GDN_OK
+                                                                                                     : GDN_ERR_DTYPE;
+}
+
+int page_table(const gdn::PagedCache& c, const int* table, int rows, int max_pages, long long stride,
+               gdn::PageTable* t) {
+  if (rows < 0 || rows > (1 << 30) || max_pages < 0 || (long long)max_pages * c.page > (1LL << 30) || stride < 0)
+    return GDN_ERR_SHAPE;
+  if (!aligned(table, 4)) return GDN_ERR_ALIGN;
+  if (!table && rows > 0 && max_pages > 0) return GDN_ERR_ARG;
+  t->table = table, t->rows = rows, t->max_pages = max_pages, t->stride = stride;
+  return GDN_OK;
+}
+
+int append_problem(const gdn_kv_append_shape* s, const gdn_paged_cache* cache, const int* table, const int* cu,
+                   gdn::KvAppendProblem* p, gdn::PagedCache* c) {
+  if (!s) return GDN_ERR_ARG;
+  int rc = paged_cache(cache, c);
+  if (rc != GDN_OK) return rc;
+  if ((rc = check_format(*c, s->dtype)) != GDN_OK) return rc;
+  if ((rc = check_rotation(c->D, s->R, s->P, s->dtype)) != GDN_OK) return rc;
+  if (s->B < 0 || s->T < 0 || s->H < 0 || s->H > 65535 || (long long)s->B * s->T > (1LL << 30)) return GDN_ERR_SHAPE;
+  if (any_negative({s->q_stride, s->k_stride, s->v_stride})) return GDN_ERR_SHAPE;
+  if (cu ? s->B != 1 : s->rows != s->B) return GDN_ERR_SHAPE;
+  *p = gdn::KvAppendProblem{};
+  if ((rc = page_table(*c, table, s->rows, s->max_pages, s->table_stride, &p->pt)) != GDN_OK) return rc;
+  p->B = s->B, p->T = s->T, p->H = s->H, p->R = s->R, p->P = s->P;
+  p->bf16 = s->dtype == GDN_BF16, p->interleaved = s->interleaved != 0;
+  set_strides(p->qs, s->q_stride, s->B, s->T, s->H);
+  set_strides(p->ks, s->k_stride, s->B, s->T, c->Hkv);
+  set_strides(p->vs, s->v_stride, s->B, s->T, c->Hkv);
+  return GDN_OK;
+}
+
+int paged_problem(const gdn_attn_paged_shape* s, const gdn_paged_cache* cache, gdn::AttnPagedProblem* p,
+                  gdn::PagedCache* c) {
+  if (!s) return GDN_ERR_ARG;
+  int rc = paged_cache(cache, c);
+  if (rc != GDN_OK) return rc;
+  if ((rc = check_format(*c, s->dtype)) != GDN_OK) return rc;
+  if ((rc = check_heads(s->H, c->Hkv, c->D, s->dtype)) != GDN_OK) return rc;
+  if (s->B < 0 || s->T < 0 || (s->H == 0 && c->Hkv > 0)) return GDN_ERR_SHAPE;
+  if ((long long)s->B * c->Hkv > 65535 || (c->Hkv > 0 && (long long)s->H / c->Hkv * s->T > 65535LL * 8))
+    return GDN_ERR_SHAPE;
+  *p = gdn::AttnPagedProblem{};
+  if ((rc = page_table(*c, nullptr, 0, s->max_pages, s->table_stride, &p->pt)) != GDN_OK) return rc;
+  p->pt.rows = s->B;
+  p->B = s->B, p->T = s->T, p->H = s->H, p->bf16 = s->dtype == GDN_BF16;
+  return GDN_OK;
+}
+
+bool paged_empty(const gdn::AttnPagedProblem& p) { return p.B == 0 || p.T == 0 || p.H == 0; }
+
 }  // namespace
 
 extern "C" {
@@ -224,6 +362,110 @@ int gdn_attn_decode(const gdn_attn_decode_shape* shape, const void* q, const voi
   p.q = q, p.k = k, p.v = v, p.kc = k_cache, p.vc = v_cache, p.lens = lens;
   p.scale = scale, p.o = o, p.ws = ws;
   return done(gdn::attn_decode(p, static_cast<cudaStream_t>(stream)));
+}
+
+int gdn_qk_norm_rope_fwd(const gdn_qk_rope_shape* shape, const void* q, const void* k, const float* wq,
+                         const float* wk, float eps, const float* cos, const float* sin, const int* positions,
+                         void* qo, void* ko, void* stream) {
+  gdn::QkRopeProblem p;
+  int rc = rope_problem(shape, wq, wk, eps, cos, sin, positions, &p);
+  if (rc != GDN_OK || rope_empty(p)) return rc;
+  if ((rc = rope_inputs(&p, q, k)) != GDN_OK) return rc;
+  if ((p.H > 0 && !qo) || (p.Hkv > 0 && !ko)) return GDN_ERR_ARG;
+  if (!all_aligned16({qo, ko})) return GDN_ERR_ALIGN;
+  p.qo = qo, p.ko = ko;
+  return done(gdn::qk_rope_fwd(p, static_cast<cudaStream_t>(stream)));
+}
+
+size_t gdn_qk_norm_rope_bwd_workspace(const gdn_qk_rope_shape* shape) {
+  if (!shape || shape->D < 1 || shape->D > 128) return 0;
+  gdn::QkRopeProblem p;
+  p.D = shape->D;
+  return gdn::qk_rope_bwd_workspace(p);
+}
+
+int gdn_qk_norm_rope_bwd(const gdn_qk_rope_shape* shape, const void* q, const void* k, const float* wq,
+                         const float* wk, float eps, const float* cos, const float* sin, const int* positions,
+                         const void* dqo, const void* dko, void* dq, void* dk, float* dwq, float* dwk, void* ws,
+                         size_t ws_bytes, void* stream) {
+  gdn::QkRopeProblem p;
+  int rc = rope_problem(shape, wq, wk, eps, cos, sin, positions, &p);
+  if (rc != GDN_OK) return rc;
+  if (wq && any_null({dwq, dwk})) return GDN_ERR_ARG;
+  if (!aligned(dwq, 4) || !aligned(dwk, 4)) return GDN_ERR_ALIGN;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (rope_empty(p)) {
+    if (!wq) return GDN_OK;
+    cudaError_t e = cudaMemsetAsync(dwq, 0, p.D * sizeof(float), st);
+    if (e == cudaSuccess) e = cudaMemsetAsync(dwk, 0, p.D * sizeof(float), st);
+    return done(e);
+  }
+  if ((rc = rope_inputs(&p, q, k)) != GDN_OK) return rc;
+  if ((p.H > 0 && any_null({dqo, dq})) || (p.Hkv > 0 && any_null({dko, dk}))) return GDN_ERR_ARG;
+  if (!all_aligned16({dqo, dko, dq, dk, ws})) return GDN_ERR_ALIGN;
+  if (wq && (!ws || ws_bytes < gdn::qk_rope_bwd_workspace(p))) return GDN_ERR_WORKSPACE;
+  p.dqo = dqo, p.dko = dko, p.dq = dq, p.dk = dk, p.dwq = dwq, p.dwk = dwk, p.ws = ws;
+  return done(gdn::qk_rope_bwd(p, st));
+}
+
+int gdn_kv_append(const gdn_kv_append_shape* shape, const gdn_paged_cache* cache, const void* k, const void* v,
+                  const void* q, const float* cos, const float* sin, const int* table, const int* lens,
+                  const int* cu_seqlens, void* qo, void* stream) {
+  gdn::KvAppendProblem p;
+  gdn::PagedCache c;
+  int rc = append_problem(shape, cache, table, cu_seqlens, &p, &c);
+  if (rc != GDN_OK) return rc;
+  if ((p.R > 0) != (cos != nullptr) || (p.R > 0) != (sin != nullptr)) return GDN_ERR_ARG;
+  if (p.B == 0 || p.T == 0 || p.H + c.Hkv == 0) return GDN_OK;
+  if ((c.Hkv > 0 && any_null({k, v})) || (p.H > 0 && any_null({q, qo})) || (p.pt.rows > 0 && !lens)) return GDN_ERR_ARG;
+  const size_t e = p.bf16 ? 2 : 4;
+  for (const void* x : {k, v, q})
+    if (!aligned(x, e)) return GDN_ERR_ALIGN;
+  if (!aligned(cos, 4) || !aligned(sin, 4) || !aligned(lens, 4) || !aligned(cu_seqlens, 4) || !aligned(qo, 16))
+    return GDN_ERR_ALIGN;
+  p.k = k, p.v = v, p.q = q, p.cos = cos, p.sin = sin, p.lens = lens, p.cu = cu_seqlens, p.qo = qo;
+  return done(gdn::kv_append(p, c, static_cast<cudaStream_t>(stream)));
+}
+
+int gdn_kv_gather(const gdn_paged_cache* cache, const int* table, int rows, int max_pages, long long table_stride,
+                  const int* cu_seqlens, int total, int dtype, void* k, void* v, void* stream) {
+  gdn::KvGatherProblem p;
+  gdn::PagedCache c;
+  int rc = paged_cache(cache, &c);
+  if (rc != GDN_OK) return rc;
+  if ((rc = check_format(c, dtype)) != GDN_OK) return rc;
+  if (total < 0 || total > (1 << 30)) return GDN_ERR_SHAPE;
+  if ((rc = page_table(c, table, rows, max_pages, table_stride, &p.pt)) != GDN_OK) return rc;
+  if (total == 0 || c.Hkv == 0) return GDN_OK;
+  if (any_null({cu_seqlens, k, v})) return GDN_ERR_ARG;
+  if (!aligned(cu_seqlens, 4) || !all_aligned16({k, v})) return GDN_ERR_ALIGN;
+  p.total = total, p.bf16 = dtype == GDN_BF16, p.cu = cu_seqlens, p.k = k, p.v = v;
+  return done(gdn::kv_gather(p, c, static_cast<cudaStream_t>(stream)));
+}
+
+size_t gdn_attn_paged_workspace(const gdn_attn_paged_shape* shape, const gdn_paged_cache* cache) {
+  gdn::AttnPagedProblem p;
+  gdn::PagedCache c;
+  if (paged_problem(shape, cache, &p, &c) != GDN_OK || paged_empty(p)) return 0;
+  return gdn::attn_paged_workspace(p, c);
+}
+
+int gdn_attn_paged(const gdn_attn_paged_shape* shape, const gdn_paged_cache* cache, const void* q,
+                   const int* table, const int* lens, float scale, void* o, void* ws, size_t ws_bytes,
+                   void* stream) {
+  gdn::AttnPagedProblem p;
+  gdn::PagedCache c;
+  int rc = paged_problem(shape, cache, &p, &c);
+  if (rc != GDN_OK) return rc;
+  if (!(scale > 0.f) || !isfinite(scale)) return GDN_ERR_ARG;
+  if (paged_empty(p)) return GDN_OK;
+  if (any_null({q, lens, o}) || (!table && p.pt.max_pages > 0)) return GDN_ERR_ARG;
+  if (!all_aligned16({q, o, ws}) || !aligned(lens, 4) || !aligned(table, 4)) return GDN_ERR_ALIGN;
+  const size_t need = gdn::attn_paged_workspace(p, c);
+  if (need > 0 && (!ws || ws_bytes < need)) return GDN_ERR_WORKSPACE;
+  p.pt.table = table;
+  p.q = q, p.lens = lens, p.scale = scale, p.o = o, p.ws = ws;
+  return done(gdn::attn_paged(p, c, static_cast<cudaStream_t>(stream)));
 }
 
 int gdn_layer_norm_fwd(const gdn_norm_shape* shape, const void* x, const float* weight, const float* bias,

@@ -89,8 +89,11 @@ typedef enum {
   GDN_ERR_WORKSPACE = -5,      /* workspace NULL or smaller than required      */
   GDN_ERR_CUDA = -6,           /* a CUDA call failed; see gdn_last_cuda_error  */
   GDN_ERR_DEVICE_TIMEOUT = -7, /* a bounded device-side wait ran out           */
-  GDN_ERR_SEQLENS = -8         /* packed sequences: cu_seqlens not rising from
-                                  0 to T (found on the device; see *_varlen)   */
+  GDN_ERR_SEQLENS = -8,        /* packed sequences: cu_seqlens not rising from
+                                  0 to T (found on the device; see *_varlen);
+                                  a length or position out of its range        */
+  GDN_ERR_PAGE = -9            /* a block table names a page that the cache does
+                                  not have (found on the device)               */
 } gdn_status;
 
 /* GDN_BF16_G16 (KDA only): bf16 token tensors, and the per-key-dimension gate
@@ -465,6 +468,159 @@ GDN_API int gdn_attn_decode(const gdn_attn_decode_shape* shape, const void* q, c
                             const void* v, void* k_cache, void* v_cache, const int* lens,
                             float scale, void* o, void* ws, size_t ws_bytes, void* stream);
 
+/* Norm and rotation of the query and key heads in front of a softmax attention
+ * layer, in one pass.  Per row x of D values (one head of one token), with
+ * weight w [D] (fp32; wq for the heads of q, wk for those of k):
+ *   n = x / sqrt(mean(x^2) + eps) * w          (wq = wk = NULL: n = x),
+ * and the first R values of n are turned by position.  The pairs are
+ * (i, i + R / 2), i < R / 2, or with interleaved != 0 (2 i, 2 i + 1); a token at
+ * position p turns pair i by the angle whose cosine and sine are cos[p][i] and
+ * sin[p][i] (fp32 tables [P, R / 2]):
+ *   y_a = n_a cos - n_b sin,   y_b = n_b cos + n_a sin;   values past R are n.
+ * R = 0 (cos, sin, positions NULL) is the norm alone; without weights R > 0.
+ * positions (DEVICE, int32 [B, T], 4-byte aligned) are the tokens' positions;
+ * NULL: token t of a row has position t.  A token whose position is outside
+ * [0, P) gets rows of zeros (and gives no gradient), and gdn_device_status()
+ * returns GDN_ERR_SEQLENS.
+ *
+ * Layout: q [B, T, H, D], k [B, T, Hkv, D], the D values of a head contiguous,
+ * any non-negative batch, token and head strides (views of one projection); qo,
+ * ko, dqo, dko, dq, dk contiguous.  D in [1, 128]; R even, in [0, D]; H and Hkv
+ * in [0, 65535]; B T <= 2^30, B T (H + Hkv) < 2^40; dtype GDN_F32 or GDN_BF16.
+ * q, k aligned to their element, the fp32 tensors to 4 bytes, everything else
+ * to 16.  Rows go in 16-byte vectors where D and R are multiples of 8 and q, k,
+ * the weights and the tables are aligned for it, and value by value otherwise.
+ * All arithmetic is fp32; results are rounded once.
+ *
+ * The backward returns dq and dk (gradients with respect to q and k, given those
+ * of qo and ko) and, with weights, dwq and dwk [D] (fp32, overwritten, summed
+ * over all tokens and heads in a fixed order: reproducible).  It reads q and k
+ * again; the forward saves nothing.  Errors: GDN_ERR_ARG (a NULL pointer; only
+ * one weight, or only one table; eps negative or not finite; neither norm nor
+ * rotation), GDN_ERR_SHAPE, GDN_ERR_DTYPE, GDN_ERR_ALIGN, GDN_ERR_WORKSPACE,
+ * GDN_ERR_CUDA. */
+typedef struct {
+  int B, T, H, Hkv, D;
+  int R, P;           /* rotated values per head; positions of the tables */
+  int interleaved;
+  int dtype;          /* gdn_dtype */
+  long long q_stride[3], k_stride[3]; /* batch, token, head, in elements */
+} gdn_qk_rope_shape;
+
+GDN_API int gdn_qk_norm_rope_fwd(const gdn_qk_rope_shape* shape, const void* q, const void* k,
+                                 const float* wq, const float* wk, float eps, const float* cos,
+                                 const float* sin, const int* positions, void* qo, void* ko,
+                                 void* stream);
+GDN_API size_t gdn_qk_norm_rope_bwd_workspace(const gdn_qk_rope_shape* shape);
+GDN_API int gdn_qk_norm_rope_bwd(const gdn_qk_rope_shape* shape, const void* q, const void* k,
+                                 const float* wq, const float* wk, float eps, const float* cos,
+                                 const float* sin, const int* positions, const void* dqo,
+                                 const void* dko, void* dq, void* dk, float* dwq, float* dwk,
+                                 void* ws, size_t ws_bytes, void* stream);
+
+/* Paged caches of keys and values.  A cache is `pages` pages of `page` tokens
+ * (a power of two): k and v [pages, page, Hkv, D], the D values of a head
+ * contiguous, with any non-negative page, token and head strides.  Slot n of row
+ * b (its n-th token) lies at place n % page of page table[b][n / page]; the
+ * block table (DEVICE, int32 [rows, max_pages], rows table_stride elements
+ * apart) is the caller's, and pages may stand in any order and be shared by
+ * rows that only read them.  Entries of a table that belong to no token of a
+ * call are not read.  An entry outside [0, pages) is found on the device: its
+ * tokens are not stored, and read as zeros, and gdn_device_status() returns
+ * GDN_ERR_PAGE.
+ *
+ * Formats: GDN_CACHE_F32, GDN_CACHE_BF16, and GDN_CACHE_I4 (D a multiple of 32),
+ * where every 32 values of a head have a step (bf16) and a code of 4 bits each:
+ *   step = max|x| / 7, rounded to 5 significant bits (half up),
+ *   code = x / step rounded to the nearest integer (half to even), in [-7, 7].
+ * k and v are then bytes [pages, page, Hkv, D / 2], byte i holding code + 8 of
+ * values 2 i (low four bits) and 2 i + 1; k_scale and v_scale are bf16 [pages,
+ * page, Hkv, D / 32].  A step of 0 has codes of 0; a NaN or infinity makes its 32
+ * values NaN.  The values that a cache stands for, code * step, are exact in bf16.
+ * Strides are in elements (bytes for the codes).  Alignment: k and v to their
+ * element; GDN_CACHE_I4: k and v bases and strides to 16 bytes, k_scale and
+ * v_scale bases to 16 bytes and strides multiples of D / 32 elements. */
+typedef enum { GDN_CACHE_F32 = 0, GDN_CACHE_BF16 = 1, GDN_CACHE_I4 = 2 } gdn_cache_format;
+
+typedef struct {
+  int pages, page, Hkv, D;
+  int format;              /* gdn_cache_format */
+  void *k, *v;
+  void *k_scale, *v_scale; /* GDN_CACHE_I4, else ignored */
+  long long k_stride[3], v_stride[3], k_scale_stride[3], v_scale_stride[3]; /* page, token, head */
+} gdn_paged_cache;
+
+/* Appends new tokens to rows of a paged cache: token t of row b goes to slot
+ * lens[b] + t (lens: DEVICE, int32 [rows], not changed).  On the way k is turned
+ * by the position that is its slot (pairs and tables as above; R = 0: not at
+ * all), v goes in as it is; with H > 0 the queries q [.., H, D] of the same
+ * tokens are turned too and written to qo (contiguous).  A rotated row has the
+ * same bits as from gdn_qk_norm_rope_fwd without weights.
+ *
+ * The new tokens are k, v [B, T, Hkv, D] (rows = B), or with cu_seqlens (DEVICE,
+ * int32 [rows + 1]) packed: B = 1, T all tokens, row b's being [cu_seqlens[b],
+ * cu_seqlens[b + 1]).  Tokens from cu_seqlens[rows] on belong to no row, as in
+ * the padded batch of a captured graph; so do the tokens of a row whose lens[b]
+ * is negative (a row that is not in use).  They are not stored, and their rows
+ * of qo are zeros.  The same holds, and gdn_device_status() returns
+ * GDN_ERR_SEQLENS, for a row that would not fit max_pages pages, for tokens
+ * whose slot is outside the tables of angles, and where cu_seqlens does not rise
+ * from 0 to at most T (what is stored is then unspecified; every access stays
+ * inside the arrays).  No two tokens of a call may have the same slot.
+ *
+ * dtype is that of q, k, v and qo; the cache has it too, or GDN_CACHE_I4.
+ * Alignment: q, k, v to their element, qo to 16 bytes.  B T <= 2^30, rows <= 2^30,
+ * max_pages page <= 2^30, H and Hkv <= 65535.  Errors as above. */
+typedef struct {
+  int B, T, H;        /* H: query heads to rotate, 0: none */
+  int R, P;
+  int interleaved;
+  int dtype;          /* gdn_dtype */
+  int rows, max_pages;
+  long long table_stride;
+  long long q_stride[3], k_stride[3], v_stride[3];
+} gdn_kv_append_shape;
+
+GDN_API int gdn_kv_append(const gdn_kv_append_shape* shape, const gdn_paged_cache* cache,
+                          const void* k, const void* v, const void* q, const float* cos,
+                          const float* sin, const int* table, const int* lens,
+                          const int* cu_seqlens, void* qo, void* stream);
+
+/* Reads rows of a paged cache back: the first cu_seqlens[b + 1] - cu_seqlens[b]
+ * tokens of row b to k, v [total, Hkv, D] (contiguous, 16-byte aligned) from
+ * token cu_seqlens[b] on, as gdn_attn_fwd takes them (cu_seqlens: DEVICE, int32
+ * [rows + 1], rising from 0 to total, else GDN_ERR_SEQLENS by
+ * gdn_device_status() and unspecified values).  dtype is the cache's; from
+ * GDN_CACHE_I4, GDN_BF16 (exact) or GDN_F32. */
+GDN_API int gdn_kv_gather(const gdn_paged_cache* cache, const int* table, int rows, int max_pages,
+                          long long table_stride, const int* cu_seqlens, int total, int dtype,
+                          void* k, void* v, void* stream);
+
+/* Attention of T new tokens per row against the pages that hold them already:
+ * with lens [B] as in the gdn_kv_append call that stored them (the tokens before
+ * the new ones), new token t of q [B, T, H, D] sees the slots <= lens[b] + t.
+ * o [B, T, H, D]; both contiguous.  Rows as in the single-token form on a
+ * contiguous cache; a row whose lens[b] is negative is not in use and gets o =
+ * 0, and so does one that would not fit max_pages pages, for which
+ * gdn_device_status() returns GDN_ERR_SEQLENS.
+ *
+ * q may be bf16 with GDN_CACHE_BF16 or GDN_CACHE_I4, fp32 with GDN_CACHE_F32 or
+ * GDN_CACHE_I4.  Limits: max_pages page <= 2^30, B Hkv <= 65535, H / Hkv T <=
+ * 65535 * 8, no key heads without query heads.  Errors as above (GDN_ERR_ALIGN:
+ * q, o or ws not 16-byte aligned). */
+typedef struct {
+  int B, T, H;
+  int dtype;          /* gdn_dtype of q and o */
+  int max_pages;
+  long long table_stride;
+} gdn_attn_paged_shape;
+
+GDN_API size_t gdn_attn_paged_workspace(const gdn_attn_paged_shape* shape,
+                                        const gdn_paged_cache* cache);
+GDN_API int gdn_attn_paged(const gdn_attn_paged_shape* shape, const gdn_paged_cache* cache,
+                           const void* q, const int* table, const int* lens, float scale, void* o,
+                           void* ws, size_t ws_bytes, void* stream);
+
 /* Layer norm of rows of D values (the pre-norm of a layer), with weight [D]
  * and bias [D] (fp32; bias may be NULL):
  *   mean = sum(x) / D,  rstd = 1 / sqrt(sum((x - mean)^2) / D + eps),
@@ -493,8 +649,8 @@ GDN_API const char* gdn_status_str(int status);
 GDN_API int gdn_last_cuda_error(void);
 
 /* Reads and clears the device status word of the current device: GDN_OK,
- * GDN_ERR_DEVICE_TIMEOUT, GDN_ERR_SEQLENS, or GDN_ERR_ALIGN (an attention
- * kernel found its shared memory unaligned and did nothing); GDN_ERR_ARG only
+ * GDN_ERR_DEVICE_TIMEOUT, GDN_ERR_SEQLENS, GDN_ERR_PAGE, or GDN_ERR_ALIGN (an
+ * attention kernel found its shared memory unaligned and did nothing); GDN_ERR_ARG only
  * from gdn_attn_wait_selftest.  Synchronises the
  * current device.  Returns GDN_ERR_CUDA if the read itself fails. */
 GDN_API int gdn_device_status(void);
