@@ -197,19 +197,454 @@ __global__ void __launch_bounds__(kThreads) attn_paged_simt_kernel(Args a) {
   }
 }
 
+// ---------------------------------------------------------------- warp-level tensor path
+//
+// bf16 queries, D a multiple of 8 (bf16 pages, padded with zeros to DP) or D = DP
+// (4 bits), 16-byte aligned pages.  Few rows and a bandwidth bound leave nothing
+// for tcgen05's 128-row tiles to do: mma.m16n8k16 takes them.  A lane is (g, t) =
+// (lane / 4, lane % 4) in the fragments below.
+//
+//   S = Q K^T: the M = 16 rows are queries (NR = 1: 8 of them and 8 of zeros), N = 8
+//   keys.  Lane (g, t) gets row g (and g + 8) and keys 2 t, 2 t + 1, which is what
+//   O^T = V^T P^T wants of P as its B operand: M = 16 of the D values, N = 8 rows,
+//   K = 16 keys.  P never leaves its lane.
+//   The order of the D values within a product is free.  A lane takes whole words of
+//   a key's row (both K's and V's), so that nothing is moved for the fragments' sake.
+//
+// 4 bits.  A word holds 8 codes; w >> 4 n & 0x000f000f, put into the mantissas of two
+// bf16 128s, is 128 + (code + 8) of values n and n + 4: one shift and one logic
+// operation for two.  Steps go to the scores: per 32 values
+//   s += step (sum_d q_d (136 + code_d) - 136 sum_d q_d),
+// the second sum as the accumulator's start, once per segment (the products are
+// exact; 136 against codes of about 3 costs the fp32 sum over 32 values some 6 of
+// its 24 bits, and bf16 q has 8).  For V the 136 is taken off before the product: sums
+// over thousands of keys of one sign would drown what is left of codes that cancel.
+// Its steps go to the probabilities, p step in fp32, rounded once to bf16: one weight
+// per key, row and 32 values.
+//
+// Each warp streams its own blocks of KS keys (w, w + 4, ...) through a ring of
+// kStages stages (cp.async) and keeps its own m, l and accumulators, so the warps
+// meet only at a segment's end.
+constexpr int kStages = 3;
+
+template <int n>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool valid) {
+  if constexpr (n == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16u : 0u) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(n), "r"(valid ? (uint32_t)n : 0u)
+                 : "memory");
+}
+template <int n>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
+                                    float c0, float c1, float c2, float c3) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+// 128 + (code + 8) of two codes as bf16, and the codes
+__device__ __forceinline__ uint32_t codes136(uint32_t w, int n) { return ((w >> (4 * n)) & 0x000f000fu) | 0x43004300u; }
+__device__ __forceinline__ uint32_t codes(uint32_t w, int n) {
+  const uint32_t x = codes136(w, n), o = 0xc308c308u;  // -136
+  const __nv_bfloat162 y = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&o));
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+__device__ __forceinline__ float lo16(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float hi16(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+template <int DP, bool I4>
+struct Stage {
+  static constexpr int KS = I4 ? 32 : 16;          // keys
+  static constexpr int row = I4 ? DP / 2 : DP * 2;  // bytes of a key's row
+  static constexpr int NC = row / 16;               // 16-byte chunks of it
+  static constexpr int step = I4 ? DP / 16 : 0;     // bytes of a key's steps
+  static constexpr int v = KS * row, ks = 2 * v, vs = ks + KS * step, bytes = vs + KS * step;
+  // Chunk c of key r lies at c ^ f(r), so that the lanes of a load (eight keys' words
+  // of one chunk; two words each of four keys two apart) meet no bank twice.
+  __device__ __forceinline__ static uint32_t at(int r, int c) {
+    const int f = !I4 ? (r & 6) ^ ((r & 1) << 2) : DP == 128 ? (r >> 1) & 3 : (r >> 2) & 1;
+    return r * row + ((c ^ f) << 4);
+  }
+};
+
+template <int DP, int NR, bool I4>
+__global__ void __launch_bounds__(kThreads, I4 ? (NR == 1 ? 4 : 3) : 2) attn_paged_mma_kernel(Args a) {
+  using St = Stage<DP, I4>;
+  constexpr int KS = St::KS, NG = DP / 32, NT = KS / 8, kQ = 8 * NR;  // kQ: query rows per CTA
+  extern __shared__ __align__(128) unsigned char sm[];
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane / 4, t = lane % 4, row0 = blockIdx.y * kQ;
+  const uint32_t ring = smem_u32(sm) + w * kStages * St::bytes;
+  grid_dep_launch();
+  empty_rows<__nv_bfloat16>(a);
+  if (threadIdx.x == 0) a.starts[(long)blockIdx.y * gridDim.x + blockIdx.x].x = -1;
+  Walk<Args> wk;
+  if (!wk.init(a)) return;
+  while (wk.segment(a)) {
+    const int b = wk.b, hk = wk.hk, old = wk.keys - a.T, k1 = wk.k1;
+    const unsigned char* kb = static_cast<const unsigned char*>(a.k) + hk * a.ks[2] * (I4 ? 1 : 2);
+    const unsigned char* vb = static_cast<const unsigned char*>(a.v) + hk * a.vs[2] * (I4 ? 1 : 2);
+    const int blocks = (k1 - wk.k0 + KS - 1) / KS;  // this warp's are w, w + 4, ...
+    const int mine = blocks > w ? (blocks - w + 3) / 4 : 0;
+
+    // the page of this lane's key of block i
+    auto lookup = [&](int i) {
+      const int j = wk.k0 + (w + 4 * i) * KS + lane % KS;
+      return i < mine && j < k1 ? a.page_of(b, j) : -1;
+    };
+    // block i into its stage; pg: lookup(i)
+    auto fetch = [&](int i, int pg) {
+      const int j0 = wk.k0 + (w + 4 * i) * KS, mask = (1 << a.shift) - 1;
+      const uint32_t dst = ring + i % kStages * St::bytes;
+      const int c = lane % St::NC;
+#pragma unroll
+      for (int r = lane / St::NC; r < KS; r += 32 / St::NC) {
+        const int p = __shfl_sync(0xffffffffu, pg, r), at = (j0 + r) & mask;
+        const bool in = p >= 0 && c * (I4 ? 32 : 8) < a.D;
+        const unsigned char* ks = kb + (p * a.ks[0] + at * a.ks[1]) * (I4 ? 1 : 2) + c * 16;
+        const unsigned char* vs = vb + (p * a.vs[0] + at * a.vs[1]) * (I4 ? 1 : 2) + c * 16;
+        cp_async<16>(dst + St::at(r, c), in ? ks : kb, in);
+        cp_async<16>(dst + St::v + St::at(r, c), in ? vs : vb, in);
+      }
+      if constexpr (I4) {
+        const int at = (j0 + lane) & mask;
+        const bool in = pg >= 0;
+        const __nv_bfloat16 *ks = a.k_scale + hk * a.kss[2], *vs = a.v_scale + hk * a.vss[2];
+        cp_async<St::step>(dst + St::ks + lane * St::step, in ? ks + pg * a.kss[0] + at * a.kss[1] : ks, in);
+        cp_async<St::step>(dst + St::vs + lane * St::step, in ? vs + pg * a.vss[0] + at * a.vss[1] : vs, in);
+      }
+    };
+    int pg = lookup(0);
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+      const int next = lookup(i + 1);
+      if (i < mine) fetch(i, pg);
+      cp_async_commit();
+      pg = next;
+    }
+
+    // q as A fragments, rows g (and g + 8): the values that face a lane's words of K
+    uint32_t qf[DP / 16][2][NR];  // [product][k 2 t .., 2 t + 8 ..][row]
+    float base136[NG][NR];        // 4 bits: -136 sum of a row's q over 32 values
+#pragma unroll
+    for (int x = 0; x < NR; ++x) {
+      const int r = row0 + g + 8 * x;
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (r < a.R ? row_at(a, b, hk, r) : 0);
+#pragma unroll
+      for (int j = 0; j < NG; ++j) {
+        // 4 bits: word t of chunk j, values 32 j + 8 t + ..; bf16: chunk t + 4 j, values 8 (t + 4 j) + ..
+        const int d = 32 * j + 8 * t;
+        const uint4 v = r < a.R && d < a.D ? *reinterpret_cast<const uint4*>(q + d) : make_uint4(0, 0, 0, 0);
+        if constexpr (I4) {
+          // pairs (n, n + 4)
+          qf[2 * j][0][x] = __byte_perm(v.x, v.z, 0x5410), qf[2 * j][1][x] = __byte_perm(v.x, v.z, 0x7632);
+          qf[2 * j + 1][0][x] = __byte_perm(v.y, v.w, 0x5410), qf[2 * j + 1][1][x] = __byte_perm(v.y, v.w, 0x7632);
+          float sum = lo16(v.x) + hi16(v.x) + lo16(v.y) + hi16(v.y) + lo16(v.z) + hi16(v.z) + lo16(v.w) + hi16(v.w);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+          base136[j][x] = -136.f * sum;
+        } else {
+          qf[2 * j][0][x] = v.x, qf[2 * j][1][x] = v.y, qf[2 * j + 1][0][x] = v.z, qf[2 * j + 1][1][x] = v.w;
+        }
+      }
+    }
+    float acc[DP / 16][NR][4], m[NR], l[NR];
+    int last[NR];  // last key that the row sees
+#pragma unroll
+    for (int x = 0; x < NR; ++x) {
+      m[x] = -INFINITY, l[x] = 0.f;
+      last[x] = min(k1 - 1, old + (row0 + g + 8 * x) / a.G);
+#pragma unroll
+      for (int n = 0; n < DP / 16; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[n][x][e] = 0.f;
+    }
+    for (int i = 0; i < mine; ++i) {
+      cp_async_wait<kStages - 2>();
+      __syncwarp();
+      {
+        const int next = lookup(i + kStages);
+        if (i + kStages - 1 < mine) fetch(i + kStages - 1, pg);  // over the stage read in the pass before
+        cp_async_commit();
+        pg = next;
+      }
+      const uint32_t st = ring + i % kStages * St::bytes;
+      const int j0 = wk.k0 + (w + 4 * i) * KS;
+      float s[NT][NR][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (I4) {
+          uint32_t sc[NG];  // steps of keys 2 t and 2 t + 1, two groups to a word
+          if constexpr (NG == 4) {
+            const uint4 v = lds128(st + St::ks + (8 * n + 2 * t) * St::step);
+            sc[0] = v.x, sc[1] = v.y, sc[2] = v.z, sc[3] = v.w;
+          } else {
+            const uint2 v = lds64(st + St::ks + (8 * n + 2 * t) * St::step);
+            sc[0] = v.x, sc[1] = v.y;
+          }
+#pragma unroll
+          for (int x = 0; x < NR; ++x) s[n][x][0] = s[n][x][1] = 0.f;
+#pragma unroll
+          for (int j = 0; j < NG; ++j) {
+            const uint32_t k = lds32(st + St::at(8 * n + g, j) + 4 * t);
+            const float c0 = base136[j][0], c2 = NR == 2 ? base136[j][NR - 1] : 0.f;
+            mma(d, qf[2 * j][0][0], NR == 2 ? qf[2 * j][0][NR - 1] : 0u, qf[2 * j][1][0], NR == 2 ? qf[2 * j][1][NR - 1] : 0u,
+                codes136(k, 0), codes136(k, 1), c0, c0, c2, c2);
+            mma(d, qf[2 * j + 1][0][0], NR == 2 ? qf[2 * j + 1][0][NR - 1] : 0u, qf[2 * j + 1][1][0],
+                NR == 2 ? qf[2 * j + 1][1][NR - 1] : 0u, codes136(k, 2), codes136(k, 3), d[0], d[1], d[2], d[3]);
+            const float e0 = j & 1 ? hi16(sc[j / 2]) : lo16(sc[j / 2]);
+            const float e1 = j & 1 ? hi16(sc[NG / 2 + j / 2]) : lo16(sc[NG / 2 + j / 2]);
+#pragma unroll
+            for (int x = 0; x < NR; ++x)
+              s[n][x][0] = fmaf(d[2 * x], e0, s[n][x][0]), s[n][x][1] = fmaf(d[2 * x + 1], e1, s[n][x][1]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < NG; ++j) {
+            const uint4 k = lds128(st + St::at(8 * n + g, t + 4 * j));
+            mma(d, qf[2 * j][0][0], NR == 2 ? qf[2 * j][0][NR - 1] : 0u, qf[2 * j][1][0], NR == 2 ? qf[2 * j][1][NR - 1] : 0u, k.x,
+                k.y, d[0], d[1], d[2], d[3]);
+            mma(d, qf[2 * j + 1][0][0], NR == 2 ? qf[2 * j + 1][0][NR - 1] : 0u, qf[2 * j + 1][1][0],
+                NR == 2 ? qf[2 * j + 1][1][NR - 1] : 0u, k.z, k.w, d[0], d[1], d[2], d[3]);
+          }
+#pragma unroll
+          for (int x = 0; x < NR; ++x) s[n][x][0] = d[2 * x], s[n][x][1] = d[2 * x + 1];
+        }
+      }
+      const bool edge = j0 + KS - 1 > old || j0 + KS > k1;  // new tokens' causal order, the segment's end
+      bool raise = false;
+      float f[NR];
+#pragma unroll
+      for (int x = 0; x < NR; ++x) {
+        if (edge) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (j0 + 8 * n + 2 * t + e > last[x]) s[n][x][e] = -INFINITY;
+        }
+        float top = fmaxf(s[0][x][0], s[0][x][1]);
+#pragma unroll
+        for (int n = 1; n < NT; ++n) top = fmaxf(top, fmaxf(s[n][x][0], s[n][x][1]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)) * a.c;
+        f[x] = 1.f;
+        if (top - m[x] > 8.f) {  // see the prompt kernel: P at most 2^8
+          f[x] = ex2(m[x] - top);
+          m[x] = top;
+          raise = true;
+        }
+      }
+      if (__any_sync(0xffffffffu, raise)) {  // the accumulators' rows are 2 t and 2 t + 1
+#pragma unroll
+        for (int x = 0; x < NR; ++x) {
+          l[x] *= f[x];
+          const float f0 = __shfl_sync(0xffffffffu, f[x], 8 * t), f1 = __shfl_sync(0xffffffffu, f[x], 8 * t + 4);
+#pragma unroll
+          for (int n = 0; n < DP / 16; ++n) acc[n][x][0] *= f0, acc[n][x][1] *= f1, acc[n][x][2] *= f0, acc[n][x][3] *= f1;
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < NR; ++x) {
+        const float base = m[x] == -INFINITY ? 0.f : m[x];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          s[n][x][0] = ex2(fmaf(s[n][x][0], a.c, -base)), s[n][x][1] = ex2(fmaf(s[n][x][1], a.c, -base));
+          l[x] += s[n][x][0] + s[n][x][1];
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < KS / 16; ++h) {  // 16 keys: this lane's are 16 h + 2 t, + 1, + 8, + 9
+        const int r = 16 * h + 2 * t;
+        if constexpr (I4) {
+          uint32_t sc[2][NG];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            if constexpr (NG == 4) {
+              const uint4 v = lds128(st + St::vs + (r + 8 * y) * St::step);
+              sc[y][0] = v.x, sc[y][1] = v.y, sc[y][2] = v.z, sc[y][3] = v.w;
+            } else {
+              const uint2 v = lds64(st + St::vs + (r + 8 * y) * St::step);
+              sc[y][0] = v.x, sc[y][1] = v.y;
+            }
+          }
+          const uint32_t half = g & 1 ? 0x7632 : 0x5410;
+#pragma unroll
+          for (int j = 0; j < NG; ++j) {
+            uint32_t pf[NR][2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const float e0 = j & 1 ? hi16(sc[y][j / 2]) : lo16(sc[y][j / 2]);
+              const float e1 = j & 1 ? hi16(sc[y][NG / 2 + j / 2]) : lo16(sc[y][NG / 2 + j / 2]);
+#pragma unroll
+              for (int x = 0; x < NR; ++x) pf[x][y] = pack_bf16(s[2 * h + y][x][0] * e0, s[2 * h + y][x][1] * e1);
+            }
+            // values 32 j + 4 g .. + 3 of the four keys
+            const uint32_t at = st + St::v + 4 * (g / 2);
+            const uint32_t v0 = __byte_perm(lds32(at + St::at(r, j)), lds32(at + St::at(r + 1, j)), half);
+            const uint32_t v1 = __byte_perm(lds32(at + St::at(r + 8, j)), lds32(at + St::at(r + 9, j)), half);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const uint32_t a0 = codes(v0, 2 * y), a1 = codes(v0, 2 * y + 1), a2 = codes(v1, 2 * y), a3 = codes(v1, 2 * y + 1);
+#pragma unroll
+              for (int x = 0; x < NR; ++x) {
+                float(&c)[4] = acc[2 * j + y][x];
+                mma(c, a0, a1, a2, a3, pf[x][0], pf[x][1], c[0], c[1], c[2], c[3]);
+              }
+            }
+          }
+        } else {
+          uint32_t pf[NR][2];
+#pragma unroll
+          for (int x = 0; x < NR; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) pf[x][y] = pack_bf16(s[2 * h + y][x][0], s[2 * h + y][x][1]);
+#pragma unroll
+          for (int j = 0; j < DP / 64; ++j) {  // values 8 (g + 8 j) .. + 7
+            const uint4 v0 = lds128(st + St::v + St::at(r, g + 8 * j)), v1 = lds128(st + St::v + St::at(r + 1, g + 8 * j));
+            const uint4 v2 = lds128(st + St::v + St::at(r + 8, g + 8 * j)), v3 = lds128(st + St::v + St::at(r + 9, g + 8 * j));
+            const uint32_t u0[4] = {v0.x, v0.y, v0.z, v0.w}, u1[4] = {v1.x, v1.y, v1.z, v1.w};
+            const uint32_t u2[4] = {v2.x, v2.y, v2.z, v2.w}, u3[4] = {v3.x, v3.y, v3.z, v3.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const uint32_t a0 = __byte_perm(u0[y], u1[y], 0x5410), a1 = __byte_perm(u0[y], u1[y], 0x7632);
+              const uint32_t a2 = __byte_perm(u2[y], u3[y], 0x5410), a3 = __byte_perm(u2[y], u3[y], 0x7632);
+#pragma unroll
+              for (int x = 0; x < NR; ++x) {
+                float(&c)[4] = acc[4 * j + y][x];
+                mma(c, a0, a1, a2, a3, pf[x][0], pf[x][1], c[0], c[1], c[2], c[3]);
+              }
+            }
+          }
+        }
+      }
+      __syncwarp();
+    }
+    cp_async_wait<0>();
+    // the four warps' pieces: maxima and sums, then the scaled accumulators
+    float* ml = reinterpret_cast<float*>(sm);  // [4][kQ][2]
+    float* part = ml + 4 * kQ * 2;             // [4][kQ][DP]
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < NR; ++x) {
+      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+      if (t == 0) {
+        float* p = ml + (w * kQ + g + 8 * x) * 2;
+        p[0] = m[x], p[1] = l[x];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < NR; ++x)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * x + 2 * t + e;
+        float top = -INFINITY;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) top = fmaxf(top, ml[(p * kQ + r) * 2]);
+        const float mine_m = ml[(w * kQ + r) * 2], f = mine_m == -INFINITY ? 0.f : ex2(mine_m - top);
+#pragma unroll
+        for (int n = 0; n < DP / 16; ++n) {
+          const int d = I4 ? 32 * (n / 2) + 4 * g + 2 * (n % 2) : 8 * (g + 8 * (n / 4)) + 2 * (n % 4);
+          *reinterpret_cast<float2*>(part + (w * kQ + r) * DP + d) = make_float2(acc[n][x][e] * f, acc[n][x][2 + e] * f);
+        }
+      }
+    __syncthreads();
+    const long slot = wk.whole ? 0 : slot_of(a, wk) * kQ;
+    for (int i = threadIdx.x; i < kQ * (DP / 4); i += kThreads) {
+      const int rl = i / (DP / 4), c = i % (DP / 4) * 4, r = row0 + rl;
+      if (r >= a.R || c >= a.D) continue;
+      float top = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) top = fmaxf(top, ml[(p * kQ + rl) * 2]);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        // a piece without keys adds 0; one whose scores are all NaN has m = -inf too, and adds its l
+        const float mp = ml[(p * kQ + rl) * 2], base = top == -INFINITY ? 0.f : top;
+        sum = fmaf(ex2(mp - base), ml[(p * kQ + rl) * 2 + 1], sum);
+        const float4 y = *reinterpret_cast<const float4*>(part + (p * kQ + rl) * DP + c);
+        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+      }
+      if (wk.whole) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + row_at(a, b, hk, r) + c) =
+            make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
+      } else {
+        *reinterpret_cast<float4*>(a.acc + (slot + rl) * a.D + c) = x;
+        if (c == 0) a.ml[2 * (slot + rl)] = top, a.ml[2 * (slot + rl) + 1] = sum;
+      }
+    }
+    __syncthreads();
+  }
+}
+
 // ---------------------------------------------------------------- host
 
+bool use_mma(const AttnPagedProblem& p, const PagedCache& c) {
+  if (!p.bf16) return false;
+  if (c.format == GDN_CACHE_I4) return c.D == 64 || c.D == 128;  // its alignment is the format's
+  if (c.D % 8 || (uintptr_t)c.k & 15 || (uintptr_t)c.v & 15) return false;
+  for (int i = 0; i < 3; ++i)
+    if (c.ks[i] % 8 || c.vs[i] % 8) return false;
+  return true;
+}
+
 struct Plan {
+  bool mma;
   int rows, blocks, ctas;  // query rows per CTA, row blocks (grid.y), CTAs that share the units (grid.x)
 };
 
+// CTAs that run at once on an SM: CUDA cores 4; mma bf16 2, 4 bits 4 (8 rows) or 3.
 Plan plan_of(const AttnPagedProblem& p, const PagedCache& c) {
   Plan q;
   const int R = p.H / c.Hkv * p.T;
-  q.rows = kRows;
+  q.mma = use_mma(p, c);
+  q.rows = !q.mma ? kRows : R <= 8 ? 8 : 16;
   q.blocks = (R + q.rows - 1) / q.rows;
-  q.ctas = ctas_for(p.B, c.Hkv, (long)p.pt.max_pages * c.page, q.blocks, 4);
+  const int per_sm = !q.mma ? 4 : c.format != GDN_CACHE_I4 ? 2 : q.rows == 8 ? 4 : 3;
+  q.ctas = ctas_for(p.B, c.Hkv, (long)p.pt.max_pages * c.page, q.blocks, per_sm);
   return q;
+}
+
+template <bool I4>
+cudaError_t launch_mma(const Args& a, const Plan& pl, cudaStream_t s) {
+  const dim3 grid(pl.ctas, pl.blocks);
+  auto go = [&](auto kernel, int smem) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) kernel<<<grid, kThreads, smem, s>>>(a);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+  };
+  // the ring, or the four warps' pieces
+  auto smem = [&](int stage, int DP) {
+    return std::max(4 * kStages * stage, 4 * pl.rows * (DP + 2) * (int)sizeof(float));
+  };
+  if (a.D <= 64) {
+    const int n = smem(Stage<64, I4>::bytes, 64);
+    return pl.rows == 8 ? go(attn_paged_mma_kernel<64, 1, I4>, n) : go(attn_paged_mma_kernel<64, 2, I4>, n);
+  }
+  const int n = smem(Stage<128, I4>::bytes, 128);
+  return pl.rows == 8 ? go(attn_paged_mma_kernel<128, 1, I4>, n) : go(attn_paged_mma_kernel<128, 2, I4>, n);
 }
 
 template <typename T>
@@ -233,14 +668,17 @@ cudaError_t run(const AttnPagedProblem& p, const PagedCache& c, cudaStream_t s) 
   a.acc = reinterpret_cast<float*>(ws + ws_starts(pl.blocks, pl.ctas) + ws_ml(pl.blocks, pl.ctas, pl.rows));
   const dim3 grid(pl.ctas, pl.blocks);
   const bool i4 = c.format == GDN_CACHE_I4;
+  cudaError_t e = cudaSuccess;
   prof_before(s);
-  if (c.D <= 64)
+  if (pl.mma)
+    e = i4 ? launch_mma<true>(a, pl, s) : launch_mma<false>(a, pl, s);
+  else if (c.D <= 64)
     i4 ? attn_paged_simt_kernel<T, I4, 64><<<grid, kThreads, 0, s>>>(a)
        : attn_paged_simt_kernel<T, T, 64><<<grid, kThreads, 0, s>>>(a);
   else
     i4 ? attn_paged_simt_kernel<T, I4, 128><<<grid, kThreads, 0, s>>>(a)
        : attn_paged_simt_kernel<T, T, 128><<<grid, kThreads, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaGetLastError();
   prof_after(s, kAttnPaged);
   if (e != cudaSuccess || pl.ctas == 1) return e;
   prof_before(s);
