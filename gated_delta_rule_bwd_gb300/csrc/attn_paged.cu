@@ -9,6 +9,8 @@
 // with the cache.  Work split: the batch's units of 64 keys evenly over the CTAs,
 // and a second kernel that joins what is split (attn_split.cuh).
 
+#include <type_traits>
+
 #include "attn_split.cuh"
 #include "paged.cuh"
 
@@ -29,6 +31,7 @@ struct Args {
   float c;                       // scale log2 e
   long long table_stride;
   long long ks[3], vs[3], kss[3], vss[3];  // page, token, head
+  uint32_t k16[3], v16[3], ksr[3], vsr[3]; // tensor path: the same in 16-byte vectors, and in a key's steps
   const int *table, *lens;
   const void *q, *k, *v;
   const __nv_bfloat16 *k_scale, *v_scale;
@@ -204,28 +207,42 @@ __global__ void __launch_bounds__(kThreads) attn_paged_simt_kernel(Args a) {
 // for tcgen05's 128-row tiles to do: mma.m16n8k16 takes them.  A lane is (g, t) =
 // (lane / 4, lane % 4) in the fragments below.
 //
-//   S = Q K^T: the M = 16 rows are queries (NR = 1: 8 of them and 8 of zeros), N = 8
-//   keys.  Lane (g, t) gets row g (and g + 8) and keys 2 t, 2 t + 1, which is what
-//   O^T = V^T P^T wants of P as its B operand: M = 16 of the D values, N = 8 rows,
-//   K = 16 keys.  P never leaves its lane.
-//   The order of the D values within a product is free.  A lane takes whole words of
-//   a key's row (both K's and V's), so that nothing is moved for the fragments' sake.
+//   S^T = K Q^T: M = 16 keys, N = 8 query rows (NR tiles of them), K = 16 of the D
+//   values.  Lane (g, t) gets keys g and g + 8 of rows 2 t and 2 t + 1.
+//   O^T = V^T P^T: M = 16 of the D values, N = 8 rows, K = 16 keys; P comes from S^T by
+//   movmatrix (8 x 8 transpositions between registers), and the accumulators' rows
+//   are 2 t and 2 t + 1 again, so that a lane scales its own.
+//   Few rows fill N = 8 better than M = 16, and what is made anew for each product,
+//   K's and V's fragments, are whole A operands: with q there, half of it zeros for
+//   8 rows, the registers were moved together again for each product.
 //
-// 4 bits.  A word holds 8 codes; w >> 4 n & 0x000f000f, put into the mantissas of two
-// bf16 128s, is 128 + (code + 8) of values n and n + 4: one shift and one logic
-// operation for two.  Steps go to the scores: per 32 values
-//   s += step (sum_d q_d (136 + code_d) - 136 sum_d q_d),
-// the second sum as the accumulator's start, once per segment (the products are
-// exact; 136 against codes of about 3 costs the fp32 sum over 32 values some 6 of
-// its 24 bits, and bf16 q has 8).  For V the 136 is taken off before the product: sums
-// over thousands of keys of one sign would drown what is left of codes that cancel.
-// Its steps go to the probabilities, p step in fp32, rounded once to bf16: one weight
-// per key, row and 32 values.
+// bf16: fragments by ldmatrix (V transposed on the way).
+// 4 bits: the order of the D values within a product is free, and a lane takes whole
+// words.  A word holds 8 codes; w >> 4 n & 0x000f000f, put into the mantissas of two
+// bf16 128s, is 128 + (code + 8) = 136 + code of values n and n + 4: one shift and one
+// logic operation for two.  For K the products take that as it is, and the steps go
+// to the scores, per 32 values
+//   s = sum_j step_j (sum_d q_d (136 + code_d)) - sum_j step_j 136 sum_d q_d,
+// the second sum (j the key's groups) as one product of the steps with 136 sum q in
+// three bf16 terms.  136 against codes of about 3 costs the fp32 sum over 32 values
+// some 6 of its 24 bits; bf16 q has 8.  For V the 136 is taken off before the
+// product: sums over thousands of keys of one sign would drown what is left of codes
+// that cancel.  Its steps go to the probabilities, p step in fp32, rounded once to
+// bf16: one weight per key, row and 32 values.
 //
 // Each warp streams its own blocks of KS keys (w, w + 4, ...) through a ring of
 // kStages stages (cp.async) and keeps its own m, l and accumulators, so the warps
 // meet only at a segment's end.
-constexpr int kStages = 3;
+#ifndef KEYS4
+#define KEYS4 32
+#endif
+#ifndef PER4
+#define PER4 3
+#endif
+#ifndef STAGES
+#define STAGES 3
+#endif
+constexpr int kStages = STAGES, kKeys4 = KEYS4;
 
 template <int n>
 __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool valid) {
@@ -249,17 +266,34 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
-                                    float c0, float c1, float c2, float c3) {
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {  // d += a b
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {  // d = a b
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 // 128 + (code + 8) of two codes as bf16, and the codes
 __device__ __forceinline__ uint32_t codes136(uint32_t w, int n) { return ((w >> (4 * n)) & 0x000f000fu) | 0x43004300u; }
@@ -273,63 +307,93 @@ __device__ __forceinline__ float hi16(uint32_t v) { return __uint_as_float(v & 0
 
 template <int DP, bool I4>
 struct Stage {
-  static constexpr int KS = I4 ? 32 : 16;          // keys
+  static constexpr int KS = I4 ? kKeys4 : 16;       // keys
   static constexpr int row = I4 ? DP / 2 : DP * 2;  // bytes of a key's row
   static constexpr int NC = row / 16;               // 16-byte chunks of it
-  static constexpr int step = I4 ? DP / 16 : 0;     // bytes of a key's steps
+  using Steps = std::conditional_t<DP == 128, uint2, uint32_t>;  // a key's steps (4 bits)
+  static constexpr int step = I4 ? (int)sizeof(Steps) : 0;
   static constexpr int v = KS * row, ks = 2 * v, vs = ks + KS * step, bytes = vs + KS * step;
-  // Chunk c of key r lies at c ^ f(r), so that the lanes of a load (eight keys' words
-  // of one chunk; two words each of four keys two apart) meet no bank twice.
-  __device__ __forceinline__ static uint32_t at(int r, int c) {
-    const int f = !I4 ? (r & 6) ^ ((r & 1) << 2) : DP == 128 ? (r >> 1) & 3 : (r >> 2) & 1;
-    return r * row + ((c ^ f) << 4);
+  // Chunk c of key r lies at c ^ f(r), so that the lanes of a load (bf16: eight keys'
+  // chunks; 4 bits: eight keys' words of a chunk, two words each of four keys two
+  // apart) meet no bank twice.
+  // The same for r + 8; 4 bits: for r + 1 of an even r.
+  __device__ __forceinline__ static uint32_t f(int r) {
+    return (!I4 ? r & 7 : DP == 128 ? (r >> 1) & 3 : (r >> 2) & 1) << 4;
   }
+  __device__ __forceinline__ static uint32_t at(int r, int c) { return r * row + ((c << 4) ^ f(r)); }
 };
 
 template <int DP, int NR, bool I4>
-__global__ void __launch_bounds__(kThreads, I4 ? (NR == 1 ? 4 : 3) : 2) attn_paged_mma_kernel(Args a) {
+__global__ void __launch_bounds__(kThreads, I4 ? (NR == 1 ? PER4 : 3) : 2) attn_paged_mma_kernel(Args a) {
   using St = Stage<DP, I4>;
-  constexpr int KS = St::KS, NG = DP / 32, NT = KS / 8, kQ = 8 * NR;  // kQ: query rows per CTA
+  constexpr int KS = St::KS, NG = DP / 32, NT = KS / 16, kQ = 8 * NR;  // kQ: query rows per CTA
   extern __shared__ __align__(128) unsigned char sm[];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane / 4, t = lane % 4, row0 = blockIdx.y * kQ;
   const uint32_t ring = smem_u32(sm) + w * kStages * St::bytes;
   grid_dep_launch();
   empty_rows<__nv_bfloat16>(a);
   if (threadIdx.x == 0) a.starts[(long)blockIdx.y * gridDim.x + blockIdx.x].x = -1;
+  __shared__ Walk<Args> kept;  // not in registers while a segment runs
   Walk<Args> wk;
   if (!wk.init(a)) return;
   while (wk.segment(a)) {
-    const int b = wk.b, hk = wk.hk, old = wk.keys - a.T, k1 = wk.k1;
-    const unsigned char* kb = static_cast<const unsigned char*>(a.k) + hk * a.ks[2] * (I4 ? 1 : 2);
-    const unsigned char* vb = static_cast<const unsigned char*>(a.v) + hk * a.vs[2] * (I4 ? 1 : 2);
-    const int blocks = (k1 - wk.k0 + KS - 1) / KS;  // this warp's are w, w + 4, ...
+    const int b = wk.b, hk = wk.hk, old = wk.keys - a.T, k0 = wk.k0, k1 = wk.k1;
+    if (threadIdx.x == 0) kept = wk;
+    using Steps = typename St::Steps;
+    const uint4* kb = static_cast<const uint4*>(a.k) + (size_t)hk * a.k16[2];
+    const uint4* vb = static_cast<const uint4*>(a.v) + (size_t)hk * a.v16[2];
+    const Steps* ksb = reinterpret_cast<const Steps*>(a.k_scale) + (size_t)hk * a.ksr[2];
+    const Steps* vsb = reinterpret_cast<const Steps*>(a.v_scale) + (size_t)hk * a.vsr[2];
+    const int blocks = (k1 - k0 + KS - 1) / KS;  // this warp's are w, w + 4, ...
     const int mine = blocks > w ? (blocks - w + 3) / 4 : 0;
 
     // the page of this lane's key of block i
     auto lookup = [&](int i) {
-      const int j = wk.k0 + (w + 4 * i) * KS + lane % KS;
+      const int j = k0 + (w + 4 * i) * KS + lane % KS;
       return i < mine && j < k1 ? a.page_of(b, j) : -1;
     };
     // block i into its stage; pg: lookup(i)
     auto fetch = [&](int i, int pg) {
-      const int j0 = wk.k0 + (w + 4 * i) * KS, mask = (1 << a.shift) - 1;
+      const int j0 = k0 + (w + 4 * i) * KS, mask = (1 << a.shift) - 1;
       const uint32_t dst = ring + i % kStages * St::bytes;
-      const int c = lane % St::NC;
+      constexpr int RS = 32 / St::NC;  // rows of the warp's copies at once
+      const int c = lane % St::NC, r0 = lane / St::NC;
+      const int p0 = __shfl_sync(0xffffffffu, pg, 0);
+      if (mask >= KS - 1 && j0 + KS <= k1 && p0 >= 0 && a.D == DP) {  // a whole block in one page
+        const uint32_t at = j0 & mask;
+        const uint4* ks = kb + (uint64_t)p0 * a.k16[0] + (uint64_t)(at + r0) * a.k16[1] + c;
+        const uint4* vs = vb + (uint64_t)p0 * a.v16[0] + (uint64_t)(at + r0) * a.v16[1] + c;
 #pragma unroll
-      for (int r = lane / St::NC; r < KS; r += 32 / St::NC) {
-        const int p = __shfl_sync(0xffffffffu, pg, r), at = (j0 + r) & mask;
+        for (int r = 0; r < KS; r += RS) {
+          const uint32_t to = dst + (RS % 8 == 0 ? r * St::row + St::at(r0, c) : St::at(r0 + r, c));
+          cp_async<16>(to, ks, true);
+          cp_async<16>(to + St::v, vs, true);
+          ks += (size_t)RS * a.k16[1], vs += (size_t)RS * a.v16[1];
+        }
+        if constexpr (I4) {
+          const uint32_t r = lane % KS;
+          if (lane < KS)
+            cp_async<St::step>(dst + St::ks + r * St::step, ksb + (uint64_t)p0 * a.ksr[0] + (uint64_t)(at + r) * a.ksr[1], true);
+          if (lane >= 32 - KS)
+            cp_async<St::step>(dst + St::vs + r * St::step, vsb + (uint64_t)p0 * a.vsr[0] + (uint64_t)(at + r) * a.vsr[1], true);
+        }
+        return;
+      }
+#pragma unroll 1
+      for (int r = r0; r < KS; r += RS) {
+        const int p = __shfl_sync(0xffffffffu, pg, r);
+        const uint32_t at = (j0 + r) & mask;
         const bool in = p >= 0 && c * (I4 ? 32 : 8) < a.D;
-        const unsigned char* ks = kb + (p * a.ks[0] + at * a.ks[1]) * (I4 ? 1 : 2) + c * 16;
-        const unsigned char* vs = vb + (p * a.vs[0] + at * a.vs[1]) * (I4 ? 1 : 2) + c * 16;
-        cp_async<16>(dst + St::at(r, c), in ? ks : kb, in);
-        cp_async<16>(dst + St::v + St::at(r, c), in ? vs : vb, in);
+        cp_async<16>(dst + St::at(r, c), in ? kb + (uint64_t)p * a.k16[0] + (uint64_t)at * a.k16[1] + c : kb, in);
+        cp_async<16>(dst + St::v + St::at(r, c), in ? vb + (uint64_t)p * a.v16[0] + (uint64_t)at * a.v16[1] + c : vb, in);
       }
       if constexpr (I4) {
-        const int at = (j0 + lane) & mask;
+        const uint32_t r = lane % KS, at = (j0 + r) & mask;
         const bool in = pg >= 0;
-        const __nv_bfloat16 *ks = a.k_scale + hk * a.kss[2], *vs = a.v_scale + hk * a.vss[2];
-        cp_async<St::step>(dst + St::ks + lane * St::step, in ? ks + pg * a.kss[0] + at * a.kss[1] : ks, in);
-        cp_async<St::step>(dst + St::vs + lane * St::step, in ? vs + pg * a.vss[0] + at * a.vss[1] : vs, in);
+        if (lane < KS)
+          cp_async<St::step>(dst + St::ks + r * St::step, in ? ksb + (uint64_t)pg * a.ksr[0] + (uint64_t)at * a.ksr[1] : ksb, in);
+        if (lane >= 32 - KS)
+          cp_async<St::step>(dst + St::vs + r * St::step, in ? vsb + (uint64_t)pg * a.vsr[0] + (uint64_t)at * a.vsr[1] : vsb, in);
       }
     };
     int pg = lookup(0);
@@ -341,42 +405,61 @@ __global__ void __launch_bounds__(kThreads, I4 ? (NR == 1 ? 4 : 3) : 2) attn_pag
       pg = next;
     }
 
-    // q as A fragments, rows g (and g + 8): the values that face a lane's words of K
-    uint32_t qf[DP / 16][2][NR];  // [product][k 2 t .., 2 t + 8 ..][row]
-    float base136[NG][NR];        // 4 bits: -136 sum of a row's q over 32 values
+    // q as B fragments, row g of tile x: the values that face a lane's words of K
+    uint32_t qf[DP / 16][NR][2], base[NR][2];  // base (4 bits): -136 sum q of the groups, see below
 #pragma unroll
     for (int x = 0; x < NR; ++x) {
       const int r = row0 + g + 8 * x;
       const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (r < a.R ? row_at(a, b, hk, r) : 0);
+      if constexpr (I4) {
+        float sum[NG];
 #pragma unroll
-      for (int j = 0; j < NG; ++j) {
-        // 4 bits: word t of chunk j, values 32 j + 8 t + ..; bf16: chunk t + 4 j, values 8 (t + 4 j) + ..
-        const int d = 32 * j + 8 * t;
-        const uint4 v = r < a.R && d < a.D ? *reinterpret_cast<const uint4*>(q + d) : make_uint4(0, 0, 0, 0);
-        if constexpr (I4) {
-          // pairs (n, n + 4)
-          qf[2 * j][0][x] = __byte_perm(v.x, v.z, 0x5410), qf[2 * j][1][x] = __byte_perm(v.x, v.z, 0x7632);
-          qf[2 * j + 1][0][x] = __byte_perm(v.y, v.w, 0x5410), qf[2 * j + 1][1][x] = __byte_perm(v.y, v.w, 0x7632);
-          float sum = lo16(v.x) + hi16(v.x) + lo16(v.y) + hi16(v.y) + lo16(v.z) + hi16(v.z) + lo16(v.w) + hi16(v.w);
-          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          base136[j][x] = -136.f * sum;
-        } else {
-          qf[2 * j][0][x] = v.x, qf[2 * j][1][x] = v.y, qf[2 * j + 1][0][x] = v.z, qf[2 * j + 1][1][x] = v.w;
+        for (int j = 0; j < NG; ++j) {  // word t of chunk j: values 32 j + 8 t + .., in pairs (n, n + 4)
+          const uint4 v = r < a.R ? *reinterpret_cast<const uint4*>(q + 32 * j + 8 * t) : make_uint4(0, 0, 0, 0);
+          qf[2 * j][x][0] = __byte_perm(v.x, v.z, 0x5410), qf[2 * j][x][1] = __byte_perm(v.x, v.z, 0x7632);
+          qf[2 * j + 1][x][0] = __byte_perm(v.y, v.w, 0x5410), qf[2 * j + 1][x][1] = __byte_perm(v.y, v.w, 0x7632);
+          float y = lo16(v.x) + hi16(v.x) + lo16(v.y) + hi16(v.y) + lo16(v.z) + hi16(v.z) + lo16(v.w) + hi16(v.w);
+          y += __shfl_xor_sync(0xffffffffu, y, 1);
+          y += __shfl_xor_sync(0xffffffffu, y, 2);
+          sum[j] = -136.f * y;
         }
+        // The sums as three terms of 8 bits, against the groups' steps: k = NG i + j is
+        // term i of group j; a lane has k = 2 t, 2 t + 1 and 2 t + 8, 2 t + 9.
+        auto term = [&](int k) {
+          float y = 0.f;
+#pragma unroll
+          for (int j = 0; j < NG; ++j) y = k % NG == j ? sum[j] : y;
+          const float hi = __bfloat162float(__float2bfloat16_rn(y)), mid = __bfloat162float(__float2bfloat16_rn(y - hi));
+          return k / NG == 0 ? hi : k / NG == 1 ? mid : k / NG == 2 ? (y - hi) - mid : 0.f;
+        };
+        base[x][0] = pack_bf16(term(2 * t), term(2 * t + 1));
+        base[x][1] = pack_bf16(term(2 * t + 8), term(2 * t + 9));
+      } else {
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int d = 16 * k + 8 * y + 2 * t;
+            qf[k][x][y] = r < a.R && d < a.D ? *reinterpret_cast<const uint32_t*>(q + d) : 0u;
+          }
       }
     }
-    float acc[DP / 16][NR][4], m[NR], l[NR];
-    int last[NR];  // last key that the row sees
+    float acc[DP / 16][NR][4], m[NR][2], l[NR][2];
+    int last[NR][2];  // last key that the row sees
 #pragma unroll
     for (int x = 0; x < NR; ++x) {
-      m[x] = -INFINITY, l[x] = 0.f;
-      last[x] = min(k1 - 1, old + (row0 + g + 8 * x) / a.G);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[x][e] = -INFINITY, l[x][e] = 0.f;
+        last[x][e] = min(k1 - 1, old + (row0 + 8 * x + 2 * t + e) / a.G);
+      }
 #pragma unroll
       for (int n = 0; n < DP / 16; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[n][x][e] = 0.f;
     }
+    // 4 bits: this lane's words of keys g, .. and of keys 2 t, ..
+    const uint32_t k_at = g * St::row + 4 * t, k_f = St::f(g), v_at = 2 * t * St::row + 4 * (g / 2), v_f = St::f(2 * t);
     for (int i = 0; i < mine; ++i) {
       cp_async_wait<kStages - 2>();
       __syncwarp();
@@ -387,104 +470,115 @@ __global__ void __launch_bounds__(kThreads, I4 ? (NR == 1 ? 4 : 3) : 2) attn_pag
         pg = next;
       }
       const uint32_t st = ring + i % kStages * St::bytes;
-      const int j0 = wk.k0 + (w + 4 * i) * KS;
-      float s[NT][NR][2];
+      const int j0 = k0 + (w + 4 * i) * KS;
+      float s[NT][NR][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
         if constexpr (I4) {
-          uint32_t sc[NG];  // steps of keys 2 t and 2 t + 1, two groups to a word
-          if constexpr (NG == 4) {
-            const uint4 v = lds128(st + St::ks + (8 * n + 2 * t) * St::step);
-            sc[0] = v.x, sc[1] = v.y, sc[2] = v.z, sc[3] = v.w;
-          } else {
-            const uint2 v = lds64(st + St::ks + (8 * n + 2 * t) * St::step);
-            sc[0] = v.x, sc[1] = v.y;
+          uint32_t sc[2][NG / 2];  // steps of keys g and g + 8, two groups to a word
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t at = st + St::ks + (16 * n + 8 * y + g) * St::step;
+            if constexpr (NG == 4) {
+              const uint2 v = lds64(at);
+              sc[y][0] = v.x, sc[y][1] = v.y;
+            } else {
+              sc[y][0] = lds32(at);
+            }
+          }
+          {
+            const uint32_t c0 = NG == 4 && t & 1 ? sc[0][NG / 2 - 1] : sc[0][0], c1 = NG == 4 && t & 1 ? sc[1][NG / 2 - 1] : sc[1][0];
+            const uint32_t steps[4] = {c0, c1, c0, c1};
+#pragma unroll
+            for (int x = 0; x < NR; ++x) mma0(s[n][x], steps, base[x][0], base[x][1]);
           }
 #pragma unroll
-          for (int x = 0; x < NR; ++x) s[n][x][0] = s[n][x][1] = 0.f;
-#pragma unroll
           for (int j = 0; j < NG; ++j) {
-            const uint32_t k = lds32(st + St::at(8 * n + g, j) + 4 * t);
-            const float c0 = base136[j][0], c2 = NR == 2 ? base136[j][NR - 1] : 0.f;
-            mma(d, qf[2 * j][0][0], NR == 2 ? qf[2 * j][0][NR - 1] : 0u, qf[2 * j][1][0], NR == 2 ? qf[2 * j][1][NR - 1] : 0u,
-                codes136(k, 0), codes136(k, 1), c0, c0, c2, c2);
-            mma(d, qf[2 * j + 1][0][0], NR == 2 ? qf[2 * j + 1][0][NR - 1] : 0u, qf[2 * j + 1][1][0],
-                NR == 2 ? qf[2 * j + 1][1][NR - 1] : 0u, codes136(k, 2), codes136(k, 3), d[0], d[1], d[2], d[3]);
-            const float e0 = j & 1 ? hi16(sc[j / 2]) : lo16(sc[j / 2]);
-            const float e1 = j & 1 ? hi16(sc[NG / 2 + j / 2]) : lo16(sc[NG / 2 + j / 2]);
+            const uint32_t at = st + 16 * n * St::row + k_at + ((j << 4) ^ k_f);
+            const uint32_t u0 = lds32(at), u1 = lds32(at + 8 * St::row);
+            const uint32_t f0[4] = {codes136(u0, 0), codes136(u1, 0), codes136(u0, 1), codes136(u1, 1)};
+            const uint32_t f1[4] = {codes136(u0, 2), codes136(u1, 2), codes136(u0, 3), codes136(u1, 3)};
+            const float e0 = j & 1 ? hi16(sc[0][j / 2]) : lo16(sc[0][j / 2]), e1 = j & 1 ? hi16(sc[1][j / 2]) : lo16(sc[1][j / 2]);
 #pragma unroll
-            for (int x = 0; x < NR; ++x)
-              s[n][x][0] = fmaf(d[2 * x], e0, s[n][x][0]), s[n][x][1] = fmaf(d[2 * x + 1], e1, s[n][x][1]);
+            for (int x = 0; x < NR; ++x) {
+              float d[4];
+              mma0(d, f0, qf[2 * j][x][0], qf[2 * j][x][1]);
+              mma(d, f1, qf[2 * j + 1][x][0], qf[2 * j + 1][x][1]);
+              s[n][x][0] = fmaf(d[0], e0, s[n][x][0]), s[n][x][1] = fmaf(d[1], e0, s[n][x][1]);
+              s[n][x][2] = fmaf(d[2], e1, s[n][x][2]), s[n][x][3] = fmaf(d[3], e1, s[n][x][3]);
+            }
           }
         } else {
 #pragma unroll
-          for (int j = 0; j < NG; ++j) {
-            const uint4 k = lds128(st + St::at(8 * n + g, t + 4 * j));
-            mma(d, qf[2 * j][0][0], NR == 2 ? qf[2 * j][0][NR - 1] : 0u, qf[2 * j][1][0], NR == 2 ? qf[2 * j][1][NR - 1] : 0u, k.x,
-                k.y, d[0], d[1], d[2], d[3]);
-            mma(d, qf[2 * j + 1][0][0], NR == 2 ? qf[2 * j + 1][0][NR - 1] : 0u, qf[2 * j + 1][1][0],
-                NR == 2 ? qf[2 * j + 1][1][NR - 1] : 0u, k.z, k.w, d[0], d[1], d[2], d[3]);
-          }
+          for (int k = 0; k < DP / 16; ++k) {
+            uint32_t f[4];
+            ldsm4(f, st + St::at(16 * n + lane % 16, 2 * k + lane / 16));
 #pragma unroll
-          for (int x = 0; x < NR; ++x) s[n][x][0] = d[2 * x], s[n][x][1] = d[2 * x + 1];
+            for (int x = 0; x < NR; ++x)
+              k == 0 ? mma0(s[n][x], f, qf[k][x][0], qf[k][x][1]) : mma(s[n][x], f, qf[k][x][0], qf[k][x][1]);
+          }
         }
       }
       const bool edge = j0 + KS - 1 > old || j0 + KS > k1;  // new tokens' causal order, the segment's end
       bool raise = false;
-      float f[NR];
+      float f[NR][2];
 #pragma unroll
-      for (int x = 0; x < NR; ++x) {
-        if (edge) {
+      for (int x = 0; x < NR; ++x)
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+        for (int e = 0; e < 2; ++e) {
+          if (edge) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if (j0 + 8 * n + 2 * t + e > last[x]) s[n][x][e] = -INFINITY;
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+                if (j0 + 16 * n + 8 * y + g > last[x][e]) s[n][x][2 * y + e] = -INFINITY;
+          }
+          float top = fmaxf(s[0][x][e], s[0][x][2 + e]);
+#pragma unroll
+          for (int n = 1; n < NT; ++n) top = fmaxf(top, fmaxf(s[n][x][e], s[n][x][2 + e]));
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          top *= a.c;
+          f[x][e] = 1.f;
+          if (top - m[x][e] > 8.f) {  // see the prompt kernel: P at most 2^8
+            f[x][e] = ex2(m[x][e] - top);
+            m[x][e] = top;
+            raise = true;
+          }
         }
-        float top = fmaxf(s[0][x][0], s[0][x][1]);
-#pragma unroll
-        for (int n = 1; n < NT; ++n) top = fmaxf(top, fmaxf(s[n][x][0], s[n][x][1]));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)) * a.c;
-        f[x] = 1.f;
-        if (top - m[x] > 8.f) {  // see the prompt kernel: P at most 2^8
-          f[x] = ex2(m[x] - top);
-          m[x] = top;
-          raise = true;
-        }
-      }
-      if (__any_sync(0xffffffffu, raise)) {  // the accumulators' rows are 2 t and 2 t + 1
+      if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int x = 0; x < NR; ++x) {
-          l[x] *= f[x];
-          const float f0 = __shfl_sync(0xffffffffu, f[x], 8 * t), f1 = __shfl_sync(0xffffffffu, f[x], 8 * t + 4);
+          l[x][0] *= f[x][0], l[x][1] *= f[x][1];
 #pragma unroll
-          for (int n = 0; n < DP / 16; ++n) acc[n][x][0] *= f0, acc[n][x][1] *= f1, acc[n][x][2] *= f0, acc[n][x][3] *= f1;
+          for (int n = 0; n < DP / 16; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[n][x][e] *= f[x][e & 1];
         }
       }
 #pragma unroll
-      for (int x = 0; x < NR; ++x) {
-        const float base = m[x] == -INFINITY ? 0.f : m[x];
+      for (int x = 0; x < NR; ++x)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          s[n][x][0] = ex2(fmaf(s[n][x][0], a.c, -base)), s[n][x][1] = ex2(fmaf(s[n][x][1], a.c, -base));
-          l[x] += s[n][x][0] + s[n][x][1];
+        for (int e = 0; e < 2; ++e) {
+          const float low = m[x][e] == -INFINITY ? 0.f : m[x][e];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            s[n][x][e] = ex2(fmaf(s[n][x][e], a.c, -low)), s[n][x][2 + e] = ex2(fmaf(s[n][x][2 + e], a.c, -low));
+            l[x][e] += s[n][x][e] + s[n][x][2 + e];
+          }
         }
-      }
 #pragma unroll
-      for (int h = 0; h < KS / 16; ++h) {  // 16 keys: this lane's are 16 h + 2 t, + 1, + 8, + 9
-        const int r = 16 * h + 2 * t;
+      for (int n = 0; n < NT; ++n) {
         if constexpr (I4) {
-          uint32_t sc[2][NG];
+          uint32_t sc[2][NG / 2];
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
+            const uint32_t at = st + St::vs + (16 * n + 8 * y + g) * St::step;
             if constexpr (NG == 4) {
-              const uint4 v = lds128(st + St::vs + (r + 8 * y) * St::step);
-              sc[y][0] = v.x, sc[y][1] = v.y, sc[y][2] = v.z, sc[y][3] = v.w;
-            } else {
-              const uint2 v = lds64(st + St::vs + (r + 8 * y) * St::step);
+              const uint2 v = lds64(at);
               sc[y][0] = v.x, sc[y][1] = v.y;
+            } else {
+              sc[y][0] = lds32(at);
             }
           }
           const uint32_t half = g & 1 ? 0x7632 : 0x5410;
@@ -493,23 +587,19 @@ __global__ void __launch_bounds__(kThreads, I4 ? (NR == 1 ? 4 : 3) : 2) attn_pag
             uint32_t pf[NR][2];
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              const float e0 = j & 1 ? hi16(sc[y][j / 2]) : lo16(sc[y][j / 2]);
-              const float e1 = j & 1 ? hi16(sc[y][NG / 2 + j / 2]) : lo16(sc[y][NG / 2 + j / 2]);
+              const float e = j & 1 ? hi16(sc[y][j / 2]) : lo16(sc[y][j / 2]);
 #pragma unroll
-              for (int x = 0; x < NR; ++x) pf[x][y] = pack_bf16(s[2 * h + y][x][0] * e0, s[2 * h + y][x][1] * e1);
+              for (int x = 0; x < NR; ++x) pf[x][y] = transposed(pack_bf16(s[n][x][2 * y] * e, s[n][x][2 * y + 1] * e));
             }
-            // values 32 j + 4 g .. + 3 of the four keys
-            const uint32_t at = st + St::v + 4 * (g / 2);
-            const uint32_t v0 = __byte_perm(lds32(at + St::at(r, j)), lds32(at + St::at(r + 1, j)), half);
-            const uint32_t v1 = __byte_perm(lds32(at + St::at(r + 8, j)), lds32(at + St::at(r + 9, j)), half);
+            // values 32 j + 4 g .. + 3 of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+            const uint32_t at = st + St::v + 16 * n * St::row + v_at + ((j << 4) ^ v_f);
+            const uint32_t v0 = __byte_perm(lds32(at), lds32(at + St::row), half);
+            const uint32_t v1 = __byte_perm(lds32(at + 8 * St::row), lds32(at + 9 * St::row), half);
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              const uint32_t a0 = codes(v0, 2 * y), a1 = codes(v0, 2 * y + 1), a2 = codes(v1, 2 * y), a3 = codes(v1, 2 * y + 1);
+              const uint32_t v[4] = {codes(v0, 2 * y), codes(v0, 2 * y + 1), codes(v1, 2 * y), codes(v1, 2 * y + 1)};
 #pragma unroll
-              for (int x = 0; x < NR; ++x) {
-                float(&c)[4] = acc[2 * j + y][x];
-                mma(c, a0, a1, a2, a3, pf[x][0], pf[x][1], c[0], c[1], c[2], c[3]);
-              }
+              for (int x = 0; x < NR; ++x) mma(acc[2 * j + y][x], v, pf[x][0], pf[x][1]);
             }
           }
         } else {
@@ -517,23 +607,13 @@ __global__ void __launch_bounds__(kThreads, I4 ? (NR == 1 ? 4 : 3) : 2) attn_pag
 #pragma unroll
           for (int x = 0; x < NR; ++x)
 #pragma unroll
-            for (int y = 0; y < 2; ++y) pf[x][y] = pack_bf16(s[2 * h + y][x][0], s[2 * h + y][x][1]);
+            for (int y = 0; y < 2; ++y) pf[x][y] = transposed(pack_bf16(s[n][x][2 * y], s[n][x][2 * y + 1]));
 #pragma unroll
-          for (int j = 0; j < DP / 64; ++j) {  // values 8 (g + 8 j) .. + 7
-            const uint4 v0 = lds128(st + St::v + St::at(r, g + 8 * j)), v1 = lds128(st + St::v + St::at(r + 1, g + 8 * j));
-            const uint4 v2 = lds128(st + St::v + St::at(r + 8, g + 8 * j)), v3 = lds128(st + St::v + St::at(r + 9, g + 8 * j));
-            const uint32_t u0[4] = {v0.x, v0.y, v0.z, v0.w}, u1[4] = {v1.x, v1.y, v1.z, v1.w};
-            const uint32_t u2[4] = {v2.x, v2.y, v2.z, v2.w}, u3[4] = {v3.x, v3.y, v3.z, v3.w};
+          for (int k = 0; k < DP / 16; ++k) {
+            uint32_t v[4];
+            ldsm4_trans(v, st + St::v + St::at(16 * n + (lane & 7) + (lane >> 4) * 8, 2 * k + ((lane >> 3) & 1)));
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const uint32_t a0 = __byte_perm(u0[y], u1[y], 0x5410), a1 = __byte_perm(u0[y], u1[y], 0x7632);
-              const uint32_t a2 = __byte_perm(u2[y], u3[y], 0x5410), a3 = __byte_perm(u2[y], u3[y], 0x7632);
-#pragma unroll
-              for (int x = 0; x < NR; ++x) {
-                float(&c)[4] = acc[4 * j + y][x];
-                mma(c, a0, a1, a2, a3, pf[x][0], pf[x][1], c[0], c[1], c[2], c[3]);
-              }
-            }
+            for (int x = 0; x < NR; ++x) mma(acc[k][x], v, pf[x][0], pf[x][1]);
           }
         }
       }
@@ -544,15 +624,18 @@ __global__ void __launch_bounds__(kThreads, I4 ? (NR == 1 ? 4 : 3) : 2) attn_pag
     float* ml = reinterpret_cast<float*>(sm);  // [4][kQ][2]
     float* part = ml + 4 * kQ * 2;             // [4][kQ][DP]
     __syncthreads();
+    wk = kept;
 #pragma unroll
-    for (int x = 0; x < NR; ++x) {
-      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
-      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
-      if (t == 0) {
-        float* p = ml + (w * kQ + g + 8 * x) * 2;
-        p[0] = m[x], p[1] = l[x];
+    for (int x = 0; x < NR; ++x)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], o);
+        if (g == 0) {
+          float* p = ml + (w * kQ + 8 * x + 2 * t + e) * 2;
+          p[0] = m[x][e], p[1] = l[x][e];
+        }
       }
-    }
     __syncthreads();
 #pragma unroll
     for (int x = 0; x < NR; ++x)
@@ -562,11 +645,15 @@ __global__ void __launch_bounds__(kThreads, I4 ? (NR == 1 ? 4 : 3) : 2) attn_pag
         float top = -INFINITY;
 #pragma unroll
         for (int p = 0; p < 4; ++p) top = fmaxf(top, ml[(p * kQ + r) * 2]);
-        const float mine_m = ml[(w * kQ + r) * 2], f = mine_m == -INFINITY ? 0.f : ex2(mine_m - top);
+        const float f = m[x][e] == -INFINITY ? 0.f : ex2(m[x][e] - top);
 #pragma unroll
         for (int n = 0; n < DP / 16; ++n) {
-          const int d = I4 ? 32 * (n / 2) + 4 * g + 2 * (n % 2) : 8 * (g + 8 * (n / 4)) + 2 * (n % 4);
-          *reinterpret_cast<float2*>(part + (w * kQ + r) * DP + d) = make_float2(acc[n][x][e] * f, acc[n][x][2 + e] * f);
+          float* p = part + (w * kQ + r) * DP;
+          if constexpr (I4) {  // rows g and g + 8 of a product are neighbours
+            *reinterpret_cast<float2*>(p + 32 * (n / 2) + 4 * g + 2 * (n % 2)) = make_float2(acc[n][x][e] * f, acc[n][x][2 + e] * f);
+          } else {
+            p[16 * n + g] = acc[n][x][e] * f, p[16 * n + g + 8] = acc[n][x][2 + e] * f;
+          }
         }
       }
     __syncthreads();
@@ -603,10 +690,13 @@ __global__ void __launch_bounds__(kThreads, I4 ? (NR == 1 ? 4 : 3) : 2) attn_pag
 
 bool use_mma(const AttnPagedProblem& p, const PagedCache& c) {
   if (!p.bf16) return false;
-  if (c.format == GDN_CACHE_I4) return c.D == 64 || c.D == 128;  // its alignment is the format's
-  if (c.D % 8 || (uintptr_t)c.k & 15 || (uintptr_t)c.v & 15) return false;
-  for (int i = 0; i < 3; ++i)
-    if (c.ks[i] % 8 || c.vs[i] % 8) return false;
+  const bool i4 = c.format == GDN_CACHE_I4;
+  if (i4 ? c.D != 64 && c.D != 128 : c.D % 8 || (uintptr_t)c.k & 15 || (uintptr_t)c.v & 15) return false;
+  const long long vec = i4 ? 16 : 8, most = vec << 32;  // strides in vectors (and steps) fit 32 bits
+  for (int i = 0; i < 3; ++i) {
+    if (c.ks[i] % vec || c.vs[i] % vec || c.ks[i] >= most || c.vs[i] >= most) return false;
+    if (i4 && (c.kss[i] / (c.D / kStepGroup) > UINT32_MAX || c.vss[i] / (c.D / kStepGroup) > UINT32_MAX)) return false;
+  }
   return true;
 }
 
@@ -622,7 +712,7 @@ Plan plan_of(const AttnPagedProblem& p, const PagedCache& c) {
   q.mma = use_mma(p, c);
   q.rows = !q.mma ? kRows : R <= 8 ? 8 : 16;
   q.blocks = (R + q.rows - 1) / q.rows;
-  const int per_sm = !q.mma ? 4 : c.format != GDN_CACHE_I4 ? 2 : q.rows == 8 ? 4 : 3;
+  const int per_sm = !q.mma ? 4 : c.format != GDN_CACHE_I4 ? 2 : q.rows == 8 ? PER4 : 3;
   q.ctas = ctas_for(p.B, c.Hkv, (long)p.pt.max_pages * c.page, q.blocks, per_sm);
   return q;
 }
@@ -659,6 +749,11 @@ cudaError_t run(const AttnPagedProblem& p, const PagedCache& c, cudaStream_t s) 
   for (int i = 0; i < 3; ++i) {
     a.ks[i] = c.ks[i], a.vs[i] = c.vs[i], a.kss[i] = c.kss[i], a.vss[i] = c.vss[i];
     a.vec = a.vec && c.ks[i] % 4 == 0 && c.vs[i] % 4 == 0;
+    if (pl.mma) {
+      const int vec = c.format == GDN_CACHE_I4 ? 16 : 8, steps = std::max(1, c.D / kStepGroup);
+      a.k16[i] = (uint32_t)(c.ks[i] / vec), a.v16[i] = (uint32_t)(c.vs[i] / vec);
+      a.ksr[i] = (uint32_t)(c.kss[i] / steps), a.vsr[i] = (uint32_t)(c.vss[i] / steps);
+    }
   }
   a.q = p.q, a.k = c.k, a.v = c.v, a.o = p.o;
   a.k_scale = static_cast<const __nv_bfloat16*>(c.k_scale), a.v_scale = static_cast<const __nv_bfloat16*>(c.v_scale);
