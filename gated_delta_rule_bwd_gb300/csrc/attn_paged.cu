@@ -295,13 +295,25 @@ __device__ __forceinline__ uint32_t transposed(uint32_t v) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-// 128 + (code + 8) of two codes as bf16, and the codes
-__device__ __forceinline__ uint32_t codes136(uint32_t w, int n) { return ((w >> (4 * n)) & 0x000f000fu) | 0x43004300u; }
-__device__ __forceinline__ uint32_t codes(uint32_t w, int n) {
-  const uint32_t x = codes136(w, n), o = 0xc308c308u;  // -136
-  const __nv_bfloat162 y = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&o));
-  return *reinterpret_cast<const uint32_t*>(&y);
-}
+// 128 + (code + 8) of two codes as bf16, and the codes.  The constants come as
+// registers: with both as immediates it takes two logic operations.
+struct Magic {
+  uint32_t mask, one;
+  __device__ __forceinline__ Magic() {
+    asm volatile("mov.b32 %0, 0x000f000f;" : "=r"(mask));
+    asm volatile("mov.b32 %0, 0x43004300;" : "=r"(one));
+  }
+  __device__ __forceinline__ uint32_t codes136(uint32_t w, int n) const {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w >> (4 * n)), "r"(mask), "r"(one));
+    return r;
+  }
+  __device__ __forceinline__ uint32_t codes(uint32_t w, int n) const {
+    const uint32_t x = codes136(w, n), o = 0xc308c308u;  // -136
+    const __nv_bfloat162 y = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&o));
+    return *reinterpret_cast<const uint32_t*>(&y);
+  }
+};
 __device__ __forceinline__ float lo16(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi16(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
@@ -460,6 +472,7 @@ __global__ void __launch_bounds__(kThreads, I4 ? (NR == 1 ? PER4 : 3) : 2) attn_
     }
     // 4 bits: this lane's words of keys g, .. and of keys 2 t, ..
     const uint32_t k_at = g * St::row + 4 * t, k_f = St::f(g), v_at = 2 * t * St::row + 4 * (g / 2), v_f = St::f(2 * t);
+    const Magic magic;
     for (int i = 0; i < mine; ++i) {
       cp_async_wait<kStages - 2>();
       __syncwarp();
@@ -496,8 +509,8 @@ __global__ void __launch_bounds__(kThreads, I4 ? (NR == 1 ? PER4 : 3) : 2) attn_
           for (int j = 0; j < NG; ++j) {
             const uint32_t at = st + 16 * n * St::row + k_at + ((j << 4) ^ k_f);
             const uint32_t u0 = lds32(at), u1 = lds32(at + 8 * St::row);
-            const uint32_t f0[4] = {codes136(u0, 0), codes136(u1, 0), codes136(u0, 1), codes136(u1, 1)};
-            const uint32_t f1[4] = {codes136(u0, 2), codes136(u1, 2), codes136(u0, 3), codes136(u1, 3)};
+            const uint32_t f0[4] = {magic.codes136(u0, 0), magic.codes136(u1, 0), magic.codes136(u0, 1), magic.codes136(u1, 1)};
+            const uint32_t f1[4] = {magic.codes136(u0, 2), magic.codes136(u1, 2), magic.codes136(u0, 3), magic.codes136(u1, 3)};
             const float e0 = j & 1 ? hi16(sc[0][j / 2]) : lo16(sc[0][j / 2]), e1 = j & 1 ? hi16(sc[1][j / 2]) : lo16(sc[1][j / 2]);
 #pragma unroll
             for (int x = 0; x < NR; ++x) {
@@ -597,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, I4 ? (NR == 1 ? PER4 : 3) : 2) attn_
             const uint32_t v1 = __byte_perm(lds32(at + 8 * St::row), lds32(at + 9 * St::row), half);
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              const uint32_t v[4] = {codes(v0, 2 * y), codes(v0, 2 * y + 1), codes(v1, 2 * y), codes(v1, 2 * y + 1)};
+              const uint32_t v[4] = {magic.codes(v0, 2 * y), magic.codes(v0, 2 * y + 1), magic.codes(v1, 2 * y), magic.codes(v1, 2 * y + 1)};
 #pragma unroll
               for (int x = 0; x < NR; ++x) mma(acc[2 * j + y][x], v, pf[x][0], pf[x][1]);
             }
