@@ -9,6 +9,8 @@
 // with the cache.  Work split: the batch's units of 64 keys evenly over the CTAs,
 // and a second kernel that joins what is split (attn_split.cuh).
 
+#include <cuda_fp16.h>
+
 #include <type_traits>
 
 #include "attn_split.cuh"
@@ -31,7 +33,8 @@ struct Args {
   float c;                       // scale log2 e
   long long table_stride;
   long long ks[3], vs[3], kss[3], vss[3];  // page, token, head
-  uint32_t k16[3], v16[3], ksr[3], vsr[3]; // tensor path: the same in 16-byte vectors, and in a key's steps
+  uint32_t k16[3], v16[3], ksr[3], vsr[3];  // tensor path: the same in 16-byte vectors, and in a key's steps
+  bool dense;                               // a page's tokens of one head lie together
   const int *table, *lens;
   const void *q, *k, *v;
   const __nv_bfloat16 *k_scale, *v_scale;
@@ -218,17 +221,25 @@ __global__ void __launch_bounds__(kThreads) attn_paged_simt_kernel(Args a) {
 //
 // bf16: fragments by ldmatrix (V transposed on the way).
 // 4 bits: the order of the D values within a product is free, and a lane takes whole
-// words.  A word holds 8 codes; w >> 4 n & 0x000f000f, put into the mantissas of two
-// bf16 128s, is 128 + (code + 8) = 136 + code of values n and n + 4: one shift and one
-// logic operation for two.  For K the products take that as it is, and the steps go
-// to the scores, per 32 values
-//   s = sum_j step_j (sum_d q_d (136 + code_d)) - sum_j step_j 136 sum_d q_d,
-// the second sum (j the key's groups) as one product of the steps with 136 sum q in
-// three bf16 terms.  136 against codes of about 3 costs the fp32 sum over 32 values
-// some 6 of its 24 bits; bf16 q has 8.  For V the 136 is taken off before the
-// product: sums over thousands of keys of one sign would drown what is left of codes
-// that cancel.  Its steps go to the probabilities, p step in fp32, rounded once to
-// bf16: one weight per key, row and 32 values.
+// words of 8 codes, held c = code + 8.
+//   K: a byte below the exponent of an fp16 1024 is X = 1024 + c0 + 16 c1 (two bytes of a
+//   word by one byte permutation), and without its upper four bits L = 1024 + c0 (one
+//   logic operation), so that
+//     q0 c0 + q1 c1 = (q1 / 16) X + (q0 - q1 / 16) L - 1024 (both weights):
+//   half an operation a code.  The weights are fp16 (q scaled by a power of two per row,
+//   so that its largest value is in [1, 2)): the first is exact, the second off by 2^-12 of
+//   itself, which reaches the score as that part of a c0 (q, as bf16, has 2^-9).  The
+//   constants, with the 8 in c, go back once per key, with the steps, which are
+//   applied to the scores:
+//     s = sum_j step_j (sum_d of the group's products) + sum_j step_j base_j,
+//   the second sum (j a key's groups) as one product of the steps with base in three
+//   bf16 terms.  1024 against c of about 3 costs the fp32 sums over a group some 9 of
+//   their 24 bits.
+//   V: w >> 4 n & 0x000f000f (a word of two keys' halves), put into the mantissas of two
+//   bf16 128s, is 128 + c: one shift and one logic operation for two codes.  The 136 is
+//   taken off before the product: sums over thousands of keys of one sign would drown
+//   what is left of codes that cancel.  V's steps go to the probabilities, p step in
+//   fp32, rounded once to bf16: one weight per key, row and 32 values.
 //
 // Each warp streams its own blocks of KS keys (w, w + 4, ...) through a ring of
 // kStages stages (cp.async) and keeps its own m, l and accumulators, so the warps
@@ -278,6 +289,19 @@ __device__ __forceinline__ void mma0(float (&d)[4], const uint32_t (&a)[4], uint
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
+// the same of fp16
+__device__ __forceinline__ void mma0_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -295,8 +319,8 @@ __device__ __forceinline__ uint32_t transposed(uint32_t v) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-// 128 + (code + 8) of two codes as bf16, and the codes.  The constants come as
-// registers: with both as immediates it takes two logic operations.
+// Two codes as bf16, 128 + (code + 8).  The constants come as registers: with both
+// as immediates it takes two logic operations.
 struct Magic {
   uint32_t mask, one;
   __device__ __forceinline__ Magic() {
@@ -304,15 +328,19 @@ struct Magic {
     asm volatile("mov.b32 %0, 0x43004300;" : "=r"(one));
   }
   __device__ __forceinline__ uint32_t codes136(uint32_t w, int n) const {
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w >> (4 * n)), "r"(mask), "r"(one));
-    return r;
+    uint32_t x;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(x) : "r"(w >> (4 * n)), "r"(mask), "r"(one));
+    return x;
   }
+#ifndef X_MMAOFF
   __device__ __forceinline__ uint32_t codes(uint32_t w, int n) const {
-    const uint32_t x = codes136(w, n), o = 0xc308c308u;  // -136
+    const uint32_t x = codes136(w, n), o = 0xc308c308u;
     const __nv_bfloat162 y = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&o));
     return *reinterpret_cast<const uint32_t*>(&y);
   }
+#else
+  __device__ __forceinline__ uint32_t codes(uint32_t w, int n) const { return codes136(w, n); }
+#endif
 };
 __device__ __forceinline__ float lo16(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi16(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
@@ -346,6 +374,8 @@ __global__ void __launch_bounds__(kThreads, I4 ? (NR == 1 ? PER4 : 3) : 2) attn_
   empty_rows<__nv_bfloat16>(a);
   if (threadIdx.x == 0) a.starts[(long)blockIdx.y * gridDim.x + blockIdx.x].x = -1;
   __shared__ Walk<Args> kept;  // not in registers while a segment runs
+  __shared__ uint4 q_frag[I4 ? NG : 1][NR][32];  // 4 bits: q's fragments, group sums and powers of two
+  __shared__ float q_sum[kQ][NG], q_up[kQ];
   Walk<Args> wk;
   if (!wk.init(a)) return;
   while (wk.segment(a)) {
@@ -372,22 +402,32 @@ __global__ void __launch_bounds__(kThreads, I4 ? (NR == 1 ? PER4 : 3) : 2) attn_
       const int c = lane % St::NC, r0 = lane / St::NC;
       const int p0 = __shfl_sync(0xffffffffu, pg, 0);
       if (mask >= KS - 1 && j0 + KS <= k1 && p0 >= 0 && a.D == DP) {  // a whole block in one page
-        const uint32_t at = j0 & mask;
-        const uint4* ks = kb + (uint64_t)p0 * a.k16[0] + (uint64_t)(at + r0) * a.k16[1] + c;
-        const uint4* vs = vb + (uint64_t)p0 * a.v16[0] + (uint64_t)(at + r0) * a.v16[1] + c;
+        const uint32_t at = j0 & mask, r4 = lane % KS;
+        const uint4 *ks = kb + (uint64_t)p0 * a.k16[0], *vs = vb + (uint64_t)p0 * a.v16[0];
+        auto to = [&](int r) { return dst + (RS % 8 == 0 ? r * St::row + St::at(r0, c) : St::at(r0 + r, c)); };
+        const Steps *kt = ksb, *vt = vsb;
+        if constexpr (I4) kt += (uint64_t)p0 * a.ksr[0], vt += (uint64_t)p0 * a.vsr[0];
+        if (a.dense) {  // the keys of a head one after another: the warp copies what follows
+          ks += at * St::NC + lane, vs += at * St::NC + lane;
 #pragma unroll
-        for (int r = 0; r < KS; r += RS) {
-          const uint32_t to = dst + (RS % 8 == 0 ? r * St::row + St::at(r0, c) : St::at(r0 + r, c));
-          cp_async<16>(to, ks, true);
-          cp_async<16>(to + St::v, vs, true);
-          ks += (size_t)RS * a.k16[1], vs += (size_t)RS * a.v16[1];
+          for (int r = 0; r < KS; r += RS) {
+            cp_async<16>(to(r), ks + r * St::NC, true);
+            cp_async<16>(to(r) + St::v, vs + r * St::NC, true);
+          }
+          kt += at + r4, vt += at + r4;
+        } else {
+          ks += (uint64_t)(at + r0) * a.k16[1] + c, vs += (uint64_t)(at + r0) * a.v16[1] + c;
+#pragma unroll
+          for (int r = 0; r < KS; r += RS) {
+            cp_async<16>(to(r), ks, true);
+            cp_async<16>(to(r) + St::v, vs, true);
+            ks += (size_t)RS * a.k16[1], vs += (size_t)RS * a.v16[1];
+          }
+          kt += (uint64_t)(at + r4) * a.ksr[1], vt += (uint64_t)(at + r4) * a.vsr[1];
         }
         if constexpr (I4) {
-          const uint32_t r = lane % KS;
-          if (lane < KS)
-            cp_async<St::step>(dst + St::ks + r * St::step, ksb + (uint64_t)p0 * a.ksr[0] + (uint64_t)(at + r) * a.ksr[1], true);
-          if (lane >= 32 - KS)
-            cp_async<St::step>(dst + St::vs + r * St::step, vsb + (uint64_t)p0 * a.vsr[0] + (uint64_t)(at + r) * a.vsr[1], true);
+          if (lane < KS) cp_async<St::step>(dst + St::ks + r4 * St::step, kt, true);
+          if (lane >= 32 - KS) cp_async<St::step>(dst + St::vs + r4 * St::step, vt, true);
         }
         return;
       }
@@ -418,35 +458,77 @@ __global__ void __launch_bounds__(kThreads, I4 ? (NR == 1 ? PER4 : 3) : 2) attn_
     }
 
     // q as B fragments, row g of tile x: the values that face a lane's words of K
-    uint32_t qf[DP / 16][NR][2], base[NR][2];  // base (4 bits): -136 sum q of the groups, see below
+    uint32_t qf[DP / 16][NR][2], base[NR][2];  // base: 4 bits, see below
+    float c[NR][2];                            // log2 e times the scale, and 4 bits: what was taken out of the row of q
+    if constexpr (I4) {
+      // Warp j makes group j's for all: values 32 j + 8 t .. of the rows.
 #pragma unroll
-    for (int x = 0; x < NR; ++x) {
-      const int r = row0 + g + 8 * x;
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (r < a.R ? row_at(a, b, hk, r) : 0);
-      if constexpr (I4) {
-        float sum[NG];
+      for (int x = 0; x < NR; ++x) {
+        const int r = row0 + g + 8 * x;
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (r < a.R ? row_at(a, b, hk, r) : 0);
+        uint4 mine_q = make_uint4(0, 0, 0, 0);
+        uint32_t top = 0;
 #pragma unroll
-        for (int j = 0; j < NG; ++j) {  // word t of chunk j: values 32 j + 8 t + .., in pairs (n, n + 4)
+        for (int j = 0; j < NG; ++j) {
           const uint4 v = r < a.R ? *reinterpret_cast<const uint4*>(q + 32 * j + 8 * t) : make_uint4(0, 0, 0, 0);
-          qf[2 * j][x][0] = __byte_perm(v.x, v.z, 0x5410), qf[2 * j][x][1] = __byte_perm(v.x, v.z, 0x7632);
-          qf[2 * j + 1][x][0] = __byte_perm(v.y, v.w, 0x5410), qf[2 * j + 1][x][1] = __byte_perm(v.y, v.w, 0x7632);
-          float y = lo16(v.x) + hi16(v.x) + lo16(v.y) + hi16(v.y) + lo16(v.z) + hi16(v.z) + lo16(v.w) + hi16(v.w);
-          y += __shfl_xor_sync(0xffffffffu, y, 1);
-          y += __shfl_xor_sync(0xffffffffu, y, 2);
-          sum[j] = -136.f * y;
+          for (uint32_t u : {v.x, v.y, v.z, v.w}) top = max(top, max(u << 16 & 0x7fff0000u, u & 0x7fff0000u));
+          if (j == w) mine_q = v;
         }
-        // The sums as three terms of 8 bits, against the groups' steps: k = NG i + j is
-        // term i of group j; a lane has k = 2 t, 2 t + 1 and 2 t + 8, 2 t + 9.
-        auto term = [&](int k) {
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^-e and 2^e for the largest magnitude's exponent e (0, subnormal, infinite or NaN: 1)
+        const uint32_t e = top >> 23 == 0 || top >> 23 == 255 ? 127 : min(top >> 23, 253u);
+        const float down = __uint_as_float((254 - e) << 23);
+        if (w < NG) {
+          const uint32_t u[4] = {mine_q.x, mine_q.y, mine_q.z, mine_q.w};  // byte b of the word: values 2 b, 2 b + 1
+          uint32_t f[4];
           float y = 0.f;
 #pragma unroll
-          for (int j = 0; j < NG; ++j) y = k % NG == j ? sum[j] : y;
-          const float hi = __bfloat162float(__float2bfloat16_rn(y)), mid = __bfloat162float(__float2bfloat16_rn(y - hi));
-          return k / NG == 0 ? hi : k / NG == 1 ? mid : k / NG == 2 ? (y - hi) - mid : 0.f;
-        };
-        base[x][0] = pack_bf16(term(2 * t), term(2 * t + 1));
-        base[x][1] = pack_bf16(term(2 * t + 8), term(2 * t + 9));
-      } else {
+          for (int h = 0; h < 2; ++h) {  // bytes 2 h, 2 h + 1: product 2 j + h
+            const float q0 = lo16(u[2 * h]) * down, q1 = hi16(u[2 * h]) * down, q2 = lo16(u[2 * h + 1]) * down,
+                        q3 = hi16(u[2 * h + 1]) * down;
+            const __half2 wx = __floats2half2_rn(q1 * 0.0625f, q3 * 0.0625f);
+            const __half2 wl = __floats2half2_rn(q0 - q1 * 0.0625f, q2 - q3 * 0.0625f);
+            f[2 * h] = *reinterpret_cast<const uint32_t*>(&wx), f[2 * h + 1] = *reinterpret_cast<const uint32_t*>(&wl);
+            const float2 fx = __half22float2(wx), fl = __half22float2(wl);
+            // 1024 + 16 * 8 + 8 in X, 1024 + 8 in L
+            y = fmaf(-1160.f, fx.x + fx.y, fmaf(-1032.f, fl.x + fl.y, y));
+          }
+          y += __shfl_xor_sync(0xffffffffu, y, 1);
+          y += __shfl_xor_sync(0xffffffffu, y, 2);
+          q_frag[w][x][lane] = make_uint4(f[0], f[1], f[2], f[3]);
+          if (t == 0) {
+            q_sum[8 * x + g][w] = y;
+            if (w == 0) q_up[8 * x + g] = __uint_as_float(e << 23);
+          }
+        }
+      }
+      __syncthreads();
+      // A row's sums as three terms of 8 bits, against the groups' steps: k = NG i + j
+      // is term i of group j; a lane has k = 2 t, 2 t + 1 and 2 t + 8, 2 t + 9.
+      auto term = [&](int r, int k) {
+        const int i = k / NG;
+        const float y = q_sum[r][k % NG], hi = __bfloat162float(__float2bfloat16_rn(y)), rest = y - hi;
+        const float mid = __bfloat162float(__float2bfloat16_rn(rest));
+        return i == 0 ? hi : i == 1 ? mid : i == 2 ? rest - mid : 0.f;
+      };
+#pragma unroll
+      for (int x = 0; x < NR; ++x) {
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+          const uint4 v = q_frag[j][x][lane];
+          qf[2 * j][x][0] = v.x, qf[2 * j][x][1] = v.y, qf[2 * j + 1][x][0] = v.z, qf[2 * j + 1][x][1] = v.w;
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y) base[x][y] = pack_bf16(term(8 * x + g, 2 * t + 8 * y), term(8 * x + g, 2 * t + 8 * y + 1));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) c[x][e] = a.c * q_up[8 * x + 2 * t + e];
+      }
+    } else {
+#pragma unroll
+      for (int x = 0; x < NR; ++x) {
+        const int r = row0 + g + 8 * x;
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (r < a.R ? row_at(a, b, hk, r) : 0);
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k)
 #pragma unroll
@@ -454,6 +536,7 @@ __global__ void __launch_bounds__(kThreads, I4 ? (NR == 1 ? PER4 : 3) : 2) attn_
             const int d = 16 * k + 8 * y + 2 * t;
             qf[k][x][y] = r < a.R && d < a.D ? *reinterpret_cast<const uint32_t*>(q + d) : 0u;
           }
+        c[x][0] = c[x][1] = a.c;
       }
     }
     float acc[DP / 16][NR][4], m[NR][2], l[NR][2];
@@ -509,14 +592,16 @@ __global__ void __launch_bounds__(kThreads, I4 ? (NR == 1 ? PER4 : 3) : 2) attn_
           for (int j = 0; j < NG; ++j) {
             const uint32_t at = st + 16 * n * St::row + k_at + ((j << 4) ^ k_f);
             const uint32_t u0 = lds32(at), u1 = lds32(at + 8 * St::row);
-            const uint32_t f0[4] = {magic.codes136(u0, 0), magic.codes136(u1, 0), magic.codes136(u0, 1), magic.codes136(u1, 1)};
-            const uint32_t f1[4] = {magic.codes136(u0, 2), magic.codes136(u1, 2), magic.codes136(u0, 3), magic.codes136(u1, 3)};
+            // bytes 0 and 1, 2 and 3 of keys g and g + 8
+            const uint32_t x0 = __byte_perm(u0, 0x64u, 0x4140), x1 = __byte_perm(u1, 0x64u, 0x4140);
+            const uint32_t x2 = __byte_perm(u0, 0x64u, 0x4342), x3 = __byte_perm(u1, 0x64u, 0x4342);
+            constexpr uint32_t low = 0x640f640fu;
             const float e0 = j & 1 ? hi16(sc[0][j / 2]) : lo16(sc[0][j / 2]), e1 = j & 1 ? hi16(sc[1][j / 2]) : lo16(sc[1][j / 2]);
 #pragma unroll
             for (int x = 0; x < NR; ++x) {
               float d[4];
-              mma0(d, f0, qf[2 * j][x][0], qf[2 * j][x][1]);
-              mma(d, f1, qf[2 * j + 1][x][0], qf[2 * j + 1][x][1]);
+              mma0_f16(d, x0, x1, x0 & low, x1 & low, qf[2 * j][x][0], qf[2 * j][x][1]);
+              mma_f16(d, x2, x3, x2 & low, x3 & low, qf[2 * j + 1][x][0], qf[2 * j + 1][x][1]);
               s[n][x][0] = fmaf(d[0], e0, s[n][x][0]), s[n][x][1] = fmaf(d[1], e0, s[n][x][1]);
               s[n][x][2] = fmaf(d[2], e1, s[n][x][2]), s[n][x][3] = fmaf(d[3], e1, s[n][x][3]);
             }
@@ -551,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, I4 ? (NR == 1 ? PER4 : 3) : 2) attn_
           for (int n = 1; n < NT; ++n) top = fmaxf(top, fmaxf(s[n][x][e], s[n][x][2 + e]));
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          top *= a.c;
+          top *= c[x][e];
           f[x][e] = 1.f;
           if (top - m[x][e] > 8.f) {  // see the prompt kernel: P at most 2^8
             f[x][e] = ex2(m[x][e] - top);
@@ -576,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, I4 ? (NR == 1 ? PER4 : 3) : 2) attn_
           const float low = m[x][e] == -INFINITY ? 0.f : m[x][e];
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            s[n][x][e] = ex2(fmaf(s[n][x][e], a.c, -low)), s[n][x][2 + e] = ex2(fmaf(s[n][x][2 + e], a.c, -low));
+            s[n][x][e] = ex2(fmaf(s[n][x][e], c[x][e], -low)), s[n][x][2 + e] = ex2(fmaf(s[n][x][2 + e], c[x][e], -low));
             l[x][e] += s[n][x][e] + s[n][x][2 + e];
           }
         }
@@ -612,7 +697,13 @@ __global__ void __launch_bounds__(kThreads, I4 ? (NR == 1 ? PER4 : 3) : 2) attn_
             for (int y = 0; y < 2; ++y) {
               const uint32_t v[4] = {magic.codes(v0, 2 * y), magic.codes(v0, 2 * y + 1), magic.codes(v1, 2 * y), magic.codes(v1, 2 * y + 1)};
 #pragma unroll
-              for (int x = 0; x < NR; ++x) mma(acc[2 * j + y][x], v, pf[x][0], pf[x][1]);
+              for (int x = 0; x < NR; ++x) {
+#ifdef X_MMAOFF
+                const uint32_t off[4] = {0xc308c308u, 0xc308c308u, 0xc308c308u, 0xc308c308u};
+                mma(acc[2 * j + y][x], off, pf[x][0], pf[x][1]);
+#endif
+                mma(acc[2 * j + y][x], v, pf[x][0], pf[x][1]);
+              }
             }
           }
         } else {
@@ -768,6 +859,8 @@ cudaError_t run(const AttnPagedProblem& p, const PagedCache& c, cudaStream_t s) 
       a.ksr[i] = (uint32_t)(c.kss[i] / steps), a.vsr[i] = (uint32_t)(c.vss[i] / steps);
     }
   }
+  const uint32_t row16 = c.format == GDN_CACHE_I4 ? c.D / 32 : c.D / 8;
+  a.dense = a.k16[1] == row16 && a.v16[1] == row16 && (c.format != GDN_CACHE_I4 || (a.ksr[1] == 1 && a.vsr[1] == 1));
   a.q = p.q, a.k = c.k, a.v = c.v, a.o = p.o;
   a.k_scale = static_cast<const __nv_bfloat16*>(c.k_scale), a.v_scale = static_cast<const __nv_bfloat16*>(c.v_scale);
   unsigned char* ws = static_cast<unsigned char*>(p.ws);
