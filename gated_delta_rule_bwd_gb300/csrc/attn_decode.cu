@@ -513,7 +513,7 @@ cudaError_t run(const AttnDecodeProblem& p, cudaStream_t s) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr, cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attn_combine_kernel<T, Args>, a, pl.ctas, pl.rows);
+  e = cudaLaunchKernelEx(&cfg, attn_combine_kernel<T, 1, Args>, a, pl.ctas, pl.rows);
   prof_after(s, kAttnCombine);
   return e;
 }

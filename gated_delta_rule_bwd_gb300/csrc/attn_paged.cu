@@ -244,16 +244,10 @@ __global__ void __launch_bounds__(kThreads) attn_paged_simt_kernel(Args a) {
 // Each warp streams its own blocks of KS keys (w, w + 4, ...) through a ring of
 // kStages stages (cp.async) and keeps its own m, l and accumulators, so the warps
 // meet only at a segment's end.
-#ifndef KEYS4
-#define KEYS4 32
-#endif
-#ifndef PER4
-#define PER4 3
-#endif
-#ifndef STAGES
-#define STAGES 3
-#endif
-constexpr int kStages = STAGES, kKeys4 = KEYS4;
+constexpr int kStages = 3;
+// CTAs per SM.  4 bits: at three, 165 registers; four (128) keep the same share of the
+// issue slots busy, and there are more of them to set up (57 us for 55).
+constexpr int kPerSm16 = 2, kPerSm4 = 3;
 
 template <int n>
 __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool valid) {
@@ -332,22 +326,18 @@ struct Magic {
     asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(x) : "r"(w >> (4 * n)), "r"(mask), "r"(one));
     return x;
   }
-#ifndef X_MMAOFF
   __device__ __forceinline__ uint32_t codes(uint32_t w, int n) const {
     const uint32_t x = codes136(w, n), o = 0xc308c308u;
     const __nv_bfloat162 y = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&o));
     return *reinterpret_cast<const uint32_t*>(&y);
   }
-#else
-  __device__ __forceinline__ uint32_t codes(uint32_t w, int n) const { return codes136(w, n); }
-#endif
 };
 __device__ __forceinline__ float lo16(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi16(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
 template <int DP, bool I4>
 struct Stage {
-  static constexpr int KS = I4 ? kKeys4 : 16;       // keys
+  static constexpr int KS = I4 ? 32 : 16;           // keys
   static constexpr int row = I4 ? DP / 2 : DP * 2;  // bytes of a key's row
   static constexpr int NC = row / 16;               // 16-byte chunks of it
   using Steps = std::conditional_t<DP == 128, uint2, uint32_t>;  // a key's steps (4 bits)
@@ -364,7 +354,7 @@ struct Stage {
 };
 
 template <int DP, int NR, bool I4>
-__global__ void __launch_bounds__(kThreads, I4 ? (NR == 1 ? PER4 : 3) : 2) attn_paged_mma_kernel(Args a) {
+__global__ void __launch_bounds__(kThreads, I4 ? kPerSm4 : kPerSm16) attn_paged_mma_kernel(Args a) {
   using St = Stage<DP, I4>;
   constexpr int KS = St::KS, NG = DP / 32, NT = KS / 16, kQ = 8 * NR;  // kQ: query rows per CTA
   extern __shared__ __align__(128) unsigned char sm[];
@@ -697,13 +687,7 @@ __global__ void __launch_bounds__(kThreads, I4 ? (NR == 1 ? PER4 : 3) : 2) attn_
             for (int y = 0; y < 2; ++y) {
               const uint32_t v[4] = {magic.codes(v0, 2 * y), magic.codes(v0, 2 * y + 1), magic.codes(v1, 2 * y), magic.codes(v1, 2 * y + 1)};
 #pragma unroll
-              for (int x = 0; x < NR; ++x) {
-#ifdef X_MMAOFF
-                const uint32_t off[4] = {0xc308c308u, 0xc308c308u, 0xc308c308u, 0xc308c308u};
-                mma(acc[2 * j + y][x], off, pf[x][0], pf[x][1]);
-#endif
-                mma(acc[2 * j + y][x], v, pf[x][0], pf[x][1]);
-              }
+              for (int x = 0; x < NR; ++x) mma(acc[2 * j + y][x], v, pf[x][0], pf[x][1]);
             }
           }
         } else {
@@ -809,14 +793,13 @@ struct Plan {
   int rows, blocks, ctas;  // query rows per CTA, row blocks (grid.y), CTAs that share the units (grid.x)
 };
 
-// CTAs that run at once on an SM: CUDA cores 4; mma bf16 2, 4 bits 4 (8 rows) or 3.
 Plan plan_of(const AttnPagedProblem& p, const PagedCache& c) {
   Plan q;
   const int R = p.H / c.Hkv * p.T;
   q.mma = use_mma(p, c);
   q.rows = !q.mma ? kRows : R <= 8 ? 8 : 16;
   q.blocks = (R + q.rows - 1) / q.rows;
-  const int per_sm = !q.mma ? 4 : c.format != GDN_CACHE_I4 ? 2 : q.rows == 8 ? PER4 : 3;
+  const int per_sm = !q.mma ? 4 : c.format == GDN_CACHE_I4 ? kPerSm4 : kPerSm16;
   q.ctas = ctas_for(p.B, c.Hkv, (long)p.pt.max_pages * c.page, q.blocks, per_sm);
   return q;
 }
@@ -885,13 +868,16 @@ cudaError_t run(const AttnPagedProblem& p, const PagedCache& c, cudaStream_t s) 
   prof_before(s);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(pl.ctas, std::min(a.R, pl.rows), pl.blocks);
-  cfg.blockDim = dim3(kThreads);
+  // few rows are in many pieces: as many threads as help with one row of all CTAs' pieces
+  const bool wide = pl.ctas >= 32 * p.B * c.Hkv;
+  cfg.blockDim = dim3(wide ? 8 * kThreads : kThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr, cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attn_combine_kernel<T, Args>, a, pl.ctas, pl.rows);
+  e = wide ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<T, 8, Args>, a, pl.ctas, pl.rows)
+           : cudaLaunchKernelEx(&cfg, attn_combine_kernel<T, 1, Args>, a, pl.ctas, pl.rows);
   prof_after(s, kAttnPagedCombine);
   return e;
 }

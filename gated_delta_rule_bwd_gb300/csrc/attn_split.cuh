@@ -120,14 +120,16 @@ __device__ __forceinline__ long long row_at(const A& a, int b, int hk, int r) {
   return (((long long)b * a.T + r / a.G) * a.H + hk * a.G + r % a.G) * a.D;
 }
 
-// One CTA of 128 threads per (row of a block, CTA that starts a row it does
-// not end): slots 2 c + 1, 2 (c + 1), 2 (c + 2), ... of the row.
-template <typename T, class A>
-__global__ void __launch_bounds__(kThreads) attn_combine_kernel(A a, int ctas, int rows) {
+// One CTA of P times 128 threads per (row of a block, CTA that starts a row it does
+// not end): slots 2 c + 1, 2 (c + 1), 2 (c + 2), ... of the row.  The P groups of
+// threads take every P-th slot, and their sums are added in order.
+template <typename T, int P, class A>
+__global__ void __launch_bounds__(P * kThreads) attn_combine_kernel(A a, int ctas, int rows) {
   __shared__ float f[kMaxCtas];
-  __shared__ float red[8];
+  __shared__ float red[8 * P];
+  __shared__ float sums[P > 1 ? P * kThreads : 1];
   tc::grid_dep_wait();
-  const int c0 = blockIdx.x, r = blockIdx.z * rows + blockIdx.y, d = threadIdx.x;
+  const int c0 = blockIdx.x, r = blockIdx.z * rows + blockIdx.y, th = threadIdx.x, d = th % kThreads, part = th / kThreads;
   const int4 st = a.starts[(long)blockIdx.z * ctas + c0];
   if (st.x < 0 || r >= a.R) return;
   const int n = st.z - c0 + 1;
@@ -135,27 +137,40 @@ __global__ void __launch_bounds__(kThreads) attn_combine_kernel(A a, int ctas, i
     return ((long)blockIdx.z * 2 * ctas + (i ? 2 * (c0 + i) : 2 * c0 + 1)) * rows + blockIdx.y;
   };
   float m = -INFINITY;
-  for (int i = d; i < n; i += kThreads) m = fmaxf(m, a.ml[2 * at(i)]);
+  for (int i = th; i < n; i += P * kThreads) m = fmaxf(m, a.ml[2 * at(i)]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((d & 31) == 0) red[d >> 5] = m;
+  if ((th & 31) == 0) red[th >> 5] = m;
   __syncthreads();
-  m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  m = red[0];
+#pragma unroll
+  for (int i = 1; i < 4 * P; ++i) m = fmaxf(m, red[i]);
   float sum = 0.f;
-  for (int i = d; i < n; i += kThreads) {
+  for (int i = th; i < n; i += P * kThreads) {
     const float mi = a.ml[2 * at(i)], e = mi == -INFINITY ? 0.f : exp2f(mi - m);
     f[i] = e;
     sum = fmaf(e, a.ml[2 * at(i) + 1], sum);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if ((d & 31) == 0) red[4 + (d >> 5)] = sum;
+  if ((th & 31) == 0) red[4 * P + (th >> 5)] = sum;
   __syncthreads();
-  sum = red[4] + red[5] + red[6] + red[7];
-  if (d >= a.D) return;
+  sum = red[4 * P];
+#pragma unroll
+  for (int i = 1; i < 4 * P; ++i) sum += red[4 * P + i];
   float x = 0.f;
+  if (d < a.D) {
 #pragma unroll 8
-  for (int i = 0; i < n; ++i) x = fmaf(f[i], a.acc[at(i) * a.D + d], x);
+    for (int i = part; i < n; i += P) x = fmaf(f[i], a.acc[at(i) * a.D + d], x);
+  }
+  if constexpr (P > 1) {
+    sums[th] = x;
+    __syncthreads();
+    if (part > 0) return;
+#pragma unroll
+    for (int i = 1; i < P; ++i) x += sums[i * kThreads + d];
+  }
+  if (d >= a.D) return;
   static_cast<T*>(a.o)[row_at(a, st.x, st.y, r) + d] = from_f32<T>(sum == 0.f ? 0.f : x / sum);
 }
 
