@@ -29,6 +29,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import NamedTuple, Optional
 
@@ -208,21 +209,20 @@ def lib():
             L.gdn_layer_norm_bwd_workspace.restype = sz
             L.gdn_layer_norm_bwd.argtypes = [ns] + [vp] * 9 + [sz, vp]
             L.gdn_layer_norm_bwd.restype = ctypes.c_int
-            qs, pc, ks, ps = (ctypes.POINTER(QkRopeShape), ctypes.POINTER(PagedCacheDesc),
-                              ctypes.POINTER(KvAppendShape), ctypes.POINTER(AttnPagedShape))
-            L.gdn_qk_norm_rope_fwd.argtypes = [qs] + [vp] * 4 + [f32] + [vp] * 6
+            # shapes and caches go in as packed bytes (or by reference to a Structure)
+            L.gdn_qk_norm_rope_fwd.argtypes = [vp] * 5 + [f32] + [vp] * 6
             L.gdn_qk_norm_rope_fwd.restype = i32
-            L.gdn_qk_norm_rope_bwd_workspace.argtypes = [qs]
+            L.gdn_qk_norm_rope_bwd_workspace.argtypes = [vp]
             L.gdn_qk_norm_rope_bwd_workspace.restype = sz
-            L.gdn_qk_norm_rope_bwd.argtypes = [qs] + [vp] * 4 + [f32] + [vp] * 10 + [sz, vp]
+            L.gdn_qk_norm_rope_bwd.argtypes = [vp] * 5 + [f32] + [vp] * 10 + [sz, vp]
             L.gdn_qk_norm_rope_bwd.restype = i32
-            L.gdn_kv_append.argtypes = [ks, pc] + [vp] * 10
+            L.gdn_kv_append.argtypes = [vp] * 12
             L.gdn_kv_append.restype = i32
-            L.gdn_kv_gather.argtypes = [pc, vp, i32, i32, ctypes.c_longlong, vp, i32, i32, vp, vp, vp]
+            L.gdn_kv_gather.argtypes = [vp, vp, i32, i32, ctypes.c_longlong, vp, i32, i32, vp, vp, vp]
             L.gdn_kv_gather.restype = i32
-            L.gdn_attn_paged_workspace.argtypes = [ps, pc]
+            L.gdn_attn_paged_workspace.argtypes = [vp, vp]
             L.gdn_attn_paged_workspace.restype = sz
-            L.gdn_attn_paged.argtypes = [ps, pc, vp, vp, vp, f32, vp, vp, sz, vp]
+            L.gdn_attn_paged.argtypes = [vp] * 5 + [f32, vp, vp, sz, vp]
             L.gdn_attn_paged.restype = i32
             L.gdn_profile_begin.argtypes = [ctypes.c_int]
             L.gdn_profile_begin.restype = ctypes.c_int
@@ -907,16 +907,44 @@ def rope_table(n, R, base=10000.0, device="cuda"):
     return angle.cos().float(), angle.sin().float()
 
 
+# A decode step calls these once per layer with little for the GPU to do, so their
+# checks are few expressions on what every call has, and build their messages only
+# when one fails; shapes go to the library as packed bytes.
+_QK_ROPE = struct.Struct("@9i6q")      # gdn_qk_rope_shape
+_CACHE = struct.Struct("@5i4P12q")     # gdn_paged_cache
+_APPEND = struct.Struct("@9i10q")      # gdn_kv_append_shape
+_PAGED = struct.Struct("@5iq")         # gdn_attn_paged_shape
+
+
 def _f32(name, x, device, shape):
     if not _same(x, torch.float32, device, shape):
         _nb_check(name, x, torch.float32, device, shape)
+
+
+def _i32(name, x, device, shape):
+    if not _same(x, torch.int32, device, shape):
+        _nb_check(name, x, torch.int32, device, shape)
+
+
+def _empty(x, dtype, device):
+    """A contiguous tensor of x's shape."""
+    return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=dtype, device=device)
+
+
+def _heads(name, x, dtype, device):
+    """x's strides, a [B, T, H, D] tensor whose head rows are contiguous."""
+    st = x.stride() if isinstance(x, torch.Tensor) else ()
+    if len(st) == 4 and st[3] == 1 and x.dtype is dtype and x.device == device and x.is_cuda and x.shape[3] > 0:
+        return st
+    _attn_tensor(name, x, dtype, device)
+    return st
 
 
 def _tables(cos, sin, D, device):
     """R and P of the tables (0, 0: none)."""
     if cos is None and sin is None:
         return 0, 0
-    if cos is None or sin is None or cos.dim() != 2:
+    if not isinstance(cos, torch.Tensor) or not isinstance(sin, torch.Tensor) or cos.dim() != 2:
         raise GdnError("cos and sin must be fp32 tables [positions, R / 2], both or neither")
     _f32("cos", cos, device, cos.shape)
     _f32("sin", sin, device, cos.shape)
@@ -930,9 +958,10 @@ def _qk_args(q, k, q_weight, k_weight, cos, sin, positions, interleaved):
     if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPES:
         raise GdnError("q must be a fp32 or bf16 tensor")
     dtype, device = q.dtype, q.device
-    qs, ks = _attn_tensor("q", q, dtype, device), _attn_tensor("k", k, dtype, device)
+    qs, ks = _heads("q", q, dtype, device), _heads("k", k, dtype, device)
     B, T, H, D = q.shape
-    if k.shape[0] != B or k.shape[1] != T or k.shape[3] != D:
+    Bk, Tk, Hkv, Dk = k.shape
+    if Bk != B or Tk != T or Dk != D:
         raise GdnError(f"k: expected [{B}, {T}, Hkv, {D}], got {tuple(k.shape)}")
     if (q_weight is None) != (k_weight is None):
         raise GdnError("q_weight and k_weight: both or neither")
@@ -945,9 +974,9 @@ def _qk_args(q, k, q_weight, k_weight, cos, sin, positions, interleaved):
     if positions is not None:
         if R == 0:
             raise GdnError("positions need cos and sin")
-        if not _same(positions, torch.int32, device, (B, T)):
-            _nb_check("positions", positions, torch.int32, device, (B, T))
-    return QkRopeShape(B, T, H, k.shape[2], D, R, P, int(bool(interleaved)), _DTYPES[dtype], qs, ks)
+        _i32("positions", positions, device, (B, T))
+    return _QK_ROPE.pack(B, T, H, Hkv, D, R, P, bool(interleaved), _DTYPES[dtype], qs[0], qs[1], qs[2],
+                         ks[0], ks[1], ks[2])
 
 
 def qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None,
@@ -959,13 +988,11 @@ def qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, cos=None, sin=None, pos
     Pairs are ``(i, i + R / 2)``, or ``(2 i, 2 i + 1)`` with ``interleaved``.  Weights
     or tables may be left out.  Returns ``(qo, ko)``, contiguous."""
     s = _qk_args(q, k, q_weight, k_weight, cos, sin, positions, interleaved)
-    device = q.device
-    qo = torch.empty(q.shape, dtype=q.dtype, device=device)
-    ko = torch.empty(k.shape, dtype=q.dtype, device=device)
-    _call(lib().gdn_qk_norm_rope_fwd(ctypes.byref(s), q.data_ptr(), k.data_ptr(), _addr(q_weight),
-                                     _addr(k_weight), float(eps), _addr(cos), _addr(sin),
-                                     _addr(positions), qo.data_ptr(), ko.data_ptr(),
-                                     _raw_stream(device)))
+    dtype, device = q.dtype, q.device
+    qo, ko = _empty(q, dtype, device), _empty(k, dtype, device)
+    _call((_lib or lib()).gdn_qk_norm_rope_fwd(
+        s, q.data_ptr(), k.data_ptr(), _addr(q_weight), _addr(k_weight), float(eps), _addr(cos),
+        _addr(sin), _addr(positions), qo.data_ptr(), ko.data_ptr(), _raw_stream(device)))
     return qo, ko
 
 
@@ -975,22 +1002,21 @@ def qk_norm_rope_bwd(q, k, dqo, dko, q_weight=None, k_weight=None, cos=None, sin
     returns ``(dq, dk, dq_weight, dk_weight)`` (contiguous; the last two fp32,
     reproducible sums over all tokens and heads, None without weights)."""
     s = _qk_args(q, k, q_weight, k_weight, cos, sin, positions, interleaved)
-    dtype, device, L, sp = q.dtype, q.device, lib(), ctypes.byref(s)
+    dtype, device, L = q.dtype, q.device, _lib or lib()
     if not (_same(dqo, dtype, device, q.shape) and _same(dko, dtype, device, k.shape)):
         _nb_check("dqo", dqo, dtype, device, q.shape)
         _nb_check("dko", dko, dtype, device, k.shape)
-    dq = torch.empty(q.shape, dtype=dtype, device=device)
-    dk = torch.empty(k.shape, dtype=dtype, device=device)
+    dq, dk = torch.empty_like(dqo), torch.empty_like(dko)
     dwq = dwk = ws = None
     need = 0
     if q_weight is not None:
         dwq, dwk = torch.empty_like(q_weight), torch.empty_like(k_weight)
-        need = L.gdn_qk_norm_rope_bwd_workspace(sp)
+        need = L.gdn_qk_norm_rope_bwd_workspace(s)
         ws = _workspace(need, workspace, device)
-    _call(L.gdn_qk_norm_rope_bwd(sp, q.data_ptr(), k.data_ptr(), _addr(q_weight), _addr(k_weight),
-                                 float(eps), _addr(cos), _addr(sin), _addr(positions),
-                                 dqo.data_ptr(), dko.data_ptr(), dq.data_ptr(), dk.data_ptr(),
-                                 _addr(dwq), _addr(dwk), _addr(ws), need, _raw_stream(device)))
+    _call(L.gdn_qk_norm_rope_bwd(
+        s, q.data_ptr(), k.data_ptr(), _addr(q_weight), _addr(k_weight), float(eps), _addr(cos),
+        _addr(sin), _addr(positions), dqo.data_ptr(), dko.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+        _addr(dwq), _addr(dwk), _addr(ws), need, _raw_stream(device)))
     return dq, dk, dwq, dwk
 
 
@@ -1027,46 +1053,49 @@ def new_paged_cache(pages, page, Hkv, D, dtype=torch.bfloat16, bits=None, device
 
 
 def _cache_args(cache, device):
-    """The ABI's view of a cache."""
-    cache = tuple(x for x in cache if x is not None)
-    if len(cache) not in (2, 4) or not all(isinstance(x, torch.Tensor) and x.dim() == 4
-                                           and x.device == device for x in cache):
-        raise GdnError(f"the cache must be (k, v) or (k, v, k_scale, v_scale), [pages, page, Hkv, .] "
-                       f"tensors on {device}")
+    """The ABI's view of a cache (packed), and its heads, values per head and format."""
+    n = 4 if len(cache) == 4 and cache[2] is not None else 2
+    if n == 2 and any(x is not None for x in cache[2:]) or len(cache) < 2 or len(cache) > 4:
+        raise GdnError("the cache must be (k, v) or (k, v, k_scale, v_scale)")
+    for x in cache[:n]:
+        if not isinstance(x, torch.Tensor) or x.dim() != 4 or x.device != device:
+            raise GdnError(f"the cache must be [pages, page, Hkv, .] tensors on {device}, "
+                           f"(k, v) or (k, v, k_scale, v_scale)")
     k, v = cache[0], cache[1]
-    shape = k.shape
-    if v.shape != shape or v.dtype is not k.dtype:
-        raise GdnError(f"the cache's k and v differ: {tuple(shape)} {k.dtype}, {tuple(v.shape)} {v.dtype}")
-    kst, vst = k.stride(), v.stride()
+    shape, dtype, kst, vst = k.shape, k.dtype, k.stride(), v.stride()
+    if v.shape != shape or v.dtype is not dtype:
+        raise GdnError(f"the cache's k and v differ: {tuple(shape)} {dtype}, {tuple(v.shape)} {v.dtype}")
     pages, page, Hkv, D = shape
     if D == 0:
         raise GdnError("the cache's heads have no values (D = 0)")
     if (kst[3] != 1 or vst[3] != 1) and D > 1:
         raise GdnError("the values of a head must be contiguous in the cache")
-    if len(cache) == 2:
-        if k.dtype not in _DTYPES:
-            raise GdnError(f"a cache of {k.dtype}: fp32, bf16, or uint8 codes with scales")
-        return PagedCacheDesc(pages, page, Hkv, D, _DTYPES[k.dtype], k.data_ptr(), v.data_ptr(),
-                              None, None, kst[:3], vst[:3])
+    if n == 2:
+        if dtype not in _DTYPES:
+            raise GdnError(f"a cache of {dtype}: fp32, bf16, or uint8 codes with scales")
+        form = _DTYPES[dtype]
+        return _CACHE.pack(pages, page, Hkv, D, form, k.data_ptr(), v.data_ptr(), 0, 0, *kst[:3],
+                           *vst[:3], 0, 0, 0, 0, 0, 0), Hkv, D, form
     ks, vs = cache[2], cache[3]
     steps = (pages, page, Hkv, D // 16)
-    if (k.dtype is not torch.uint8 or D % 16 or ks.dtype is not torch.bfloat16
+    if (dtype is not torch.uint8 or D % 16 or ks.dtype is not torch.bfloat16
             or vs.dtype is not torch.bfloat16 or ks.shape != steps or vs.shape != steps):
         raise GdnError(f"a 4-bit cache: uint8 codes [pages, page, Hkv, D / 2] and bf16 scales [pages, page, "
                        f"Hkv, D / 32], D a multiple of 32, got {[(tuple(x.shape), x.dtype) for x in cache]}")
     kss, vss = ks.stride(), vs.stride()
     if (kss[3] != 1 or vss[3] != 1) and steps[3] > 1:
         raise GdnError("the scales of a head must be contiguous in the cache")
-    return PagedCacheDesc(pages, page, Hkv, 2 * D, 2, k.data_ptr(), v.data_ptr(), ks.data_ptr(),
-                          vs.data_ptr(), kst[:3], vst[:3], kss[:3], vss[:3])
+    return _CACHE.pack(pages, page, Hkv, 2 * D, 2, k.data_ptr(), v.data_ptr(), ks.data_ptr(),
+                       vs.data_ptr(), *kst[:3], *vst[:3], *kss[:3], *vss[:3]), Hkv, 2 * D, 2
 
 
 def _block_table(table, rows, device):
+    """Entries per row of a block table, and its row stride."""
     if (not isinstance(table, torch.Tensor) or table.dtype is not torch.int32 or table.dim() != 2
-            or table.device != device or (rows is not None and table.shape[0] != rows)
-            or (table.shape[1] > 1 and table.stride(1) != 1)):
-        raise GdnError(f"block_table must be int32 [{'rows' if rows is None else rows}, max_pages] on "
-                       f"{device}, the entries of a row contiguous")
+            or table.device != device or table.shape[0] != rows
+            or (table.stride(1) != 1 and table.shape[1] > 1)):
+        raise GdnError(f"block_table must be int32 [{rows}, max_pages] on {device}, the entries of a row "
+                       "contiguous")
     return table.shape[1], table.stride(0)
 
 
@@ -1084,20 +1113,21 @@ def kv_append(k, v, cache, block_table, lens, q=None, cos=None, sin=None, interl
     if not isinstance(k, torch.Tensor) or k.dtype not in _DTYPES:
         raise GdnError("k must be a fp32 or bf16 tensor")
     dtype, device = k.dtype, k.device
-    kst, vst = _attn_tensor("k", k, dtype, device), _attn_tensor("v", v, dtype, device)
-    B, T, Hkv, D = k.shape
-    if v.shape != k.shape:
-        raise GdnError(f"k and v differ: {tuple(k.shape)}, {tuple(v.shape)}")
-    H, qst = 0, (0, 0, 0)
+    kst, vst = _heads("k", k, dtype, device), _heads("v", v, dtype, device)
+    shape = k.shape
+    B, T, Hkv, D = shape
+    if v.shape != shape:
+        raise GdnError(f"k and v differ: {tuple(shape)}, {tuple(v.shape)}")
+    H, qst, qo = 0, (0, 0, 0), None
     if q is not None:
-        qst = _attn_tensor("q", q, dtype, device)
-        H = q.shape[2]
-        if q.shape[0] != B or q.shape[1] != T or q.shape[3] != D:
+        qst = _heads("q", q, dtype, device)
+        Bq, Tq, H, Dq = q.shape
+        if Bq != B or Tq != T or Dq != D:
             raise GdnError(f"q: expected [{B}, {T}, H, {D}], got {tuple(q.shape)}")
-    c = _cache_args(cache, device)
-    if c.Hkv != Hkv or c.D != D or c.format not in (2, _DTYPES[dtype]):
-        raise GdnError(f"the cache holds {c.Hkv} heads of {c.D} values ({cache[0].dtype}), k is "
-                       f"{tuple(k.shape)} {dtype}")
+    c, heads, values, form = _cache_args(cache, device)
+    if heads != Hkv or values != D or form not in (2, _DTYPES[dtype]):
+        raise GdnError(f"the cache holds {heads} heads of {values} values ({cache[0].dtype}), k is "
+                       f"{tuple(shape)} {dtype}")
     R, P = _tables(cos, sin, D, device)
     rows = B
     if cu_seqlens is not None:
@@ -1105,15 +1135,15 @@ def kv_append(k, v, cache, block_table, lens, q=None, cos=None, sin=None, interl
         if B != 1:
             raise GdnError("packed sequences: the token tensors must be [1, T, H, D]")
         rows = cu_seqlens.numel() - 1
-    if not _same(lens, torch.int32, device, (rows,)):
-        _nb_check("lens", lens, torch.int32, device, (rows,))
+    _i32("lens", lens, device, (rows,))
     most, stride = _block_table(block_table, rows, device)
-    s = KvAppendShape(B, T, H, R, P, int(bool(interleaved)), _DTYPES[dtype], rows, most, stride, qst,
-                      kst, vst)
-    qo = None if q is None else torch.empty(q.shape, dtype=dtype, device=device)
-    _call(lib().gdn_kv_append(ctypes.byref(s), ctypes.byref(c), k.data_ptr(), v.data_ptr(), _addr(q),
-                              _addr(cos), _addr(sin), block_table.data_ptr(), lens.data_ptr(),
-                              _addr(cu_seqlens), _addr(qo), _raw_stream(device)))
+    s = _APPEND.pack(B, T, H, R, P, bool(interleaved), _DTYPES[dtype], rows, most, stride, *qst[:3],
+                     *kst[:3], *vst[:3])
+    if q is not None:
+        qo = _empty(q, dtype, device)
+    _call((_lib or lib()).gdn_kv_append(
+        s, c, k.data_ptr(), v.data_ptr(), _addr(q), _addr(cos), _addr(sin), block_table.data_ptr(),
+        lens.data_ptr(), _addr(cu_seqlens), _addr(qo), _raw_stream(device)))
     return qo
 
 
@@ -1125,19 +1155,19 @@ def kv_gather(cache, block_table, cu_seqlens, total, dtype=None):
     device = cache[0].device
     if device.type != "cuda":
         raise GdnError("the cache must be CUDA tensors (the library has no CPU path)")
-    c = _cache_args(cache, device)
+    c, Hkv, D, form = _cache_args(cache, device)
     if dtype is None:
-        dtype = torch.bfloat16 if c.format == 2 else cache[0].dtype
-    if dtype not in _DTYPES or c.format not in (2, _DTYPES[dtype]):
+        dtype = torch.bfloat16 if form == 2 else cache[0].dtype
+    if dtype not in _DTYPES or form not in (2, _DTYPES[dtype]):
         raise GdnError(f"a cache of {cache[0].dtype} does not give {dtype}")
     _attn_cu("cu_seqlens", cu_seqlens, device)
     rows = cu_seqlens.numel() - 1
     most, stride = _block_table(block_table, rows, device)
-    k = torch.empty((1, total, c.Hkv, c.D), dtype=dtype, device=device)
+    k = torch.empty((1, total, Hkv, D), dtype=dtype, device=device)
     v = torch.empty_like(k)
-    _call(lib().gdn_kv_gather(ctypes.byref(c), block_table.data_ptr(), rows, most, stride,
-                              cu_seqlens.data_ptr(), total, _DTYPES[dtype], k.data_ptr(),
-                              v.data_ptr(), _raw_stream(device)))
+    _call((_lib or lib()).gdn_kv_gather(
+        c, block_table.data_ptr(), rows, most, stride, cu_seqlens.data_ptr(), total, _DTYPES[dtype],
+        k.data_ptr(), v.data_ptr(), _raw_stream(device)))
     return k, v
 
 
@@ -1150,24 +1180,23 @@ def attn_paged(q, cache, block_table, lens, scale=None, workspace=None):
     if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPES:
         raise GdnError("q must be a fp32 or bf16 tensor")
     dtype, device = q.dtype, q.device
-    _attn_tensor("q", q, dtype, device)
+    _heads("q", q, dtype, device)
     if not q.is_contiguous():
         raise GdnError("q must be contiguous")
     B, T, H, D = q.shape
-    c = _cache_args(cache, device)
-    if c.D != D or c.format not in (2, _DTYPES[dtype]):
-        raise GdnError(f"the cache holds heads of {c.D} values ({cache[0].dtype}), q is {tuple(q.shape)} {dtype}")
-    if H > 0 and (c.Hkv == 0 or H % c.Hkv):
-        raise GdnError(f"{c.Hkv} key heads do not divide the {H} query heads")
-    if not _same(lens, torch.int32, device, (B,)):
-        _nb_check("lens", lens, torch.int32, device, (B,))
+    c, Hkv, values, form = _cache_args(cache, device)
+    if values != D or form not in (2, _DTYPES[dtype]):
+        raise GdnError(f"the cache holds heads of {values} values ({cache[0].dtype}), q is {tuple(q.shape)} {dtype}")
+    if H > 0 and (Hkv == 0 or H % Hkv):
+        raise GdnError(f"{Hkv} key heads do not divide the {H} query heads")
+    _i32("lens", lens, device, (B,))
     most, stride = _block_table(block_table, B, device)
-    s = AttnPagedShape(B, T, H, _DTYPES[dtype], most, stride)
-    L, sp, cp = lib(), ctypes.byref(s), ctypes.byref(c)
+    s = _PAGED.pack(B, T, H, _DTYPES[dtype], most, stride)
+    L = _lib or lib()
     o = torch.empty_like(q)
-    need = L.gdn_attn_paged_workspace(sp, cp)
+    need = L.gdn_attn_paged_workspace(s, c)
     ws = _workspace(need, workspace, device) if need else None
-    _call(L.gdn_attn_paged(sp, cp, q.data_ptr(), block_table.data_ptr(), lens.data_ptr(),
+    _call(L.gdn_attn_paged(s, c, q.data_ptr(), block_table.data_ptr(), lens.data_ptr(),
                            D ** -0.5 if scale is None else float(scale), o.data_ptr(), _addr(ws), need,
                            _raw_stream(device)))
     return o
