@@ -2,10 +2,12 @@
 // by position on the way) and rows out again (kv_gather).
 //
 // Append: token t of row b goes to slot n = lens[b] + t, that is place n % page of
-// page table[b][n / page].  A warp takes a token and walks its heads of q (if
-// given), k and v as the norm-and-rotation kernel does (rope.cuh): the angles and
-// the page are looked up once per token.  4-bit rows pass through shared memory
-// to bring 8 neighbouring values into a lane (a pair's halves lie R / 2 apart).
+// page table[b][n / page].  A CTA takes a run of tokens and looks up their places
+// together (the offsets, the length and the table stand behind one another); its
+// warps then take a token each (where there are few, a part of its heads) and walk
+// the heads of q (if given), k and v as the norm-and-rotation kernel does
+// (rope.cuh).  4-bit rows pass through shared memory to bring 8 neighbouring values
+// into a lane (a pair's halves lie R / 2 apart).
 // Gather: a CTA takes a run of packed tokens, looks up their pages once, and
 // copies (or widens) 16-byte vectors.  Both are bound by memory: each byte is
 // read and written once.
@@ -63,10 +65,12 @@ __device__ __forceinline__ int page_of(const Pages& p, int row, long long slot) 
 
 // ---------------------------------------------------------------- append
 
+constexpr int kTokens = 64;  // most tokens of a CTA
+
 struct AppendArgs {
   Pages c;
-  int T, H, Hkv, rows, D, R, P, split, interleaved;  // rows = H + 2 Hkv
-  long tokens;
+  int T, H, Hkv, rows, D, R, P, per, parts;  // rows = H + 2 Hkv; per: tokens of a CTA, parts: warps that share one
+  uint32_t tokens;
   long long qs[3], ks[3], vs[3];
   const void *q, *k, *v;
   const float *cos, *sin;
@@ -80,7 +84,7 @@ struct Place {
   bool turn, keep;  // its queries and keys are rotated (q is zeros otherwise); k and v are stored
 };
 
-__device__ __forceinline__ Place place_of(const AppendArgs& a, long tok) {
+__device__ __forceinline__ Place place_of(const AppendArgs& a, uint32_t tok) {
   Place p = {0, 0, 0, false, false};
   int row = (int)(tok / a.T), t = (int)(tok % a.T), fresh = a.T;
   if (a.cu) {
@@ -105,59 +109,62 @@ __device__ __forceinline__ Place place_of(const AppendArgs& a, long tok) {
 
 template <typename T, int V, int NP, int LR, bool IL, bool I4>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a) {
-  constexpr int GW = 32 / LR, U = V == 4 ? 4 : 1, RB = V == 4 ? LR * 8 : 128;  // RB: a row's place in shared memory
+  using N = Num<V>;
+  constexpr int GW = 32 / LR, M = kNums<V>, RB = V == 1 ? 128 : LR * 2 * V;  // RB: a row's place in shared memory
+  __shared__ Place place[kTokens];
   __shared__ __align__(16) float rows[I4 ? kWarps * GW * RB : 1];
-  if (a.cu && blockIdx.x == 0 && !rises(a.cu, a.c.nseq, (int)a.tokens, false) && threadIdx.x == 0)
-    report(GDN_ERR_SEQLENS);
-  const int lane = threadIdx.x & 31, grp = lane / LR, l = lane % LR;
-  const long job = (long)blockIdx.x * kWarps + (threadIdx.x >> 5), tok = job / a.split;
-  if (tok >= a.tokens) return;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, grp = lane / LR, l = lane % LR;
+  const uint32_t t0 = blockIdx.x * a.per, n = min((uint32_t)a.per, a.tokens - t0);
   Slot<V> slot[NP];
 #pragma unroll
   for (int i = 0; i < NP; ++i) slot[i].template set<IL>((l + i * LR) * V, a.D, a.R);
-  const int b = (int)(tok / a.T), t = (int)(tok % a.T), step = a.split * GW;
-  Raw<T, V> x[U][NP];
-  auto fetch = [&](int r0) {
+  // row r of the token at its place in q, k and v
+  auto fetch = [&](Raw<T, V> (&x)[NP], uint32_t tok, int r) {
+    const uint32_t b = tok / a.T, t = tok % a.T;
+    const int h = r - a.H;
+    const T* p = r < a.H      ? static_cast<const T*>(a.q) + b * a.qs[0] + t * a.qs[1] + r * a.qs[2]
+                 : h < a.Hkv  ? static_cast<const T*>(a.k) + b * a.ks[0] + t * a.ks[1] + h * a.ks[2]
+                              : static_cast<const T*>(a.v) + b * a.vs[0] + t * a.vs[1] + (h - a.Hkv) * a.vs[2];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = r0 + u * step + grp, h = r - a.H;
-      const T* p = r < a.H        ? static_cast<const T*>(a.q) + b * a.qs[0] + t * a.qs[1] + r * a.qs[2]
-                   : h < a.Hkv    ? static_cast<const T*>(a.k) + b * a.ks[0] + t * a.ks[1] + h * a.ks[2]
-                                  : static_cast<const T*>(a.v) + b * a.vs[0] + t * a.vs[1] + (h - a.Hkv) * a.vs[2];
-#pragma unroll
-      for (int i = 0; i < NP; ++i) x[u][i] = r < a.rows ? load(p, slot[i]) : Raw<T, V>{};
-    }
+    for (int i = 0; i < NP; ++i) x[i] = r < a.rows ? load(p, slot[i]) : Raw<T, V>{};
   };
-  int r0 = (int)(job % a.split) * GW;
-  fetch(r0);
-  const Place at = place_of(a, tok);
-  float c[NP][V], s[NP][V];
+  const int step = a.parts * GW;
+  const uint32_t jobs = n * a.parts;
+  Raw<T, V> next[NP];
+  if ((uint32_t)w < jobs) fetch(next, t0 + w / a.parts, w % a.parts * GW + grp);  // on its way while the places are looked up
+  if (threadIdx.x < n) place[threadIdx.x] = place_of(a, t0 + threadIdx.x);
+  if (a.cu && blockIdx.x == 0 && !rises(a.cu, a.c.nseq, (int)a.tokens, false) && threadIdx.x == 0) report(GDN_ERR_SEQLENS);
+  __syncthreads();
+  for (uint32_t job = w; job < jobs; job += kWarps) {
+    const uint32_t i0 = job / a.parts, tok = t0 + i0;
+    const int part = job % a.parts;
+    const Place at = place[i0];
+    Angles<V> g[NP];
 #pragma unroll
-  for (int i = 0; i < NP; ++i)
-    angles<V>(a.cos, a.sin, (long long)at.n * (a.R / 2), (l + i * LR) * V, slot[i].rot && at.turn, c[i], s[i]);
-  for (; r0 < a.rows; r0 += U * step) {
-    float xa[U][NP][V], xb[U][NP][V];
+    for (int i = 0; i < NP; ++i)
+      g[i].set(a.cos, a.sin, (long long)at.n * (a.R / 2), (l + i * LR) * V, slot[i].rot && at.turn);
+    for (int r0 = part * GW; r0 < a.rows; r0 += step) {
+      const int r = r0 + grp, h = r - a.H;
+      N xa[NP][M], xb[NP][M];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int i = 0; i < NP; ++i) widen<IL>(x[u][i], xa[u][i], xb[u][i]);
-    if (r0 + U * step < a.rows) fetch(r0 + U * step);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = r0 + u * step + grp, h = r - a.H;
-      if (r0 + u * step >= a.rows) break;  // the same for the whole warp
+      for (int i = 0; i < NP; ++i) widen<IL>(next[i], xa[i], xb[i]);
+      if (r0 + step < a.rows) {
+        fetch(next, tok, r + step);
+      } else if (job + kWarps < jobs) {
+        fetch(next, t0 + (job + kWarps) / a.parts, (job + kWarps) % a.parts * GW + grp);
+      }
 #pragma unroll
       for (int i = 0; i < NP; ++i)
-        if (slot[i].rot && h < a.Hkv) rotate<V>(c[i], s[i], xa[u][i], xb[u][i]);
+        if (slot[i].rot && h < a.Hkv) g[i].turn(xa[i], xb[i]);
       if (r < a.H) {
-        T* y = static_cast<T*>(a.qo) + (tok * a.H + r) * a.D;
+        T* y = static_cast<T*>(a.qo) + ((uint64_t)tok * a.H + r) * a.D;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
           if (!at.turn) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) xa[u][i][e] = xb[u][i][e] = 0.f;
+            for (int e = 0; e < M; ++e) xa[i][e] = xb[i][e] = splat<V>(0.f);
           }
-          store<IL>(y, slot[i], xa[u][i], xb[u][i]);
+          store<IL>(y, slot[i], xa[i], xb[i]);
         }
       }
       const bool isk = h < a.Hkv, keep = h >= 0 && r < a.rows && at.keep;
@@ -168,25 +175,34 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a) {
         if (!keep) continue;
         T* y = static_cast<T*>(isk ? a.c.k : a.c.v) + to;
 #pragma unroll
-        for (int i = 0; i < NP; ++i) store<IL>(y, slot[i], xa[u][i], xb[u][i]);
+        for (int i = 0; i < NP; ++i) store<IL>(y, slot[i], xa[i], xb[i]);
       } else {
-        if (r0 + u * step + GW <= a.H) continue;  // only queries: the same for the whole warp
-        float* row = rows + ((threadIdx.x >> 5) * GW + grp) * RB;
+        if (r0 + GW <= a.H) continue;  // only queries: the same for the whole warp
+        float* row = rows + (w * GW + grp) * RB;
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < NP; ++i) store<IL>(row, slot[i], xa[u][i], xb[u][i]);
+        for (int i = 0; i < NP; ++i) store<IL>(row, slot[i], xa[i], xb[i]);
         __syncwarp();
-        float y[8], step8;
-        const bool in = l < a.D / 8;
+        // 8 values in a row of each lane (V = 8: two passes of half a row's lanes)
+        constexpr int Q = V == 8 ? 2 : 1;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = in ? row[8 * l + e] : 0.f;
-        const uint32_t w = quantise8(y, step8);
-        if (!keep || !in) continue;
-        const long long* ss = isk ? a.c.kss : a.c.vss;
-        *reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(isk ? a.c.k : a.c.v) + to + 4 * l) = w;
-        if (l % 4 == 0)
-          static_cast<__nv_bfloat16*>(isk ? a.c.k_scale : a.c.v_scale)[at.page * ss[0] + at.at * ss[1] + hk * ss[2] + l / 4] =
-              __float2bfloat16_rn(step8);
+        for (int p = 0; p < Q; ++p) {
+          const int c = l + p * LR;
+          const bool in = c < a.D / 8;
+          float y[8], step8;
+#pragma unroll
+          for (int e = 0; e < 8; e += 4) {
+            const float4 x = in ? *reinterpret_cast<const float4*>(row + 8 * c + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+            y[e] = x.x, y[e + 1] = x.y, y[e + 2] = x.z, y[e + 3] = x.w;
+          }
+          const uint32_t codes = quantise8(y, step8);
+          if (!keep || !in) continue;
+          const long long* ss = isk ? a.c.kss : a.c.vss;
+          *reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(isk ? a.c.k : a.c.v) + to + 4 * c) = codes;
+          if (c % 4 == 0)
+            static_cast<__nv_bfloat16*>(isk ? a.c.k_scale : a.c.v_scale)[at.page * ss[0] + at.at * ss[1] + hk * ss[2] + c / 4] =
+                __float2bfloat16_rn(step8);
+        }
       }
     }
   }
@@ -194,11 +210,12 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a) {
 
 // ---------------------------------------------------------------- gather
 
-constexpr int kTokens = 256;  // most tokens of a CTA
+constexpr int kRun = 256;  // most tokens of a CTA
 
 struct GatherArgs {
   Pages c;
   int total, Hkv, D, tokens;  // tokens per CTA
+  uint32_t magic;             // ceil(2^32 / vectors of a row)
   const int* cu;
   void *k, *v;
 };
@@ -211,7 +228,7 @@ struct alignas(16) Vec {
 
 template <typename O, bool I4, int V>
 __global__ void __launch_bounds__(kThreads) kv_gather_kernel(GatherArgs a) {
-  __shared__ long long from[kTokens], step_from[I4 ? kTokens : 1];
+  __shared__ long long from[kRun], step_from[I4 ? kRun : 1];
   const bool isv = blockIdx.y;
   const int t0 = blockIdx.x * a.tokens, n = min(a.tokens, a.total - t0);
   if (blockIdx.x == 0 && !isv && !rises(a.cu, a.c.nseq, a.total, true) && threadIdx.x == 0) report(GDN_ERR_SEQLENS);
@@ -239,42 +256,48 @@ __global__ void __launch_bounds__(kThreads) kv_gather_kernel(GatherArgs a) {
     from[i] = at;
   }
   __syncthreads();
-  const int nv = a.D / V, per = a.Hkv * nv, all = n * per;
+  // Vector i of the run is number i % per of token i / per, kept up by steps of a CTA's
+  // threads; head and vector of the row by a multiplication (rem < 2^20 or so, a
+  // reciprocal rounded up: exact).
+  const uint32_t nv = a.D / V, per = a.Hkv * nv, all = n * per, dt = kThreads / per, dr = kThreads % per;
   O* out = static_cast<O*>(isv ? a.v : a.k) + (long long)t0 * a.Hkv * a.D;
+  const unsigned char* src = static_cast<const unsigned char*>(isv ? a.c.v : a.c.k);
+  const __nv_bfloat16* scale = static_cast<const __nv_bfloat16*>(isv ? a.c.v_scale : a.c.k_scale);
   constexpr int U = 4;
-  for (int i0 = threadIdx.x; i0 < all; i0 += U * kThreads) {
+  uint32_t t = threadIdx.x / per, rem = threadIdx.x % per;
+  for (uint32_t i0 = threadIdx.x; i0 < all; i0 += U * kThreads) {
     Vec<O, V> y[U];
-    long long to[U];
+    bool put[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * kThreads;
-      to[u] = -1;
-      if (i >= all) continue;
-      const int t = i / per, h = i % per / nv, d = i % nv * V;
-      const long long at = from[t];
-      if (at == -1) continue;
-      to[u] = (long long)i * V;
-      if (at < 0) {
+      const uint32_t i = i0 + u * kThreads, h = nv == 1 ? rem : __umulhi(rem, a.magic), d = (rem - h * nv) * V;
+      put[u] = false;
+      if (i < all) {
+        const long long at = from[t];
+        put[u] = at != -1;
+        if (at < 0) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) y[u].x[e] = from_f32<O>(0.f);
-      } else if constexpr (I4) {
-        const unsigned char* p = static_cast<const unsigned char*>(isv ? a.c.v : a.c.k) + at + h * st[2] + d / 2;
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
-        const float s = __bfloat162float(
-            static_cast<const __nv_bfloat16*>(isv ? a.c.v_scale : a.c.k_scale)[step_from[t] + h * ss[2] + d / kStepGroup]);
+          for (int e = 0; e < V; ++e) y[u].x[e] = from_f32<O>(0.f);
+        } else if constexpr (I4) {
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(src + at + h * st[2] + d / 2);
+          const float s = __bfloat162float(scale[step_from[t] + h * ss[2] + d / kStepGroup]);
 #pragma unroll
-        for (int e = 0; e < V; ++e) y[u].x[e] = from_f32<O>((float)((int)(w >> (4 * e) & 15) - 8) * s);
-      } else {
-        const O* p = static_cast<const O*>(isv ? a.c.v : a.c.k) + at + h * st[2] + d;
-        if constexpr (V > 1) y[u] = *reinterpret_cast<const Vec<O, V>*>(p);
-        else y[u].x[0] = p[0];
+          for (int e = 0; e < V; ++e) y[u].x[e] = from_f32<O>((float)((int)(w >> (4 * e) & 15) - 8) * s);
+        } else {
+          const O* p = reinterpret_cast<const O*>(src) + at + h * st[2] + d;
+          if constexpr (V > 1) y[u] = *reinterpret_cast<const Vec<O, V>*>(p);
+          else y[u].x[0] = p[0];
+        }
       }
+      t += dt, rem += dr;
+      if (rem >= per) rem -= per, ++t;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (to[u] < 0) continue;
-      if constexpr (V > 1) *reinterpret_cast<Vec<O, V>*>(out + to[u]) = y[u];
-      else out[to[u]] = y[u].x[0];
+      O* to = out + (uint64_t)(i0 + u * kThreads) * V;
+      if (!put[u]) continue;
+      if constexpr (V > 1) *reinterpret_cast<Vec<O, V>*>(to) = y[u];
+      else to[0] = y[u].x[0];
     }
   }
 }
@@ -284,13 +307,14 @@ __global__ void __launch_bounds__(kThreads) kv_gather_kernel(GatherArgs a) {
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
 template <typename T, int V, int NP, int LR>
-cudaError_t append(AppendArgs a, bool i4, cudaStream_t s) {
+cudaError_t append(AppendArgs a, bool interleaved, bool i4, cudaStream_t s) {
   constexpr int GW = 32 / LR;
-  const long want = (16L * sm_count() + a.tokens - 1) / a.tokens;  // warps per token, as for the norm
-  a.split = (int)std::max(1L, std::min(want, (long)(a.rows + GW - 1) / GW));
-  const unsigned ctas = (unsigned)((a.tokens * a.split + kWarps - 1) / kWarps);
+  // Two CTAs per SM's worth of runs or more; a short run's tokens are shared by warps.
+  a.per = (int)std::max(1L, std::min((long)kTokens, (long)a.tokens / (2 * sm_count())));
+  a.parts = std::max(1, std::min((a.rows + GW - 1) / GW, kWarps / a.per));
+  const unsigned ctas = (a.tokens + a.per - 1) / a.per;
   prof_before(s);
-  if (a.interleaved)
+  if (interleaved)
     i4 ? kv_append_kernel<T, V, NP, LR, true, true><<<ctas, kThreads, 0, s>>>(a)
        : kv_append_kernel<T, V, NP, LR, true, false><<<ctas, kThreads, 0, s>>>(a);
   else
@@ -305,21 +329,29 @@ cudaError_t append(const KvAppendProblem& p, const PagedCache& c, cudaStream_t s
   AppendArgs a = {};
   a.c = pages_of(c, p.pt);
   a.T = p.T, a.H = p.H, a.Hkv = c.Hkv, a.rows = p.H + 2 * c.Hkv, a.D = c.D, a.R = p.R, a.P = p.P;
-  a.tokens = (long)p.B * p.T, a.interleaved = p.interleaved;
+  a.tokens = (uint32_t)((long)p.B * p.T);
   for (int i = 0; i < 3; ++i) a.qs[i] = p.qs[i], a.ks[i] = p.ks[i], a.vs[i] = p.vs[i];
   a.q = p.q, a.k = p.k, a.v = p.v, a.cos = p.cos, a.sin = p.sin, a.lens = p.lens, a.cu = p.cu, a.qo = p.qo;
   const bool i4 = c.format == GDN_CACHE_I4;
-  bool vec = a.D % 8 == 0 && a.R % 8 == 0 && vectors(p.k, p.ks, sizeof(T)) && vectors(p.v, p.vs, sizeof(T)) &&
+  bool vec = vectors(p.k, p.ks, sizeof(T)) && vectors(p.v, p.vs, sizeof(T)) &&
              (p.H == 0 || (vectors(p.q, p.qs, sizeof(T)))) && aligned16(p.cos) && aligned16(p.sin);
   if (!i4) vec = vec && vectors(c.k, c.ks, sizeof(T)) && vectors(c.v, c.vs, sizeof(T));
-  if (!vec) return append<T, 1, 2, 32>(a, i4, s);
-  return a.D <= 64 ? append<T, 4, 1, 8>(a, i4, s) : append<T, 4, 1, 16>(a, i4, s);
+  if constexpr (sizeof(T) == 2) {
+    if (vec && a.D % 16 == 0 && a.R % 16 == 0)
+      return a.D <= 64 ? append<T, 8, 1, 4>(a, p.interleaved, i4, s) : append<T, 8, 1, 8>(a, p.interleaved, i4, s);
+  }
+  if (vec && a.D % 8 == 0 && a.R % 8 == 0)
+    return a.D <= 64 ? append<T, 4, 1, 8>(a, p.interleaved, i4, s) : append<T, 4, 1, 16>(a, p.interleaved, i4, s);
+  return append<T, 1, 2, 32>(a, p.interleaved, i4, s);
 }
 
 template <typename O, bool I4, int V>
 cudaError_t gather(GatherArgs a, cudaStream_t s) {
-  // about four vectors per thread
-  a.tokens = std::max(1, std::min(kTokens, 4 * kThreads / (a.Hkv * (a.D / V))));
+  // about four vectors per thread; more where there is work for four CTAs per SM (two
+  // of them for k, two for v) all the same
+  const int nv = a.D / V, few = 4 * kThreads / (a.Hkv * nv);
+  a.tokens = std::max(1, std::min(kRun, std::max(few, a.total / (2 * sm_count()))));
+  a.magic = nv == 1 ? 0 : (uint32_t)(((1ull << 32) + nv - 1) / nv);
   prof_before(s);
   kv_gather_kernel<O, I4, V><<<dim3((a.total + a.tokens - 1) / a.tokens, 2), kThreads, 0, s>>>(a);
   prof_after(s, kKvGather);

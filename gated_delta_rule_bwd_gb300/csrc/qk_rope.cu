@@ -8,13 +8,15 @@
 // Without weights n = x, and without angles y = n.
 //
 // Bound by memory: 2 e bytes per value forward, 3 e backward (x is read again,
-// nothing is saved).  A warp takes a token and walks its heads, so that the
-// angles are read once per token and lane; a row stays in the registers of its
-// LR lanes, several rows on their way.  Where there are few tokens, several
-// warps share one.
+// nothing is saved).  The heads of q and those of k are two problems that run side by
+// side, each with a share of the CTAs by its heads, so that a lane's weights and its
+// columns' sums of dw stay in registers for all of its rows.  A warp takes a token
+// (where there are few, a part of its heads) and walks the heads, so that the angles
+// are read once per token and lane; a row stays in the registers of its LR lanes,
+// the next ones on their way.
 //
-// dw: a lane keeps its columns' sums over all rows of its warp; they are added
-// per CTA and, by a second kernel, over the CTAs, each in a fixed order.
+// dw: the lanes' sums are added per CTA and, by a second kernel, over the CTAs, each
+// in a fixed order.
 
 #include "rope.cuh"
 
@@ -29,323 +31,321 @@ using tc::sm_count;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 
-struct Args {
-  int T, H, rows, D, R, P, split;  // rows: heads of q and of k; split: warps per token
-  long tokens;
-  float eps, inv_d;
-  long long qs[3], ks[3];
-  const void *q, *k;
-  const float *wq, *wk, *cos, *sin;
-  const int* pos;
-  void *qo, *ko;           // forward
-  const void *dqo, *dko;   // backward
-  void *dq, *dk;
-  float* partial;          // [ctas][2][D] sums of dw
+// The heads of q, or those of k.
+struct Side {
+  const void *x, *dy;
+  void *y, *dx;  // contiguous, as dy
+  const float* w;
+  float* dw;
+  long long st[3];
+  int H, chunk, parts;  // a warp's job: `chunk` heads of a token, `parts` jobs to a token
 };
 
-// A token's place and angles, the same for all lanes of the warp.
-template <int V, int NP>
-struct Token {
-  int b, t;
-  bool ok;  // its position has angles
-  float c[NP][V], s[NP][V];
+struct Args {
+  Side side[2];
+  int T, D, R, P, ctas0;  // the first ctas0 CTAs are q's
+  uint32_t tokens;
+  float eps, inv_d;
+  const float *cos, *sin;
+  const int* pos;
+  float* partial;  // [ctas][D] sums of dw
 };
 
 template <int V, int NP, int LR, bool IL>
 struct Lane {
+  static constexpr int GW = 32 / LR;  // rows of a warp at once
   Slot<V> slot[NP];
   int grp;
   __device__ __forceinline__ explicit Lane(const Args& a) {
     grp = (threadIdx.x & 31) / LR;
 #pragma unroll
-    for (int i = 0; i < NP; ++i) slot[i].template set<IL>(pair(i), a.D, a.R);
+    for (int i = 0; i < NP; ++i) slot[i].template set<IL>(first(i), a.D, a.R);
   }
-  __device__ __forceinline__ static int pair(int i) { return ((threadIdx.x & 31) % LR + i * LR) * V; }
+  __device__ __forceinline__ static int first(int i) { return ((threadIdx.x & 31) % LR + i * LR) * V; }
 
-  __device__ __forceinline__ Token<V, NP> token(const Args& a, long tok) const {
-    Token<V, NP> k;
-    k.b = (int)(tok / a.T), k.t = (int)(tok % a.T);
+  // The angles of a token, the same for all lanes of the warp; false: its position has none.
+  __device__ __forceinline__ bool angles(const Args& a, uint32_t tok, uint32_t t, Angles<V> (&g)[NP]) const {
     int n = 0;
-    k.ok = true;
+    bool ok = true;
     if (a.R) {
-      n = a.pos ? a.pos[tok] : k.t;
+      n = a.pos ? a.pos[tok] : (int)t;
       if (n < 0 || n >= a.P) {
-        k.ok = false, n = 0;
+        ok = false, n = 0;
         if ((threadIdx.x & 31) == 0) atomicExch(&tc::g_file_status, GDN_ERR_SEQLENS);
       }
     }
 #pragma unroll
-    for (int i = 0; i < NP; ++i)
-      angles<V>(a.cos, a.sin, (long long)n * (a.R / 2), pair(i), slot[i].rot && k.ok, k.c[i], k.s[i]);
-    return k;
-  }
-  // the lane's weights
-  __device__ __forceinline__ void weights(const float* w, float (&wa)[NP][V], float (&wb)[NP][V]) const {
-#pragma unroll
-    for (int i = 0; i < NP; ++i) widen<IL>(load(w, slot[i]), wa[i], wb[i]);
+    for (int i = 0; i < NP; ++i) g[i].set(a.cos, a.sin, (long long)n * (a.R / 2), first(i), slot[i].rot && ok);
+    return ok;
   }
 };
 
-// x and, in the backward, dy of row r of a token
-template <typename T>
-__device__ __forceinline__ const T* input(const Args& a, int b, int t, int r) {
-  return r < a.H ? static_cast<const T*>(a.q) + b * a.qs[0] + t * a.qs[1] + r * a.qs[2]
-                 : static_cast<const T*>(a.k) + b * a.ks[0] + t * a.ks[1] + (r - a.H) * a.ks[2];
-}
-// a contiguous [B, T, H, D] / [B, T, Hkv, D] pair
-template <typename T>
-__device__ __forceinline__ T* dense(const Args& a, void* q, void* k, long tok, int r) {
-  return r < a.H ? static_cast<T*>(q) + (tok * a.H + r) * a.D
-                 : static_cast<T*>(k) + (tok * (a.rows - a.H) + r - a.H) * a.D;
+// This CTA's side, its index and number among that side's CTAs.
+__device__ __forceinline__ Side side_of(const Args& a, uint32_t& cta, uint32_t& ctas) {
+  const bool k = blockIdx.x >= a.ctas0;
+  cta = k ? blockIdx.x - a.ctas0 : blockIdx.x;
+  ctas = k ? gridDim.x - a.ctas0 : a.ctas0;
+  return k ? a.side[1] : a.side[0];
 }
 
 template <typename T, int V, int NP, int LR, bool IL, bool NORM>
-__global__ void __launch_bounds__(kThreads) qk_rope_fwd_kernel(Args a) {
-  constexpr int GW = 32 / LR, U = V == 4 ? 4 : 1;  // rows a warp works on at once, and has on their way
-  const Lane<V, NP, LR, IL> L(a);
-  const long job = (long)blockIdx.x * kWarps + (threadIdx.x >> 5), tok = job / a.split;
-  if (tok >= a.tokens) return;
-  const int part = (int)(job % a.split), step = a.split * GW;
-  const int b = (int)(tok / a.T), t = (int)(tok % a.T);
-  Raw<T, V> x[U][NP];
-  auto fetch = [&](int r0) {
+__global__ void __launch_bounds__(kThreads, 2) qk_rope_fwd_kernel(Args a) {
+  using L = Lane<V, NP, LR, IL>;
+  using N = Num<V>;
+  constexpr int GW = L::GW, U = V == 1 ? 1 : 3, M = kNums<V>;  // U: rows on their way
+  const L lane(a);
+  uint32_t cta, ctas;
+  const Side s = side_of(a, cta, ctas);
+  N wa[NP][M], wb[NP][M];
+  if constexpr (NORM) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = r0 + u * step + L.grp;
+    for (int i = 0; i < NP; ++i) widen<IL>(load<float, V>(s.w, lane.slot[i]), wa[i], wb[i]);
+  }
+  for (uint64_t job = cta * kWarps + (threadIdx.x >> 5); job < (uint64_t)a.tokens * s.parts; job += ctas * kWarps) {
+    const uint32_t tok = (uint32_t)(job / s.parts), h0 = (uint32_t)(job % s.parts) * s.chunk, b = tok / a.T, t = tok % a.T;
+    const uint32_t h1 = min(h0 + s.chunk, s.H);
+    const T* x = static_cast<const T*>(s.x) + b * s.st[0] + t * s.st[1];
+    T* y = static_cast<T*>(s.y) + (uint64_t)tok * s.H * a.D;
+    Raw<T, V> next[U][NP];
+    auto fetch = [&](Raw<T, V> (&r)[NP], uint32_t h) {
 #pragma unroll
-      for (int i = 0; i < NP; ++i)
-        x[u][i] = r < a.rows ? load(input<T>(a, b, t, r), L.slot[i]) : Raw<T, V>{};
-    }
-  };
-  int r0 = part * GW;
-  fetch(r0);
-  const Token<V, NP> k = L.token(a, tok);
-  float wq[2][NP][V], wk[2][NP][V];
-  if constexpr (NORM) L.weights(a.wq, wq[0], wq[1]), L.weights(a.wk, wk[0], wk[1]);
-  for (; r0 < a.rows; r0 += U * step) {
-    float xa[U][NP][V], xb[U][NP][V];
+      for (int i = 0; i < NP; ++i) r[i] = h < h1 ? load(x + h * s.st[2], lane.slot[i]) : Raw<T, V>{};
+    };
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u) fetch(next[u], h0 + u * GW + lane.grp);
+    Angles<V> g[NP];
+    const bool ok = lane.angles(a, tok, t, g);
+    for (uint32_t h = h0 + lane.grp; h < h0 + s.chunk; h += GW) {  // the same number of passes for all lanes
+      N xa[NP][M], xb[NP][M];
 #pragma unroll
-      for (int i = 0; i < NP; ++i) widen<IL>(x[u][i], xa[u][i], xb[u][i]);
-    if (r0 + U * step < a.rows) fetch(r0 + U * step);
+      for (int i = 0; i < NP; ++i) widen<IL>(next[0][i], xa[i], xb[i]);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = r0 + u * step + L.grp;
+      for (int u = 0; u + 1 < U; ++u)
+#pragma unroll
+        for (int i = 0; i < NP; ++i) next[u][i] = next[u + 1][i];
+      fetch(next[U - 1], h + U * GW);
       if constexpr (NORM) {
-        float ss = 0.f;
+        N ss = splat<V>(0.f);
 #pragma unroll
         for (int i = 0; i < NP; ++i)
 #pragma unroll
-          for (int e = 0; e < V; ++e) ss = fmaf(xa[u][i][e], xa[u][i][e], fmaf(xb[u][i][e], xb[u][i][e], ss));
-        const float rstd = rsqrtf(row_sum<LR>(ss) * a.inv_d + a.eps);
-        const bool isq = r < a.H;
+          for (int e = 0; e < M; ++e) ss = fma(xa[i][e], xa[i][e], fma(xb[i][e], xb[i][e], ss));
+        const N r = splat<V>(rsqrtf(row_sum<LR>(total(ss)) * a.inv_d + a.eps));
 #pragma unroll
         for (int i = 0; i < NP; ++i)
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            xa[u][i][e] = xa[u][i][e] * rstd * (isq ? wq[0][i][e] : wk[0][i][e]);
-            xb[u][i][e] = xb[u][i][e] * rstd * (isq ? wq[1][i][e] : wk[1][i][e]);
-          }
+          for (int e = 0; e < M; ++e) xa[i][e] = mul(mul(xa[i][e], r), wa[i][e]), xb[i][e] = mul(mul(xb[i][e], r), wb[i][e]);
       }
-      if (r >= a.rows) continue;
-      T* y = dense<T>(a, a.qo, a.ko, tok, r);
+      if (h >= h1) continue;
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        if (L.slot[i].rot) rotate<V>(k.c[i], k.s[i], xa[u][i], xb[u][i]);
-        if (!k.ok) {
+        if (lane.slot[i].rot) g[i].turn(xa[i], xb[i]);
+        if (!ok) {
 #pragma unroll
-          for (int e = 0; e < V; ++e) xa[u][i][e] = xb[u][i][e] = 0.f;
+          for (int e = 0; e < M; ++e) xa[i][e] = xb[i][e] = splat<V>(0.f);
         }
-        store<IL>(y, L.slot[i], xa[u][i], xb[u][i]);
+        store<IL>(y + h * a.D, lane.slot[i], xa[i], xb[i]);
       }
     }
   }
 }
 
 template <typename T, int V, int NP, int LR, bool IL, bool NORM>
-__global__ void __launch_bounds__(kThreads) qk_rope_bwd_kernel(Args a) {
-  constexpr int GW = 32 / LR, U = V == 4 ? 2 : 1;
-  extern __shared__ float sums[];  // NORM: [kWarps * GW][2][D]
+__global__ void __launch_bounds__(kThreads, 2) qk_rope_bwd_kernel(Args a) {
+  using L = Lane<V, NP, LR, IL>;
+  using N = Num<V>;
+  constexpr int GW = L::GW, U = V == 4 ? 2 : 1, M = kNums<V>;
+  extern __shared__ float sums[];  // NORM: [kWarps * GW][D]
   tc::grid_dep_launch();
-  const Lane<V, NP, LR, IL> L(a);
-  float dwq[2][NP][V], dwk[2][NP][V], wq[2][NP][V], wk[2][NP][V];
+  const L lane(a);
+  uint32_t cta, ctas;
+  const Side s = side_of(a, cta, ctas);
+  N wa[NP][M], wb[NP][M], da[NP][M], db[NP][M];
   if constexpr (NORM) {
-    L.weights(a.wq, wq[0], wq[1]), L.weights(a.wk, wk[0], wk[1]);
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < NP; ++i)
-#pragma unroll
-        for (int e = 0; e < V; ++e) dwq[h][i][e] = dwk[h][i][e] = 0.f;
-  }
-  const int step = a.split * GW;
-  for (long job = (long)blockIdx.x * kWarps + (threadIdx.x >> 5); job < a.tokens * a.split;
-       job += (long)gridDim.x * kWarps) {
-    const long tok = job / a.split;
-    const Token<V, NP> k = L.token(a, tok);
-    for (int r0 = (int)(job % a.split) * GW; r0 < a.rows; r0 += U * step) {
-      Raw<T, V> x[U][NP], g[U][NP];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int r = r0 + u * step + L.grp;
-        const bool in = r < a.rows && k.ok;
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          x[u][i] = in ? load(input<T>(a, k.b, k.t, r), L.slot[i]) : Raw<T, V>{};
-          g[u][i] = in ? load(static_cast<const T*>(dense<T>(a, const_cast<void*>(a.dqo), const_cast<void*>(a.dko), tok, r)),
-                              L.slot[i])
-                       : Raw<T, V>{};
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int r = r0 + u * step + L.grp;
-        float ga[NP][V], gb[NP][V];
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          widen<IL>(g[u][i], ga[i], gb[i]);
-          if (L.slot[i].rot) {
-            float s[V];
-#pragma unroll
-            for (int e = 0; e < V; ++e) s[e] = -k.s[i][e];
-            rotate<V>(k.c[i], s, ga[i], gb[i]);
-          }
-        }
-        if constexpr (NORM) {
-          const bool isq = r < a.H;
-          float xa[NP][V], xb[NP][V], ss = 0.f, sg = 0.f;
-#pragma unroll
-          for (int i = 0; i < NP; ++i) {
-            widen<IL>(x[u][i], xa[i], xb[i]);
-#pragma unroll
-            for (int e = 0; e < V; ++e) ss = fmaf(xa[i][e], xa[i][e], fmaf(xb[i][e], xb[i][e], ss));
-          }
-          // rows past the last (and tokens without angles) add 0, with eps = 0 too
-          const float mean = row_sum<LR>(ss) * a.inv_d, rstd = r < a.rows && k.ok ? rsqrtf(mean + a.eps) : 0.f;
-#pragma unroll
-          for (int i = 0; i < NP; ++i)
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-              xa[i][e] *= rstd, xb[i][e] *= rstd;
-              const float ta = ga[i][e] * xa[i][e], tb = gb[i][e] * xb[i][e];
-              const float wa = isq ? wq[0][i][e] : wk[0][i][e], wb = isq ? wq[1][i][e] : wk[1][i][e];
-              if (isq) dwq[0][i][e] += ta, dwq[1][i][e] += tb;
-              else dwk[0][i][e] += ta, dwk[1][i][e] += tb;
-              sg = fmaf(ta, wa, fmaf(tb, wb, sg));
-              ga[i][e] *= wa, gb[i][e] *= wb;
-            }
-          const float m = row_sum<LR>(sg) * a.inv_d;
-#pragma unroll
-          for (int i = 0; i < NP; ++i)
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-              ga[i][e] = rstd * fmaf(-xa[i][e], m, ga[i][e]);
-              gb[i][e] = rstd * fmaf(-xb[i][e], m, gb[i][e]);
-            }
-        }
-        if (r >= a.rows) continue;
-        T* d = dense<T>(a, a.dq, a.dk, tok, r);
-#pragma unroll
-        for (int i = 0; i < NP; ++i) store<IL>(d, L.slot[i], ga[i], gb[i]);
-      }
-    }
-  }
-  if constexpr (NORM) {
-    float* mine = sums + (size_t)((threadIdx.x >> 5) * GW + L.grp) * 2 * a.D;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      store<IL>(mine, L.slot[i], dwq[0][i], dwq[1][i]);
-      store<IL>(mine + a.D, L.slot[i], dwk[0][i], dwk[1][i]);
+      widen<IL>(load<float, V>(s.w, lane.slot[i]), wa[i], wb[i]);
+#pragma unroll
+      for (int e = 0; e < M; ++e) da[i][e] = db[i][e] = splat<V>(0.f);
     }
+  }
+  for (uint64_t job = cta * kWarps + (threadIdx.x >> 5); job < (uint64_t)a.tokens * s.parts; job += ctas * kWarps) {
+    const uint32_t tok = (uint32_t)(job / s.parts), h0 = (uint32_t)(job % s.parts) * s.chunk, b = tok / a.T, t = tok % a.T;
+    const uint32_t h1 = min(h0 + s.chunk, s.H);
+    const T* x = static_cast<const T*>(s.x) + b * s.st[0] + t * s.st[1];
+    const T* dy = static_cast<const T*>(s.dy) + (uint64_t)tok * s.H * a.D;
+    T* dx = static_cast<T*>(s.dx) + (uint64_t)tok * s.H * a.D;
+    Raw<T, V> nx[U][NP], ng[U][NP];
+    auto fetch = [&](int u, uint32_t h) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        if constexpr (NORM) nx[u][i] = h < h1 ? load(x + h * s.st[2], lane.slot[i]) : Raw<T, V>{};
+        ng[u][i] = h < h1 ? load(dy + h * a.D, lane.slot[i]) : Raw<T, V>{};
+      }
+    };
+#pragma unroll
+    for (int u = 0; u < U; ++u) fetch(u, h0 + u * GW + lane.grp);
+    Angles<V> g[NP];
+    const bool ok = lane.angles(a, tok, t, g);
+    for (uint32_t h = h0 + lane.grp; h < h0 + s.chunk; h += GW) {
+      N xa[NP][M], xb[NP][M], ga[NP][M], gb[NP][M];
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        if constexpr (NORM) widen<IL>(nx[0][i], xa[i], xb[i]);
+        widen<IL>(ng[0][i], ga[i], gb[i]);
+      }
+#pragma unroll
+      for (int u = 0; u + 1 < U; ++u)
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          if constexpr (NORM) nx[u][i] = nx[u + 1][i];
+          ng[u][i] = ng[u + 1][i];
+        }
+      fetch(U - 1, h + U * GW);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        if (!ok) {  // no gradient (0, not 0 times what may be no number)
+#pragma unroll
+          for (int e = 0; e < M; ++e) ga[i][e] = gb[i][e] = splat<V>(0.f);
+          if constexpr (NORM) {
+#pragma unroll
+            for (int e = 0; e < M; ++e) xa[i][e] = xb[i][e] = splat<V>(0.f);
+          }
+        }
+        if (lane.slot[i].rot) g[i].turn_back(ga[i], gb[i]);
+      }
+      if constexpr (NORM) {
+        N ss = splat<V>(0.f), sg = ss;
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+#pragma unroll
+          for (int e = 0; e < M; ++e) ss = fma(xa[i][e], xa[i][e], fma(xb[i][e], xb[i][e], ss));
+        // rows past the last (and tokens without angles) add 0, with eps = 0 too
+        const float mean = row_sum<LR>(total(ss)) * a.inv_d, rstd = h < h1 && ok ? rsqrtf(mean + a.eps) : 0.f;
+        const N r = splat<V>(rstd);
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+#pragma unroll
+          for (int e = 0; e < M; ++e) {
+            xa[i][e] = mul(xa[i][e], r), xb[i][e] = mul(xb[i][e], r);
+            da[i][e] = fma(ga[i][e], xa[i][e], da[i][e]), db[i][e] = fma(gb[i][e], xb[i][e], db[i][e]);
+            ga[i][e] = mul(ga[i][e], wa[i][e]), gb[i][e] = mul(gb[i][e], wb[i][e]);
+            sg = fma(ga[i][e], xa[i][e], fma(gb[i][e], xb[i][e], sg));
+          }
+        const N m = splat<V>(-row_sum<LR>(total(sg)) * a.inv_d);
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+#pragma unroll
+          for (int e = 0; e < M; ++e)
+            ga[i][e] = mul(r, fma(xa[i][e], m, ga[i][e])), gb[i][e] = mul(r, fma(xb[i][e], m, gb[i][e]));
+      }
+      if (h >= h1) continue;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) store<IL>(dx + h * a.D, lane.slot[i], ga[i], gb[i]);
+    }
+  }
+  if constexpr (NORM) {
+    float* mine = sums + (size_t)((threadIdx.x >> 5) * GW + lane.grp) * a.D;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) store<IL>(mine, lane.slot[i], da[i], db[i]);
     __syncthreads();
-    for (int c = threadIdx.x; c < 2 * a.D; c += kThreads) {
-      float s = 0.f;
-      for (int i = 0; i < kWarps * GW; ++i) s += sums[(size_t)i * 2 * a.D + c];
-      a.partial[(long)blockIdx.x * 2 * a.D + c] = s;
+    for (int c = threadIdx.x; c < a.D; c += kThreads) {
+      float x = 0.f;
+      for (int i = 0; i < kWarps * GW; ++i) x += sums[(size_t)i * a.D + c];
+      a.partial[(long)blockIdx.x * a.D + c] = x;
     }
   }
 }
 
-// dw of q (columns 0 .. D - 1) and k: the CTAs' sums.  Eight warps take every
-// eighth CTA for 32 columns, and their sums are added in order.
-__global__ void __launch_bounds__(256) qk_rope_sum_kernel(const float* partial, int ctas, int D, float* dwq, float* dwk) {
-  __shared__ float s[8][32];
+// dw: the sums of a side's CTAs.  32 warps take every 32nd CTA for 32 columns, and
+// their sums are added in order.
+__global__ void __launch_bounds__(1024) qk_rope_sum_kernel(Args a, int ctas) {
+  __shared__ float s[32][33];
   tc::grid_dep_wait();
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane;
+  const int first = blockIdx.y ? a.ctas0 : 0, end = blockIdx.y ? ctas : a.ctas0;
   float x = 0.f;
-  if (c < 2 * D) {
-#pragma unroll 8
-    for (int i = w; i < ctas; i += 8) x += partial[(long)i * 2 * D + c];
+  if (c < a.D) {
+#pragma unroll 4
+    for (int i = first + w; i < end; i += 32) x += a.partial[(long)i * a.D + c];
   }
   s[w][lane] = x;
   __syncthreads();
-  if (w > 0 || c >= 2 * D) return;
+  if (w > 0 || c >= a.D) return;
   x = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x += s[i][lane];
-  (c < D ? dwq[c] : dwk[c - D]) = x;
+  for (int i = 0; i < 32; ++i) x += s[i][lane];
+  a.side[blockIdx.y].dw[c] = x;
 }
 
 // ---------------------------------------------------------------- host
 
-constexpr int kBwdCtasPerSm = 3;
+constexpr int kCtasPerSm = 2;
 
-// CTAs of the backward: as many as run at once, and no more than there are tokens' parts.
-int bwd_ctas(long tokens, int split) {
-  return (int)std::max(1L, std::min((long)kBwdCtasPerSm * sm_count(), (tokens * split + kWarps - 1) / kWarps));
-}
-
-bool use_vectors(const QkRopeProblem& p) {
+// Whether all rows go in vectors of V pairs' halves.
+bool use_vectors(const QkRopeProblem& p, int V) {
   const size_t e = p.bf16 ? 2 : 4;
-  if (p.D % 8 || p.R % 8) return false;
+  if (p.D % (2 * V) || p.R % (2 * V)) return false;
   if (!vectors(p.q, p.qs, e) || !vectors(p.k, p.ks, e)) return false;
   for (const void* x : {(const void*)p.wq, (const void*)p.wk, (const void*)p.cos, (const void*)p.sin})
     if ((uintptr_t)x & 15) return false;
   return true;
 }
 
-// Warps per token: enough that the GPU has some 16 warps per SM, if the heads allow.
-int split_of(long tokens, int rows, int gw) {
-  const long want = (16L * sm_count() + tokens - 1) / tokens;
-  return (int)std::max(1L, std::min(want, (long)(rows + gw - 1) / gw));
+// Heads per job: all of a token's, or fewer (in passes of gw) until every warp that
+// runs at once has a job.
+void set_jobs(Side& s, uint32_t tokens, int gw, long warps) {
+  const long passes = (s.H + gw - 1) / gw, want = std::max(1L, std::min(passes, (warps + tokens - 1) / tokens));
+  s.chunk = (int)((passes + want - 1) / want) * gw;
+  s.parts = s.H ? (s.H + s.chunk - 1) / s.chunk : 0;
 }
 
 template <typename T, int V, int NP, int LR, bool IL, bool NORM>
-cudaError_t launch(const QkRopeProblem& p, Args a, bool bwd, cudaStream_t s) {
+cudaError_t launch(Args a, bool bwd, cudaStream_t s) {
   constexpr int GW = 32 / LR;
-  a.split = split_of(a.tokens, a.rows, GW);
+  const int most = kCtasPerSm * sm_count(), H = a.side[0].H + a.side[1].H;
+  int ctas[2];
+  for (int i = 0; i < 2; ++i) {
+    Side& x = a.side[i];
+    const long share = std::max(1L, (long)most * x.H / H);
+    set_jobs(x, a.tokens, GW, share * kWarps);
+    ctas[i] = x.H ? (int)std::min(share, ((long)a.tokens * x.parts + kWarps - 1) / kWarps) : 0;
+  }
+  a.ctas0 = ctas[0];
+  const int all = ctas[0] + ctas[1];
   if (!bwd) {
-    const long ctas = (a.tokens * a.split + kWarps - 1) / kWarps;
     prof_before(s);
-    qk_rope_fwd_kernel<T, V, NP, LR, IL, NORM><<<(unsigned)ctas, kThreads, 0, s>>>(a);
+    qk_rope_fwd_kernel<T, V, NP, LR, IL, NORM><<<all, kThreads, 0, s>>>(a);
     prof_after(s, kQkRopeFwd);
     return cudaGetLastError();
   }
-  const int ctas = bwd_ctas(a.tokens, a.split);
-  const size_t smem = NORM ? (size_t)kWarps * GW * 2 * a.D * sizeof(float) : 0;
+  const size_t smem = NORM ? (size_t)kWarps * GW * a.D * sizeof(float) : 0;
   prof_before(s);
-  qk_rope_bwd_kernel<T, V, NP, LR, IL, NORM><<<ctas, kThreads, smem, s>>>(a);
+  qk_rope_bwd_kernel<T, V, NP, LR, IL, NORM><<<all, kThreads, smem, s>>>(a);
   prof_after(s, kQkRopeBwd);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !NORM) return e;
   prof_before(s);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((2 * a.D + 31) / 32), cfg.blockDim = dim3(256), cfg.stream = s;
+  cfg.gridDim = dim3((a.D + 31) / 32, 2), cfg.blockDim = dim3(1024), cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr, cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, qk_rope_sum_kernel, (const float*)a.partial, ctas, a.D, p.dwq, p.dwk);
+  e = cudaLaunchKernelEx(&cfg, qk_rope_sum_kernel, a, all);
   prof_after(s, kQkRopeSum);
   return e;
 }
 
 template <typename T, bool IL, bool NORM>
 cudaError_t by_size(const QkRopeProblem& p, const Args& a, bool bwd, cudaStream_t s) {
-  if (!use_vectors(p)) return launch<T, 1, 2, 32, IL, NORM>(p, a, bwd, s);
-  if (p.D <= 64) return launch<T, 4, 1, 8, IL, NORM>(p, a, bwd, s);
-  return launch<T, 4, 1, 16, IL, NORM>(p, a, bwd, s);
+  if constexpr (sizeof(T) == 2) {
+    if (use_vectors(p, 8))
+      return p.D <= 64 ? launch<T, 8, 1, 4, IL, NORM>(a, bwd, s) : launch<T, 8, 1, 8, IL, NORM>(a, bwd, s);
+  }
+  if (use_vectors(p, 4))
+    return p.D <= 64 ? launch<T, 4, 1, 8, IL, NORM>(a, bwd, s) : launch<T, 4, 1, 16, IL, NORM>(a, bwd, s);
+  return launch<T, 1, 2, 32, IL, NORM>(a, bwd, s);
 }
 
 template <typename T>
@@ -356,21 +356,23 @@ cudaError_t by_kind(const QkRopeProblem& p, const Args& a, bool bwd, cudaStream_
 
 cudaError_t run(const QkRopeProblem& p, bool bwd, cudaStream_t s) {
   Args a = {};
-  a.T = p.T, a.H = p.H, a.rows = p.H + p.Hkv, a.D = p.D, a.R = p.R, a.P = p.P;
-  a.tokens = (long)p.B * p.T;
+  a.T = p.T, a.D = p.D, a.R = p.R, a.P = p.P;
+  a.tokens = (uint32_t)((long)p.B * p.T);
   a.eps = p.eps, a.inv_d = 1.f / p.D;
-  for (int i = 0; i < 3; ++i) a.qs[i] = p.qs[i], a.ks[i] = p.ks[i];
-  a.q = p.q, a.k = p.k, a.wq = p.wq, a.wk = p.wk, a.cos = p.cos, a.sin = p.sin, a.pos = p.pos;
-  a.qo = p.qo, a.ko = p.ko, a.dqo = p.dqo, a.dko = p.dko, a.dq = p.dq, a.dk = p.dk;
+  Side &q = a.side[0], &k = a.side[1];
+  for (int i = 0; i < 3; ++i) q.st[i] = p.qs[i], k.st[i] = p.ks[i];
+  q.x = p.q, q.dy = p.dqo, q.y = p.qo, q.dx = p.dq, q.w = p.wq, q.dw = p.dwq, q.H = p.H;
+  k.x = p.k, k.dy = p.dko, k.y = p.ko, k.dx = p.dk, k.w = p.wk, k.dw = p.dwk, k.H = p.Hkv;
+  a.cos = p.cos, a.sin = p.sin, a.pos = p.pos;
   a.partial = static_cast<float*>(p.ws);
   return p.bf16 ? by_kind<__nv_bfloat16>(p, a, bwd, s) : by_kind<float>(p, a, bwd, s);
 }
 
 }  // namespace
 
-// The most CTAs that any choice of kernel has.
+// Sums of every CTA that may run (each side has one at least).
 size_t qk_rope_bwd_workspace(const QkRopeProblem& p) {
-  return (size_t)kBwdCtasPerSm * sm_count() * 2 * p.D * sizeof(float);
+  return (size_t)(kCtasPerSm * sm_count() + 2) * p.D * sizeof(float);
 }
 
 cudaError_t qk_rope_fwd(const QkRopeProblem& p, cudaStream_t s) { return run(p, false, s); }
