@@ -121,12 +121,13 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a) {
   // row r of the token at its place in q, k and v
   auto fetch = [&](Raw<T, V> (&x)[NP], uint32_t tok, int r) {
     const uint32_t b = tok / a.T, t = tok % a.T;
+    r = min(r, a.rows - 1);  // rows past the last: the last again
     const int h = r - a.H;
     const T* p = r < a.H      ? static_cast<const T*>(a.q) + b * a.qs[0] + t * a.qs[1] + r * a.qs[2]
                  : h < a.Hkv  ? static_cast<const T*>(a.k) + b * a.ks[0] + t * a.ks[1] + h * a.ks[2]
                               : static_cast<const T*>(a.v) + b * a.vs[0] + t * a.vs[1] + (h - a.Hkv) * a.vs[2];
 #pragma unroll
-    for (int i = 0; i < NP; ++i) x[i] = r < a.rows ? load(p, slot[i]) : Raw<T, V>{};
+    for (int i = 0; i < NP; ++i) x[i] = load(p, slot[i]);
   };
   const int step = a.parts * GW;
   const uint32_t jobs = n * a.parts;
@@ -140,9 +141,10 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a) {
     const int part = job % a.parts;
     const Place at = place[i0];
     Angles<V> g[NP];
+    if (a.R && at.turn) {
 #pragma unroll
-    for (int i = 0; i < NP; ++i)
-      g[i].set(a.cos, a.sin, (long long)at.n * (a.R / 2), (l + i * LR) * V, slot[i].rot && at.turn);
+      for (int i = 0; i < NP; ++i) g[i].set(a.cos, a.sin, (long long)at.n * (a.R / 2), (l + i * LR) * V, slot[i].rot);
+    }
     for (int r0 = part * GW; r0 < a.rows; r0 += step) {
       const int r = r0 + grp, h = r - a.H;
       N xa[NP][M], xb[NP][M];
@@ -155,7 +157,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a) {
       }
 #pragma unroll
       for (int i = 0; i < NP; ++i)
-        if (slot[i].rot && h < a.Hkv) g[i].turn(xa[i], xb[i]);
+        if (slot[i].rot && h < a.Hkv && at.turn) g[i].turn(xa[i], xb[i]);
       if (r < a.H) {
         T* y = static_cast<T*>(a.qo) + ((uint64_t)tok * a.H + r) * a.D;
 #pragma unroll

@@ -63,20 +63,47 @@ struct Lane {
   }
   __device__ __forceinline__ static int first(int i) { return ((threadIdx.x & 31) % LR + i * LR) * V; }
 
-  // The angles of a token, the same for all lanes of the warp; false: its position has none.
-  __device__ __forceinline__ bool angles(const Args& a, uint32_t tok, uint32_t t, Angles<V> (&g)[NP]) const {
-    int n = 0;
-    bool ok = true;
-    if (a.R) {
-      n = a.pos ? a.pos[tok] : (int)t;
-      if (n < 0 || n >= a.P) {
-        ok = false, n = 0;
-        if ((threadIdx.x & 31) == 0) atomicExch(&tc::g_file_status, GDN_ERR_SEQLENS);
-      }
-    }
+  // The angles of a position, the same for all lanes of the warp; false: it has none.
+  __device__ __forceinline__ bool angles(const Args& a, int n, Angles<V> (&g)[NP]) const {
+    if (a.R == 0) return true;
+    const bool ok = n >= 0 && n < a.P;
+    if (!ok && (threadIdx.x & 31) == 0) atomicExch(&tc::g_file_status, GDN_ERR_SEQLENS);
+    if (!ok) return false;
 #pragma unroll
-    for (int i = 0; i < NP; ++i) g[i].set(a.cos, a.sin, (long long)n * (a.R / 2), first(i), slot[i].rot && ok);
-    return ok;
+    for (int i = 0; i < NP; ++i) g[i].set(a.cos, a.sin, (long long)n * (a.R / 2), first(i), slot[i].rot);
+    return true;
+  }
+  // The sum over a row of what its lanes have.
+  __device__ __forceinline__ float sum(Num<V> x) const { return row_sum<LR>(V == 1 || slot[0].in ? total(x) : 0.f); }
+};
+
+// A warp's way through its jobs: passes of GW heads, loaded ahead across the ends of
+// jobs.
+struct Pass {
+  uint32_t tok, h, h1;  // heads h .. of a token, those below h1; no token: no pass
+  int pos;
+  bool fresh;           // the first of its job
+};
+struct Cursor {
+  Pass p;
+  uint32_t job, end;  // the job's passes end at head `end`
+  long long at;       // the token's offset in x
+  __device__ __forceinline__ void start(const Args& a, const Side& s, uint32_t j) {
+    job = j;
+    uint32_t part = 0;
+    p.tok = j;
+    if (s.parts > 1) p.tok = j / s.parts, part = j % s.parts;
+    p.h = part * s.chunk, end = p.h + s.chunk, p.h1 = 0, p.fresh = true, p.pos = 0, at = 0;
+    if (p.tok >= a.tokens) return;
+    p.h1 = min(end, (uint32_t)s.H);
+    const uint32_t b = p.tok / a.T, t = p.tok % a.T;
+    p.pos = a.R && a.pos ? a.pos[p.tok] : (int)t;
+    at = b * s.st[0] + t * s.st[1];
+  }
+  template <int GW>
+  __device__ __forceinline__ void next(const Args& a, const Side& s, uint32_t stride) {
+    p.h += GW, p.fresh = false;
+    if (p.h >= end && p.tok < a.tokens) start(a, s, job + stride);
   }
 };
 
@@ -92,7 +119,7 @@ template <typename T, int V, int NP, int LR, bool IL, bool NORM>
 __global__ void __launch_bounds__(kThreads, 2) qk_rope_fwd_kernel(Args a) {
   using L = Lane<V, NP, LR, IL>;
   using N = Num<V>;
-  constexpr int GW = L::GW, U = V == 1 ? 1 : 3, M = kNums<V>;  // U: rows on their way
+  constexpr int GW = L::GW, U = V == 1 ? 1 : 2, M = kNums<V>;  // U: passes on their way
   const L lane(a);
   uint32_t cta, ctas;
   const Side s = side_of(a, cta, ctas);
@@ -101,50 +128,60 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rope_fwd_kernel(Args a) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) widen<IL>(load<float, V>(s.w, lane.slot[i]), wa[i], wb[i]);
   }
-  for (uint64_t job = cta * kWarps + (threadIdx.x >> 5); job < (uint64_t)a.tokens * s.parts; job += ctas * kWarps) {
-    const uint32_t tok = (uint32_t)(job / s.parts), h0 = (uint32_t)(job % s.parts) * s.chunk, b = tok / a.T, t = tok % a.T;
-    const uint32_t h1 = min(h0 + s.chunk, s.H);
-    const T* x = static_cast<const T*>(s.x) + b * s.st[0] + t * s.st[1];
-    T* y = static_cast<T*>(s.y) + (uint64_t)tok * s.H * a.D;
-    Raw<T, V> next[U][NP];
-    auto fetch = [&](Raw<T, V> (&r)[NP], uint32_t h) {
+  const uint32_t stride = ctas * kWarps;
+  Cursor f;
+  f.start(a, s, cta * kWarps + (threadIdx.x >> 5));
+  Raw<T, V> next[U][NP];
+  Pass pass[U];
+  auto fetch = [&](int u) {
+    if (f.p.tok < a.tokens) {  // heads past the last: the last again
+      const T* x = static_cast<const T*>(s.x) + f.at + min(f.p.h + lane.grp, f.p.h1 - 1) * s.st[2];
 #pragma unroll
-      for (int i = 0; i < NP; ++i) r[i] = h < h1 ? load(x + h * s.st[2], lane.slot[i]) : Raw<T, V>{};
-    };
+      for (int i = 0; i < NP; ++i) next[u][i] = load(x, lane.slot[i]);
+    }
+    pass[u] = f.p;
+    f.next<GW>(a, s, stride);
+  };
 #pragma unroll
-    for (int u = 0; u < U; ++u) fetch(next[u], h0 + u * GW + lane.grp);
-    Angles<V> g[NP];
-    const bool ok = lane.angles(a, tok, t, g);
-    for (uint32_t h = h0 + lane.grp; h < h0 + s.chunk; h += GW) {  // the same number of passes for all lanes
-      N xa[NP][M], xb[NP][M];
+  for (int u = 0; u < U; ++u) fetch(u);
+  Angles<V> g[NP];
+  bool ok = true;
+  while (pass[0].tok < a.tokens) {
+    const Pass c = pass[0];
+    if (c.fresh) ok = lane.angles(a, c.pos, g);
+    N xa[NP][M], xb[NP][M];
 #pragma unroll
-      for (int i = 0; i < NP; ++i) widen<IL>(next[0][i], xa[i], xb[i]);
+    for (int i = 0; i < NP; ++i) widen<IL>(next[0][i], xa[i], xb[i]);
 #pragma unroll
-      for (int u = 0; u + 1 < U; ++u)
+    for (int u = 0; u + 1 < U; ++u) {
 #pragma unroll
-        for (int i = 0; i < NP; ++i) next[u][i] = next[u + 1][i];
-      fetch(next[U - 1], h + U * GW);
-      if constexpr (NORM) {
-        N ss = splat<V>(0.f);
+      for (int i = 0; i < NP; ++i) next[u][i] = next[u + 1][i];
+      pass[u] = pass[u + 1];
+    }
+    fetch(U - 1);
+    if constexpr (NORM) {
+      N ss = splat<V>(0.f);
 #pragma unroll
-        for (int i = 0; i < NP; ++i)
+      for (int i = 0; i < NP; ++i)
 #pragma unroll
-          for (int e = 0; e < M; ++e) ss = fma(xa[i][e], xa[i][e], fma(xb[i][e], xb[i][e], ss));
-        const N r = splat<V>(rsqrtf(row_sum<LR>(total(ss)) * a.inv_d + a.eps));
+        for (int e = 0; e < M; ++e) ss = fma(xa[i][e], xa[i][e], fma(xb[i][e], xb[i][e], ss));
+      const N r = splat<V>(rsqrtf(lane.sum(ss) * a.inv_d + a.eps));
 #pragma unroll
-        for (int i = 0; i < NP; ++i)
+      for (int i = 0; i < NP; ++i)
 #pragma unroll
-          for (int e = 0; e < M; ++e) xa[i][e] = mul(mul(xa[i][e], r), wa[i][e]), xb[i][e] = mul(mul(xb[i][e], r), wb[i][e]);
-      }
-      if (h >= h1) continue;
+        for (int e = 0; e < M; ++e) xa[i][e] = mul(mul(xa[i][e], r), wa[i][e]), xb[i][e] = mul(mul(xb[i][e], r), wb[i][e]);
+    }
+    const uint32_t h = c.h + lane.grp;
+    if (h < c.h1) {
+      T* y = static_cast<T*>(s.y) + ((uint64_t)c.tok * s.H + h) * a.D;
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        if (lane.slot[i].rot) g[i].turn(xa[i], xb[i]);
+        if (lane.slot[i].rot) NORM ? g[i].turn_fused(xa[i], xb[i]) : g[i].turn(xa[i], xb[i]);
         if (!ok) {
 #pragma unroll
           for (int e = 0; e < M; ++e) xa[i][e] = xb[i][e] = splat<V>(0.f);
         }
-        store<IL>(y + h * a.D, lane.slot[i], xa[i], xb[i]);
+        store<IL>(y, lane.slot[i], xa[i], xb[i]);
       }
     }
   }
@@ -155,93 +192,110 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rope_bwd_kernel(Args a) {
   using L = Lane<V, NP, LR, IL>;
   using N = Num<V>;
   constexpr int GW = L::GW, U = V == 4 ? 2 : 1, M = kNums<V>;
-  extern __shared__ float sums[];  // NORM: [kWarps * GW][D]
+  extern __shared__ __align__(16) float sums[];  // NORM: [kWarps * GW][D]
+  // The weights lie in shared memory: with them in registers, what is loaded ahead
+  // was spilled, and so waited for at once.
+  __shared__ __align__(16) float w[128];
   tc::grid_dep_launch();
   const L lane(a);
   uint32_t cta, ctas;
   const Side s = side_of(a, cta, ctas);
-  N wa[NP][M], wb[NP][M], da[NP][M], db[NP][M];
+  N da[NP][M], db[NP][M];
   if constexpr (NORM) {
+    for (int i = threadIdx.x; i < a.D; i += kThreads) w[i] = s.w[i];
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      widen<IL>(load<float, V>(s.w, lane.slot[i]), wa[i], wb[i]);
+    for (int i = 0; i < NP; ++i)
 #pragma unroll
       for (int e = 0; e < M; ++e) da[i][e] = db[i][e] = splat<V>(0.f);
-    }
   }
-  for (uint64_t job = cta * kWarps + (threadIdx.x >> 5); job < (uint64_t)a.tokens * s.parts; job += ctas * kWarps) {
-    const uint32_t tok = (uint32_t)(job / s.parts), h0 = (uint32_t)(job % s.parts) * s.chunk, b = tok / a.T, t = tok % a.T;
-    const uint32_t h1 = min(h0 + s.chunk, s.H);
-    const T* x = static_cast<const T*>(s.x) + b * s.st[0] + t * s.st[1];
-    const T* dy = static_cast<const T*>(s.dy) + (uint64_t)tok * s.H * a.D;
-    T* dx = static_cast<T*>(s.dx) + (uint64_t)tok * s.H * a.D;
-    Raw<T, V> nx[U][NP], ng[U][NP];
-    auto fetch = [&](int u, uint32_t h) {
+  const uint32_t stride = ctas * kWarps;
+  Cursor f;
+  f.start(a, s, cta * kWarps + (threadIdx.x >> 5));
+  Raw<T, V> nx[U][NP], ng[U][NP];
+  Pass pass[U];
+  auto fetch = [&](int u) {
+    if (f.p.tok < a.tokens) {  // heads past the last: the last again
+      const uint32_t h = min(f.p.h + lane.grp, f.p.h1 - 1);
+      const T* x = static_cast<const T*>(s.x) + f.at + h * s.st[2];
+      const T* dy = static_cast<const T*>(s.dy) + ((uint64_t)f.p.tok * s.H + h) * a.D;
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        if constexpr (NORM) nx[u][i] = h < h1 ? load(x + h * s.st[2], lane.slot[i]) : Raw<T, V>{};
-        ng[u][i] = h < h1 ? load(dy + h * a.D, lane.slot[i]) : Raw<T, V>{};
+        if constexpr (NORM) nx[u][i] = load(x, lane.slot[i]);
+        ng[u][i] = load(dy, lane.slot[i]);
       }
-    };
+    }
+    pass[u] = f.p;
+    f.next<GW>(a, s, stride);
+  };
 #pragma unroll
-    for (int u = 0; u < U; ++u) fetch(u, h0 + u * GW + lane.grp);
-    Angles<V> g[NP];
-    const bool ok = lane.angles(a, tok, t, g);
-    for (uint32_t h = h0 + lane.grp; h < h0 + s.chunk; h += GW) {
-      N xa[NP][M], xb[NP][M], ga[NP][M], gb[NP][M];
+  for (int u = 0; u < U; ++u) fetch(u);
+  Angles<V> g[NP];
+  bool ok = true;
+  while (pass[0].tok < a.tokens) {
+    const Pass c = pass[0];
+    if (c.fresh) ok = lane.angles(a, c.pos, g);
+    N xa[NP][M], xb[NP][M], ga[NP][M], gb[NP][M];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      if constexpr (NORM) widen<IL>(nx[0][i], xa[i], xb[i]);
+      widen<IL>(ng[0][i], ga[i], gb[i]);
+    }
+#pragma unroll
+    for (int u = 0; u + 1 < U; ++u) {
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        if constexpr (NORM) widen<IL>(nx[0][i], xa[i], xb[i]);
-        widen<IL>(ng[0][i], ga[i], gb[i]);
+        if constexpr (NORM) nx[u][i] = nx[u + 1][i];
+        ng[u][i] = ng[u + 1][i];
       }
+      pass[u] = pass[u + 1];
+    }
+    fetch(U - 1);
+    const uint32_t h = c.h + lane.grp;
 #pragma unroll
-      for (int u = 0; u + 1 < U; ++u)
+    for (int i = 0; i < NP; ++i) {
+      if (!ok) {  // no gradient (0, not 0 times what may be no number)
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          if constexpr (NORM) nx[u][i] = nx[u + 1][i];
-          ng[u][i] = ng[u + 1][i];
+        for (int e = 0; e < M; ++e) ga[i][e] = gb[i][e] = splat<V>(0.f);
+        if constexpr (NORM) {
+#pragma unroll
+          for (int e = 0; e < M; ++e) xa[i][e] = xb[i][e] = splat<V>(0.f);
         }
-      fetch(U - 1, h + U * GW);
+      }
+      if (lane.slot[i].rot && ok) g[i].turn_back(ga[i], gb[i]);
+    }
+    if constexpr (NORM) {
+      N ss = splat<V>(0.f), sg = ss;
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+#pragma unroll
+        for (int e = 0; e < M; ++e) ss = fma(xa[i][e], xa[i][e], fma(xb[i][e], xb[i][e], ss));
+      // rows past the last (and tokens without angles) add 0, with eps = 0 too
+      const float mean = lane.sum(ss) * a.inv_d, rstd = h < c.h1 && ok ? rsqrtf(mean + a.eps) : 0.f;
+      const N r = splat<V>(rstd);
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        if (!ok) {  // no gradient (0, not 0 times what may be no number)
+        N wa[M], wb[M];
+        widen<IL>(load<float, V>(w, lane.slot[i]), wa, wb);
 #pragma unroll
-          for (int e = 0; e < M; ++e) ga[i][e] = gb[i][e] = splat<V>(0.f);
-          if constexpr (NORM) {
-#pragma unroll
-            for (int e = 0; e < M; ++e) xa[i][e] = xb[i][e] = splat<V>(0.f);
-          }
+        for (int e = 0; e < M; ++e) {
+          xa[i][e] = mul(xa[i][e], r), xb[i][e] = mul(xb[i][e], r);
+          da[i][e] = fma(ga[i][e], xa[i][e], da[i][e]), db[i][e] = fma(gb[i][e], xb[i][e], db[i][e]);
+          ga[i][e] = mul(ga[i][e], wa[e]), gb[i][e] = mul(gb[i][e], wb[e]);
+          sg = fma(ga[i][e], xa[i][e], fma(gb[i][e], xb[i][e], sg));
         }
-        if (lane.slot[i].rot) g[i].turn_back(ga[i], gb[i]);
       }
-      if constexpr (NORM) {
-        N ss = splat<V>(0.f), sg = ss;
+      const N m = splat<V>(-lane.sum(sg) * a.inv_d);
 #pragma unroll
-        for (int i = 0; i < NP; ++i)
+      for (int i = 0; i < NP; ++i)
 #pragma unroll
-          for (int e = 0; e < M; ++e) ss = fma(xa[i][e], xa[i][e], fma(xb[i][e], xb[i][e], ss));
-        // rows past the last (and tokens without angles) add 0, with eps = 0 too
-        const float mean = row_sum<LR>(total(ss)) * a.inv_d, rstd = h < h1 && ok ? rsqrtf(mean + a.eps) : 0.f;
-        const N r = splat<V>(rstd);
+        for (int e = 0; e < M; ++e)
+          ga[i][e] = mul(r, fma(xa[i][e], m, ga[i][e])), gb[i][e] = mul(r, fma(xb[i][e], m, gb[i][e]));
+    }
+    if (h < c.h1) {
+      T* dx = static_cast<T*>(s.dx) + ((uint64_t)c.tok * s.H + h) * a.D;
 #pragma unroll
-        for (int i = 0; i < NP; ++i)
-#pragma unroll
-          for (int e = 0; e < M; ++e) {
-            xa[i][e] = mul(xa[i][e], r), xb[i][e] = mul(xb[i][e], r);
-            da[i][e] = fma(ga[i][e], xa[i][e], da[i][e]), db[i][e] = fma(gb[i][e], xb[i][e], db[i][e]);
-            ga[i][e] = mul(ga[i][e], wa[i][e]), gb[i][e] = mul(gb[i][e], wb[i][e]);
-            sg = fma(ga[i][e], xa[i][e], fma(gb[i][e], xb[i][e], sg));
-          }
-        const N m = splat<V>(-row_sum<LR>(total(sg)) * a.inv_d);
-#pragma unroll
-        for (int i = 0; i < NP; ++i)
-#pragma unroll
-          for (int e = 0; e < M; ++e)
-            ga[i][e] = mul(r, fma(xa[i][e], m, ga[i][e])), gb[i][e] = mul(r, fma(xb[i][e], m, gb[i][e]));
-      }
-      if (h >= h1) continue;
-#pragma unroll
-      for (int i = 0; i < NP; ++i) store<IL>(dx + h * a.D, lane.slot[i], ga[i], gb[i]);
+      for (int i = 0; i < NP; ++i) store<IL>(dx, lane.slot[i], ga[i], gb[i]);
     }
   }
   if constexpr (NORM) {
@@ -307,7 +361,8 @@ cudaError_t launch(Args a, bool bwd, cudaStream_t s) {
   int ctas[2];
   for (int i = 0; i < 2; ++i) {
     Side& x = a.side[i];
-    const long share = std::max(1L, (long)most * x.H / H);
+    // a token costs what two more heads would
+    const long share = std::max(1L, (long)most * (x.H + 2) / (H + 4));
     set_jobs(x, a.tokens, GW, share * kWarps);
     ctas[i] = x.H ? (int)std::min(share, ((long)a.tokens * x.parts + kWarps - 1) / kWarps) : 0;
   }

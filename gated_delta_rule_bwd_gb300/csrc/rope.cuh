@@ -83,7 +83,8 @@ __device__ __forceinline__ uint32_t thin(F2 v) {
 }
 
 // Where slot p (pairs p .. p + V - 1) of a row lies: offsets of its two halves,
-// and whether it is rotated.  Past the rotated pairs a slot is 2 V values in a row.
+// and whether it is rotated.  Past the rotated pairs a slot is 2 V values in a row;
+// a lane without a slot reads the row's first.
 template <int V>
 struct Slot {
   int oa, ob;
@@ -96,6 +97,7 @@ struct Slot {
     else if (rot) oa = p, ob = p + R / 2;
     else oa = R + 2 * (p - R / 2), ob = oa + V;
     in_b = in && ob < D;  // an odd D leaves the last value without a partner
+    if (!in) oa = ob = 0;
   }
 };
 
@@ -106,13 +108,10 @@ __device__ __forceinline__ Raw<T, V> load(const T* row, const Slot<V>& s) {
     r.a = s.in ? row[s.oa] : from_f32<T>(0.f);
     r.b = s.in_b ? row[s.ob] : from_f32<T>(0.f);
   } else {
-    r = Raw<T, V>{};
-    if (s.in) {
-      using X = decltype(r.a);
-      r.a = *reinterpret_cast<const X*>(row + s.oa), r.b = *reinterpret_cast<const X*>(row + s.ob);
-      if constexpr (sizeof(T) == 4 && V == 8) {
-        r.a2 = *reinterpret_cast<const X*>(row + s.oa + 4), r.b2 = *reinterpret_cast<const X*>(row + s.ob + 4);
-      }
+    using X = decltype(r.a);
+    r.a = *reinterpret_cast<const X*>(row + s.oa), r.b = *reinterpret_cast<const X*>(row + s.ob);
+    if constexpr (sizeof(T) == 4 && V == 8) {
+      r.a2 = *reinterpret_cast<const X*>(row + s.oa + 4), r.b2 = *reinterpret_cast<const X*>(row + s.ob + 4);
     }
   }
   return r;
@@ -203,14 +202,15 @@ __device__ __forceinline__ void store(T* row, const Slot<V>& s, const Num<V> (&a
 template <int V>
 struct Angles {
   Num<V> c[kNums<V>], s[kNums<V>];
+  // rot: whether the slot is rotated at all (what else is loaded is not used)
   __device__ __forceinline__ void set(const float* cos, const float* sin, long long row, int p, bool rot) {
+    row += rot ? p : 0;
     if constexpr (V == 1) {
-      c[0] = rot ? cos[row + p] : 1.f, s[0] = rot ? sin[row + p] : 0.f;
+      c[0] = cos[row], s[0] = sin[row];
     } else {
 #pragma unroll
       for (int i = 0; i < V; i += 4) {
-        float4 x = make_float4(1.f, 1.f, 1.f, 1.f), y = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (rot) x = *reinterpret_cast<const float4*>(cos + row + p + i), y = *reinterpret_cast<const float4*>(sin + row + p + i);
+        const float4 x = *reinterpret_cast<const float4*>(cos + row + i), y = *reinterpret_cast<const float4*>(sin + row + i);
         c[i / 2] = pair(x.x, x.y), c[i / 2 + 1] = pair(x.z, x.w);
         s[i / 2] = pair(y.x, y.y), s[i / 2 + 1] = pair(y.z, y.w);
       }
@@ -233,6 +233,16 @@ struct Angles {
         turn1(x.x, y.x, p.x, q.x), turn1(x.y, y.y, p.y, q.y);
         a[i] = pair(x.x, x.y), b[i] = pair(y.x, y.y);
       }
+    }
+  }
+  // The same with fused multiply-adds, for rows that a norm has scaled before.
+  __device__ __forceinline__ void turn_fused(Num<V> (&a)[kNums<V>], Num<V> (&b)[kNums<V>]) const {
+    const Num<V> minus = splat<V>(-1.f);
+#pragma unroll
+    for (int i = 0; i < kNums<V>; ++i) {
+      const Num<V> x = a[i], y = b[i];
+      a[i] = fma(mul(y, s[i]), minus, mul(x, c[i]));
+      b[i] = fma(y, c[i], mul(x, s[i]));
     }
   }
   // By the opposite angle (of a gradient).
