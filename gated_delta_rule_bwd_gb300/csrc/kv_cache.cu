@@ -66,6 +66,7 @@ __device__ __forceinline__ int page_of(const Pages& p, int row, long long slot) 
 // ---------------------------------------------------------------- append
 
 constexpr int kTokens = 64;  // most tokens of a CTA
+constexpr int kPerSm = 3;    // CTAs that run at once on an SM
 
 struct AppendArgs {
   Pages c;
@@ -108,7 +109,7 @@ __device__ __forceinline__ Place place_of(const AppendArgs& a, uint32_t tok) {
 }
 
 template <typename T, int V, int NP, int LR, bool IL, bool I4>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, kPerSm) kv_append_kernel(AppendArgs a) {
   using N = Num<V>;
   constexpr int GW = 32 / LR, M = kNums<V>, RB = V == 1 ? 128 : LR * 2 * V;  // RB: a row's place in shared memory
   __shared__ Place place[kTokens];
@@ -222,11 +223,41 @@ struct GatherArgs {
   void *k, *v;
 };
 
-// V values of type S from x as type O to y; a row's step for 4-bit codes.
 template <typename O, int N>
 struct alignas(16) Vec {
   O x[N];
 };
+
+// What eight codes stand for.  Put into the mantissas of bf16 128s, two at a time,
+// they are 128 + (code + 8); less 136 and times the step each is rounded once at most.
+__device__ __forceinline__ void codes_of(uint32_t w, __nv_bfloat162 (&c)[4]) {  // values (n, n + 4)
+  const uint32_t off = 0xc308c308u;  // -136
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    const uint32_t x = (w >> (4 * n) & 0x000f000fu) | 0x43004300u;
+    c[n] = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&off));
+  }
+}
+__device__ __forceinline__ void values8(uint32_t w, __nv_bfloat16 step, __nv_bfloat16 (&y)[8]) {
+  __nv_bfloat162 c[4];
+  codes_of(w, c);
+  uint32_t v[4];
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    const __nv_bfloat162 p = __hmul2_rn(c[n], __halves2bfloat162(step, step));
+    v[n] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  uint32_t* o = reinterpret_cast<uint32_t*>(y);
+  o[0] = __byte_perm(v[0], v[1], 0x5410), o[1] = __byte_perm(v[2], v[3], 0x5410);
+  o[2] = __byte_perm(v[0], v[1], 0x7632), o[3] = __byte_perm(v[2], v[3], 0x7632);
+}
+__device__ __forceinline__ void values8(uint32_t w, __nv_bfloat16 step, float (&y)[8]) {
+  __nv_bfloat162 c[4];
+  codes_of(w, c);
+  const float s = __bfloat162float(step);
+#pragma unroll
+  for (int n = 0; n < 4; ++n) y[n] = __low2float(c[n]) * s, y[n + 4] = __high2float(c[n]) * s;
+}
 
 template <typename O, bool I4, int V>
 __global__ void __launch_bounds__(kThreads) kv_gather_kernel(GatherArgs a) {
@@ -265,7 +296,7 @@ __global__ void __launch_bounds__(kThreads) kv_gather_kernel(GatherArgs a) {
   O* out = static_cast<O*>(isv ? a.v : a.k) + (long long)t0 * a.Hkv * a.D;
   const unsigned char* src = static_cast<const unsigned char*>(isv ? a.c.v : a.c.k);
   const __nv_bfloat16* scale = static_cast<const __nv_bfloat16*>(isv ? a.c.v_scale : a.c.k_scale);
-  constexpr int U = 4;
+  constexpr int U = 2;  // (4 and 8 on their way: 45 and 62 us for 42)
   uint32_t t = threadIdx.x / per, rem = threadIdx.x % per;
   for (uint32_t i0 = threadIdx.x; i0 < all; i0 += U * kThreads) {
     Vec<O, V> y[U];
@@ -282,9 +313,7 @@ __global__ void __launch_bounds__(kThreads) kv_gather_kernel(GatherArgs a) {
           for (int e = 0; e < V; ++e) y[u].x[e] = from_f32<O>(0.f);
         } else if constexpr (I4) {
           const uint32_t w = *reinterpret_cast<const uint32_t*>(src + at + h * st[2] + d / 2);
-          const float s = __bfloat162float(scale[step_from[t] + h * ss[2] + d / kStepGroup]);
-#pragma unroll
-          for (int e = 0; e < V; ++e) y[u].x[e] = from_f32<O>((float)((int)(w >> (4 * e) & 15) - 8) * s);
+          values8(w, scale[step_from[t] + h * ss[2] + d / kStepGroup], y[u].x);
         } else {
           const O* p = reinterpret_cast<const O*>(src) + at + h * st[2] + d;
           if constexpr (V > 1) y[u] = *reinterpret_cast<const Vec<O, V>*>(p);
@@ -311,8 +340,11 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 template <typename T, int V, int NP, int LR>
 cudaError_t append(AppendArgs a, bool interleaved, bool i4, cudaStream_t s) {
   constexpr int GW = 32 / LR;
-  // Two CTAs per SM's worth of runs or more; a short run's tokens are shared by warps.
-  a.per = (int)std::max(1L, std::min((long)kTokens, (long)a.tokens / (2 * sm_count())));
+  // All CTAs at once, where their runs are long enough (10541 tokens of 4 heads: 13 us;
+  // two, three and four times as many CTAs 16, 15 and 17); a short run's tokens are
+  // shared by warps.
+  const long fit = kPerSm * sm_count();
+  a.per = (int)std::min((long)kTokens, (a.tokens + fit - 1) / fit);
   a.parts = std::max(1, std::min((a.rows + GW - 1) / GW, kWarps / a.per));
   const unsigned ctas = (a.tokens + a.per - 1) / a.per;
   prof_before(s);
@@ -349,10 +381,11 @@ cudaError_t append(const KvAppendProblem& p, const PagedCache& c, cudaStream_t s
 
 template <typename O, bool I4, int V>
 cudaError_t gather(GatherArgs a, cudaStream_t s) {
-  // about four vectors per thread; more where there is work for four CTAs per SM (two
-  // of them for k, two for v) all the same
+  // About four vectors per thread; more where there is work for 32 CTAs per SM (16 for
+  // k, 16 for v) all the same: short runs end together.  60898 tokens of 4 heads of
+  // 128, bf16: 42 us, with runs eight times as long 51.
   const int nv = a.D / V, few = 4 * kThreads / (a.Hkv * nv);
-  a.tokens = std::max(1, std::min(kRun, std::max(few, a.total / (2 * sm_count()))));
+  a.tokens = std::max(1, std::min(kRun, std::max(few, a.total / (16 * sm_count()))));
   a.magic = nv == 1 ? 0 : (uint32_t)(((1ull << 32) + nv - 1) / nv);
   prof_before(s);
   kv_gather_kernel<O, I4, V><<<dim3((a.total + a.tokens - 1) / a.tokens, 2), kThreads, 0, s>>>(a);
