@@ -69,8 +69,8 @@ __device__ void empty_rows(const Args& a) {
 // ---------------------------------------------------------------- CUDA cores
 //
 // Any format and D: 4 warps, tiles of 32 keys in shared memory as fp32, 8 query
-// rows per CTA (two per warp).  A lane owns one key of the scores and DP / 32
-// columns of the accumulators.
+// rows per CTA (two per warp, which share what is read of the tile).  A lane owns one
+// key of the scores and DP / 32 columns of the accumulators.
 constexpr int kRows = 8, kKeys = 32;
 
 // Four values of a row from its value c on, or those of them that it has.
@@ -105,9 +105,9 @@ __device__ __forceinline__ float4 four<I4>(const void* base, long long at, int c
 // T: the queries' and output's type; C: the cache's (T or I4).
 template <typename T, typename C, int DP>
 __global__ void __launch_bounds__(kThreads) attn_paged_simt_kernel(Args a) {
-  constexpr int LD = DP + 4, NC = DP / 32;
+  constexpr int LD = DP + 4, NC = DP / 64;
   __shared__ __align__(16) float K[kKeys * LD], V[kKeys * LD], Q[kRows * DP];
-  __shared__ int page[kKeys];
+  __shared__ long long at[2][4][kKeys];  // offsets of a tile's rows in k, v and their steps (-1: none); the next tile's
   const int row0 = blockIdx.y * kRows, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_launch();
   empty_rows<T>(a);
@@ -121,63 +121,118 @@ __global__ void __launch_bounds__(kThreads) attn_paged_simt_kernel(Args a) {
       const int r = row0 + i / DP, c = i % DP;
       Q[i] = r < a.R && c < a.D ? to_f32(static_cast<const T*>(a.q)[row_at(a, b, hk, r) + c]) : 0.f;
     }
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, acc[2][NC] = {};
-    for (int t0 = wk.k0; t0 < wk.k1; t0 += kKeys) {
-      __syncthreads();
-      if (threadIdx.x < kKeys) page[threadIdx.x] = t0 + threadIdx.x < wk.k1 ? a.page_of(b, t0 + threadIdx.x) : -1;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    F2 acc[2][NC];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int c = 0; c < NC; ++c) acc[i][c] = f2(0.f, 0.f);
+    // warp w looks up k's, v's, k_scale's, v_scale's rows of the tile at t
+    auto lookup = [&](int t, int buf) {
+      const int j = t + lane, p = j < wk.k1 ? a.page_of(b, j) : -1, place = j & ((1 << a.shift) - 1);
+      const long long* st = w == 0 ? a.ks : w == 1 ? a.vs : w == 2 ? a.kss : a.vss;
+      at[buf][w][lane] = p < 0 ? -1 : p * st[0] + place * st[1] + hk * st[2];
+    };
+    lookup(wk.k0, 0);
+    int buf = 0;
+    for (int t0 = wk.k0; t0 < wk.k1; t0 += kKeys, buf ^= 1) {
       __syncthreads();
       {
-        const int c = threadIdx.x % (DP / 4) * 4;
-#pragma unroll 4
-        for (int r = threadIdx.x / (DP / 4); r < kKeys; r += kThreads / (DP / 4)) {
-          float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-          const int p = page[r], at = (t0 + r) & ((1 << a.shift) - 1);
-          if (p >= 0 && c < a.D) {
-            const __nv_bfloat16 *xs = nullptr, *ys = nullptr;
-            if constexpr (sizeof(C) == 1) {
-              xs = a.k_scale + p * a.kss[0] + at * a.kss[1] + hk * a.kss[2];
-              ys = a.v_scale + p * a.vss[0] + at * a.vss[1] + hk * a.vss[2];
-            }
-            x = four<C>(a.k, p * a.ks[0] + at * a.ks[1] + hk * a.ks[2], c, a.D, a.vec, xs);
-            y = four<C>(a.v, p * a.vs[0] + at * a.vs[1] + hk * a.vs[2], c, a.D, a.vec, ys);
+        // All loads on their way together: rows without a page read the first and are zeroed.
+        const int c = threadIdx.x % (DP / 4) * 4, c0 = c < a.D ? c : 0, r0 = threadIdx.x / (DP / 4);
+        constexpr int N = DP / 16, step = 4 * kThreads / DP;
+        float4 x[N], y[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int r = r0 + i * step;
+          const long long ka = max(at[buf][0][r], 0ll), va = max(at[buf][1][r], 0ll);
+          x[i] = y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (a.pages > 0) {
+            x[i] = four<C>(a.k, ka, c0, a.D, a.vec, a.k_scale + (sizeof(C) == 1 ? max(at[buf][2][r], 0ll) : 0));
+            y[i] = four<C>(a.v, va, c0, a.D, a.vec, a.v_scale + (sizeof(C) == 1 ? max(at[buf][3][r], 0ll) : 0));
           }
-          *reinterpret_cast<float4*>(K + r * LD + c) = x;
-          *reinterpret_cast<float4*>(V + r * LD + c) = y;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int r = r0 + i * step;
+          const bool in = at[buf][0][r] >= 0 && c < a.D;
+          const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+          *reinterpret_cast<float4*>(K + r * LD + c) = in ? x[i] : zero;
+          *reinterpret_cast<float4*>(V + r * LD + c) = in ? y[i] : zero;
         }
       }
+      if (t0 + kKeys < wk.k1) lookup(t0 + kKeys, buf ^ 1);
       __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = row0 + w + 4 * i;
-        if (r >= a.R) continue;
-        const float* q = Q + (w + 4 * i) * DP;
-        float s = 0.f;
+      if (row0 + w >= a.R) continue;
+      // a lane's key against the warp's two rows
+      F2 d2[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+      const float* q = Q + w * DP;
+      const bool two = row0 + w + 4 < a.R;
+      auto dots = [&](auto rows) {
 #pragma unroll 8
         for (int d = 0; d < DP; d += 4) {
           const float4 x = *reinterpret_cast<const float4*>(K + lane * LD + d);
-          const float4 y = *reinterpret_cast<const float4*>(q + d);
-          s = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, s))));
+#pragma unroll
+          for (int i = 0; i < decltype(rows)::value; ++i) {
+            const float4 y = *reinterpret_cast<const float4*>(q + 4 * i * DP + d);
+            d2[i] = fma2(f2(x.x, x.y), f2(y.x, y.y), fma2(f2(x.z, x.w), f2(y.z, y.w), d2[i]));
+          }
         }
-        const int last = min(wk.k1 - t0, old + r / a.G - t0 + 1);  // keys of the tile that the row sees
-        s = lane < last ? s * a.c : -INFINITY;
+      };
+      two ? dots(std::integral_constant<int, 2>{}) : dots(std::integral_constant<int, 1>{});
+      float e[2];
+      int seen = 0;  // keys of the tile that any of the two sees
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = row0 + w + 4 * i;
+        const int last = r < a.R ? min(wk.k1 - t0, old + r / a.G - t0 + 1) : 0;  // keys that the row sees
+        seen = max(seen, min(last, kKeys));
+        const float2 dd = unpack(d2[i]);
+        const float s = lane < last ? (dd.x + dd.y) * a.c : -INFINITY;
         float mx = s;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         mx = fmaxf(mx, m[i]);
         const float base = mx == -INFINITY ? 0.f : mx;
-        const float f = exp2f(m[i] - base), e = exp2f(s - base);
-        float sum = e;
+        const float f = exp2f(m[i] - base);
+        e[i] = exp2f(s - base);
+        float sum = e[i];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         l[i] = l[i] * f + sum;
         m[i] = mx;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) acc[i][c] *= f;
-        const int seen = max(0, min(last, kKeys));
-        for (int j = 0; j < seen; ++j) {
-          const float pj = __shfl_sync(0xffffffffu, e, j);
+        for (int c = 0; c < NC; ++c) acc[i][c] = mul2(acc[i][c], f2(f, f));
+      }
+      auto add = [&](int j, bool both) {  // key j's values, the lane's columns 2 lane, 2 lane + 1, ..
+        const float p0 = __shfl_sync(0xffffffffu, e[0], j), p1 = __shfl_sync(0xffffffffu, e[1], j);
 #pragma unroll
-          for (int c = 0; c < NC; ++c) acc[i][c] = fmaf(pj, V[j * LD + lane + 32 * c], acc[i][c]);
+        for (int c = 0; c < NC; ++c) {
+          const float2 x = *reinterpret_cast<const float2*>(V + j * LD + 2 * lane + 64 * c);
+          acc[0][c] = fma2(f2(p0, p0), f2(x.x, x.y), acc[0][c]);
+          if (both) acc[1][c] = fma2(f2(p1, p1), f2(x.x, x.y), acc[1][c]);
+        }
+      };
+      // A key that a row does not see is left out, not taken times 0: its values may
+      // be no numbers.
+      const int last0 = min(kKeys, min(wk.k1 - t0, old + (row0 + w) / a.G - t0 + 1));
+      if (last0 == kKeys && seen == kKeys) {
+        if (two) {
+#pragma unroll
+          for (int j = 0; j < kKeys; ++j) add(j, true);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kKeys; ++j) add(j, false);
+        }
+      } else {
+        for (int j = 0; j < seen; ++j) {
+          const float p0 = __shfl_sync(0xffffffffu, e[0], j), p1 = __shfl_sync(0xffffffffu, e[1], j);
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const float2 x = *reinterpret_cast<const float2*>(V + j * LD + 2 * lane + 64 * c);
+            if (j < last0) acc[0][c] = fma2(f2(p0, p0), f2(x.x, x.y), acc[0][c]);
+            if (two) acc[1][c] = fma2(f2(p1, p1), f2(x.x, x.y), acc[1][c]);
+          }
         }
       }
     }
@@ -190,13 +245,21 @@ __global__ void __launch_bounds__(kThreads) attn_paged_simt_kernel(Args a) {
         T* o = static_cast<T*>(a.o) + row_at(a, b, hk, r);
         const float f = l[i] == 0.f ? 0.f : 1.f / l[i];
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-          if (lane + 32 * c < a.D) o[lane + 32 * c] = from_f32<T>(acc[i][c] * f);
+        for (int c = 0; c < NC; ++c) {
+          const int d = 2 * lane + 64 * c;
+          const float2 x = unpack(acc[i][c]);
+          if (d < a.D) o[d] = from_f32<T>(x.x * f);
+          if (d + 1 < a.D) o[d + 1] = from_f32<T>(x.y * f);
+        }
       } else {
         const long at = slot + w + 4 * i;
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-          if (lane + 32 * c < a.D) a.acc[at * a.D + lane + 32 * c] = acc[i][c];
+        for (int c = 0; c < NC; ++c) {
+          const int d = 2 * lane + 64 * c;
+          const float2 x = unpack(acc[i][c]);
+          if (d < a.D) a.acc[at * a.D + d] = x.x;
+          if (d + 1 < a.D) a.acc[at * a.D + d + 1] = x.y;
+        }
         if (lane == 0) a.ml[2 * at] = m[i], a.ml[2 * at + 1] = l[i];
       }
     }
