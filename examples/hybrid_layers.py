@@ -4,7 +4,8 @@ each behind a layer norm, on the library's calls.
 Trains on packed sequences of different lengths (each repeats its first half,
 which the attention layer learns to look up), then continues prompts token by
 token: the mixer with ``gdn_decode`` on its state, the attention with
-``attn_decode`` on its cache.
+``attn_decode`` on its cache, or with ``kv_append`` and ``attn_paged`` on pages of
+16 or of 4 bits.
 
     python examples/hybrid_layers.py [steps]
 """
@@ -99,6 +100,18 @@ class Hybrid:
         return self.logits(x + o.flatten(2) @ self.attn_out.to(BF16)), (state, *caches, lens)
 
     @torch.no_grad()
+    def to_pages(self, memory, page=16, bits=None):
+        """The memory of ``prompt`` with the attention's part in pages, in no order."""
+        state, k_cache, v_cache, lens = memory
+        B, slots = k_cache.shape[:2]
+        each = -(-slots // page)
+        cache = gdn.new_paged_cache(B * each, page, KEY_HEADS, D, bits=bits, device=lens.device)
+        table = torch.randperm(B * each, device=lens.device).int().view(B, each)
+        seen = int(lens.max())
+        gdn.kv_append(k_cache[:, :seen], v_cache[:, :seen], cache, table, torch.zeros_like(lens))
+        return state.clone(), cache, table, lens.clone()
+
+    @torch.no_grad()
     def step(self, tokens, memory):
         """Logits of one more token per row [B, 1]; ``memory`` is extended."""
         state, k_cache, v_cache, lens = memory
@@ -106,7 +119,12 @@ class Hybrid:
         o, _ = gdn.gdn_decode(*self.mixer_inputs(x), state)
         x = x + o.flatten(2) @ self.mix_out.to(BF16)
         q, k, v = (t.contiguous() for t in self.attention_inputs(x))
-        o = gdn.attn_decode(q, k, v, k_cache, v_cache, lens)
+        if isinstance(k_cache, gdn.PagedCache):
+            cache, table = k_cache, v_cache
+            gdn.kv_append(k, v, cache, table, lens)
+            o = gdn.attn_paged(q, cache, table, lens)
+        else:
+            o = gdn.attn_decode(q, k, v, k_cache, v_cache, lens)
         lens += 1
         return self.logits(x + o.flatten(2) @ self.attn_out.to(BF16))
 
@@ -153,6 +171,11 @@ def generate(model, tokens, new):
     return torch.cat(chosen, 1), torch.cat(seen, 1)
 
 
+def follow(model, tokens, memory):
+    """The logits [B, n, VOCAB] after each of the tokens [B, n]."""
+    return torch.cat([model.step(t[:, None], memory) for t in tokens.unbind(1)], 1)
+
+
 def main(steps=1000):
     model = Hybrid()
     losses = train(model, steps)
@@ -166,6 +189,12 @@ def main(steps=1000):
               "repeated": (tokens == half[:, 8:32]).float().mean().item(),
               "difference": (step_logits - whole).abs().max().item(),
               "largest": whole.abs().max().item()}
+    # the same tokens again, on the contiguous cache and on pages
+    _, memory = model.prompt(prompts, prompts.shape[1] + 24)
+    pages = {n: model.to_pages(memory, bits=b) for n, b in (("paged", None), ("paged_4_bits", 4))}
+    plain = follow(model, tokens, memory)
+    for n, m in pages.items():
+        result[n] = (follow(model, tokens, m) - plain).abs().max().item()
     assert gdn.device_status() == 0
     return result
 
@@ -174,4 +203,5 @@ if __name__ == "__main__":
     r = main(int(sys.argv[1]) if len(sys.argv) > 1 else 1000)
     print(f"loss {r['first']:.3f} -> {r['last']:.3f}; {100 * r['repeated']:.0f} % of the generated tokens "
           f"repeat the prompt; token by token and whole logits differ by at most {r['difference']:.4f} "
-          f"(largest {r['largest']:.2f})")
+          f"(largest {r['largest']:.2f}); on pages they are {r['paged']:.4f} off, on pages of 4 bits "
+          f"{r['paged_4_bits']:.4f}")
