@@ -930,9 +930,8 @@ cudaError_t run(const AttnPagedProblem& p, const PagedCache& c, cudaStream_t s) 
   if (e != cudaSuccess || pl.ctas == 1) return e;
   prof_before(s);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(pl.ctas, std::min(a.R, pl.rows), pl.blocks);
-  // few rows are in many pieces: as many threads as help with one row of all CTAs' pieces
-  const bool wide = pl.ctas >= 32 * p.B * c.Hkv;
+  const bool wide = pl.ctas >= 16 * p.B * c.Hkv;  // few rows in many pieces
+  cfg.gridDim = dim3(wide ? p.B * c.Hkv : pl.ctas, std::min(a.R, pl.rows), pl.blocks);
   cfg.blockDim = dim3(wide ? 8 * kThreads : kThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];

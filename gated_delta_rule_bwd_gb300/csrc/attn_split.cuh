@@ -120,17 +120,31 @@ __device__ __forceinline__ long long row_at(const A& a, int b, int hk, int r) {
   return (((long long)b * a.T + r / a.G) * a.H + hk * a.G + r % a.G) * a.D;
 }
 
-// One CTA of P times 128 threads per (row of a block, CTA that starts a row it does
-// not end): slots 2 c + 1, 2 (c + 1), 2 (c + 2), ... of the row.  The P groups of
-// threads take every P-th slot, and their sums are added in order.
+// One CTA per (row of a block, CTA that starts a row it does not end): slots 2 c + 1,
+// 2 (c + 1), 2 (c + 2), ... of the row.  P > 1, for few rows in many pieces: one CTA of
+// P times 128 threads per (row of a block, b, key head), which finds the CTA that
+// starts it; the P groups of threads take every P-th slot, and their sums are added
+// in order.
 template <typename T, int P, class A>
 __global__ void __launch_bounds__(P * kThreads) attn_combine_kernel(A a, int ctas, int rows) {
   __shared__ float f[kMaxCtas];
   __shared__ float red[8 * P];
-  __shared__ float sums[P > 1 ? P * kThreads : 1];
+  __shared__ __align__(16) float sums[P > 1 ? 4 * P * kThreads : 1];
   tc::grid_dep_wait();
-  const int c0 = blockIdx.x, r = blockIdx.z * rows + blockIdx.y, th = threadIdx.x, d = th % kThreads, part = th / kThreads;
-  const int4 st = a.starts[(long)blockIdx.z * ctas + c0];
+  const int r = blockIdx.z * rows + blockIdx.y, th = threadIdx.x, d = th % kThreads, part = th / kThreads;
+  const int4* starts = a.starts + (long)blockIdx.z * ctas;
+  int c0 = blockIdx.x;
+  if constexpr (P > 1) {
+    __shared__ int found;
+    if (th == 0) found = -1;
+    __syncthreads();
+    for (int i = th; i < ctas; i += P * kThreads)
+      if (starts[i].x >= 0 && starts[i].x * a.Hkv + starts[i].y == (int)blockIdx.x) found = i;  // one at most
+    __syncthreads();
+    c0 = found;
+    if (c0 < 0) return;
+  }
+  const int4 st = starts[c0];
   if (st.x < 0 || r >= a.R) return;
   const int n = st.z - c0 + 1;
   auto at = [&](int i) {
@@ -159,16 +173,34 @@ __global__ void __launch_bounds__(P * kThreads) attn_combine_kernel(A a, int cta
 #pragma unroll
   for (int i = 1; i < 4 * P; ++i) sum += red[4 * P + i];
   float x = 0.f;
-  if (d < a.D) {
+  if (P > 1 && a.D % 4 == 0) {  // 32 groups of a vector each, and their sums in order
+    constexpr int N = P * kThreads / 32;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int c = th % 32 * 4;
+    if (c < a.D) {
 #pragma unroll 8
-    for (int i = part; i < n; i += P) x = fmaf(f[i], a.acc[at(i) * a.D + d], x);
-  }
-  if constexpr (P > 1) {
-    sums[th] = x;
+      for (int i = th / 32; i < n; i += N) {
+        const float4 y = *reinterpret_cast<const float4*>(a.acc + at(i) * a.D + c);
+        v.x = fmaf(f[i], y.x, v.x), v.y = fmaf(f[i], y.y, v.y), v.z = fmaf(f[i], y.z, v.z), v.w = fmaf(f[i], y.w, v.w);
+      }
+    }
+    *reinterpret_cast<float4*>(sums + th * 4) = v;
     __syncthreads();
     if (part > 0) return;
 #pragma unroll
-    for (int i = 1; i < P; ++i) x += sums[i * kThreads + d];
+    for (int i = 0; i < N; ++i) x += sums[i * kThreads + d];
+  } else {
+    if (d < a.D) {
+#pragma unroll 8
+      for (int i = part; i < n; i += P) x = fmaf(f[i], a.acc[at(i) * a.D + d], x);
+    }
+    if constexpr (P > 1) {
+      sums[th] = x;
+      __syncthreads();
+      if (part > 0) return;
+#pragma unroll
+      for (int i = 1; i < P; ++i) x += sums[i * kThreads + d];
+    }
   }
   if (d >= a.D) return;
   static_cast<T*>(a.o)[row_at(a, st.x, st.y, r) + d] = from_f32<T>(sum == 0.f ? 0.f : x / sum);
