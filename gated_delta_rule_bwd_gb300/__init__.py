@@ -984,8 +984,8 @@ def qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, cos=None, sin=None, pos
     """RMS norm of every head of ``q [B, T, H, D]`` and ``k [B, T, Hkv, D]`` (views of
     one projection are taken as they are) with weights ``[D]`` fp32, then rotation of
     its first R values by position: ``cos``, ``sin`` ``[P, R / 2]`` fp32 (see
-    ``rope_table``), ``positions`` int32 ``[B, T]`` (default: token t has position t).
-    Pairs are ``(i, i + R / 2)``, or ``(2 i, 2 i + 1)`` with ``interleaved``.  Weights
+    ``rope_table``), ``positions`` int32 ``[B, T]`` (default: token t has position t; a
+    token with a negative one is not in use and gets zeros).  Pairs are ``(i, i + R / 2)``, or ``(2 i, 2 i + 1)`` with ``interleaved``.  Weights
     or tables may be left out.  Returns ``(qo, ko)``, contiguous."""
     s = _qk_args(q, k, q_weight, k_weight, cos, sin, positions, interleaved)
     dtype, device = q.dtype, q.device
@@ -1161,6 +1161,8 @@ def kv_gather(cache, block_table, cu_seqlens, total, dtype=None):
     if dtype not in _DTYPES or form not in (2, _DTYPES[dtype]):
         raise GdnError(f"a cache of {cache[0].dtype} does not give {dtype}")
     _attn_cu("cu_seqlens", cu_seqlens, device)
+    if total < 0:
+        raise GdnError(f"{total} tokens")
     rows = cu_seqlens.numel() - 1
     most, stride = _block_table(block_table, rows, device)
     k = torch.empty((1, total, Hkv, D), dtype=dtype, device=device)

@@ -8,6 +8,13 @@
 // query heads of a key head and the T tokens are the R = G T rows of one product
 // with the cache.  Work split: the batch's units of 64 keys evenly over the CTAs,
 // and a second kernel that joins what is split (attn_split.cuh).
+//
+// Bound by the cache's bytes: 2 Hkv D (old + T) values per row, 2 bytes each or, in 4
+// bits, 9 / 16 of one.  Measured, 64 rows of 1638 to 8192 tokens, 16 heads on 4, D 128:
+// bf16 pages of 16 tokens 104 us the call, 6.2 TB/s; 4 bits, pages of 64: 56 us, 3.3
+// TB/s, one row of 1022361 tokens, 16 heads on 2: 76 us, 3.9 TB/s.  In 4 bits the
+// instructions come before the bytes: some 375 per warp for 16 keys (4096 values of K
+// and V), 160 of them on the integer pipe, issued 61 % of the time.
 
 #include <cuda_fp16.h>
 

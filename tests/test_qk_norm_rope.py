@@ -164,6 +164,30 @@ def test_positions_outside_the_tables(D, dtype):
 
 @gpu
 @TYPES
+@pytest.mark.parametrize("D", [64, 33])
+def test_tokens_that_are_not_in_use(D, dtype):
+    """Negative positions, as in a padded batch: zeros, no gradient, no error, whatever
+    the rows hold."""
+    q, k, w, dq, dk = inputs(1, 5, 2, 1, D, dtype, seed=15)
+    cos, sin = gdn.rope_table(8, D // 2 * 2)
+    pos = torch.tensor([[0, -1, 7, -(1 << 31), 3]], dtype=torch.int32, device="cuda")
+    use = [0, 2, 4]
+    q[:, [1, 3]], dq[:, [1, 3]], k[:, 1], dk[:, 3] = float("nan"), float("inf"), float("nan"), float("nan")
+    for x in (w, (None, None)):
+        y = gdn.qk_norm_rope_fwd(q, k, *x, cos, sin, pos)
+        g = gdn.qk_norm_rope_bwd(q, k, dq, dk, *x, cos, sin, pos)
+        assert gdn.device_status() == 0
+        s = lambda t: t[:, use].contiguous()  # noqa: E731
+        yw = gdn.qk_norm_rope_fwd(s(q), s(k), *x, cos, sin, s(pos))
+        gw = gdn.qk_norm_rope_bwd(s(q), s(k), s(dq), s(dk), *x, cos, sin, s(pos))
+        for a, b in zip((*y, *g[:2]), (*yw, *gw[:2])):
+            assert torch.equal(a[:, use], b) and not a[:, [1, 3]].any()
+        for a, b in zip(g[2:], gw[2:]):
+            assert a is b is None or torch.allclose(a, b, rtol=1e-5, atol=1e-5)
+
+
+@gpu
+@TYPES
 @pytest.mark.parametrize("D", [64, 31])
 def test_zero_rows_and_other_rows_nan(D, dtype):
     """A row of zeros gives zeros and a finite gradient; a NaN stays in its row."""
