@@ -954,7 +954,39 @@ def _tables(cos, sin, D, device):
     return 2 * half, P
 
 
+def _table_ok(cos, sin, D, device):
+    """Whether the angles are tables that a call takes (most calls' case, in one look)."""
+    shape = cos.shape
+    return (len(shape) == 2 and 0 < 2 * shape[1] <= D and cos.dtype is torch.float32
+            and sin.dtype is torch.float32 and sin.shape == shape and cos.device == device
+            and sin.device == device and cos.is_contiguous() and sin.is_contiguous())
+
+
 def _qk_args(q, k, q_weight, k_weight, cos, sin, positions, interleaved):
+    """The ABI shape of a call, packed.  First the looks that every good call passes,
+    then, if one did not, the slow ones that say why."""
+    try:
+        dtype, device, qs, ks = q.dtype, q.device, q.stride(), k.stride()
+        B, T, H, D = q.shape
+        Bk, Tk, Hkv, Dk = k.shape
+        half = cos.shape[1]
+        if (k.dtype is dtype and k.device == device and q.is_cuda and Bk == B and Tk == T and Dk == D
+                and qs[3] == 1 and ks[3] == 1 and _table_ok(cos, sin, D, device)
+                and (positions is None or (positions.dtype is torch.int32 and positions.shape == (B, T)
+                                           and positions.device == device and positions.is_contiguous()))
+                and (q_weight is k_weight is None
+                     or (q_weight.dtype is torch.float32 and k_weight.dtype is torch.float32
+                         and q_weight.shape == (D,) and k_weight.shape == (D,)
+                         and q_weight.device == device and k_weight.device == device
+                         and q_weight.is_contiguous() and k_weight.is_contiguous()))):
+            return _QK_ROPE.pack(B, T, H, Hkv, D, 2 * half, cos.shape[0], bool(interleaved),
+                                 _DTYPES[dtype], qs[0], qs[1], qs[2], ks[0], ks[1], ks[2])
+    except (AttributeError, KeyError, TypeError, ValueError, IndexError):
+        pass
+    return _qk_args_slow(q, k, q_weight, k_weight, cos, sin, positions, interleaved)
+
+
+def _qk_args_slow(q, k, q_weight, k_weight, cos, sin, positions, interleaved):
     if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPES:
         raise GdnError("q must be a fp32 or bf16 tensor")
     dtype, device = q.dtype, q.device
@@ -1054,6 +1086,31 @@ def new_paged_cache(pages, page, Hkv, D, dtype=torch.bfloat16, bits=None, device
 
 def _cache_args(cache, device):
     """The ABI's view of a cache (packed), and its heads, values per head and format."""
+    try:
+        k, v = cache[0], cache[1]
+        shape, dtype, a, b = k.shape, k.dtype, k.stride(), v.stride()
+        pages, page, Hkv, D = shape
+        if (v.shape == shape and v.dtype is dtype and k.device == device and v.device == device
+                and a[3] == 1 and b[3] == 1 and D > 0):
+            if dtype is torch.uint8:
+                ks, vs = cache[2], cache[3]
+                c, d, steps = ks.stride(), vs.stride(), (pages, page, Hkv, D // 16)
+                if (len(cache) == 4 and D % 16 == 0 and ks.dtype is torch.bfloat16
+                        and vs.dtype is torch.bfloat16 and ks.shape == steps and vs.shape == steps
+                        and ks.device == device and vs.device == device and c[3] == 1 and d[3] == 1):
+                    return _CACHE.pack(pages, page, Hkv, 2 * D, 2, k.data_ptr(), v.data_ptr(),
+                                       ks.data_ptr(), vs.data_ptr(), a[0], a[1], a[2], b[0], b[1], b[2],
+                                       c[0], c[1], c[2], d[0], d[1], d[2]), Hkv, 2 * D, 2
+            elif len(cache) == 2:
+                form = _DTYPES[dtype]
+                return _CACHE.pack(pages, page, Hkv, D, form, k.data_ptr(), v.data_ptr(), 0, 0, a[0],
+                                   a[1], a[2], b[0], b[1], b[2], 0, 0, 0, 0, 0, 0), Hkv, D, form
+    except (AttributeError, KeyError, TypeError, ValueError, IndexError):
+        pass
+    return _cache_args_slow(cache, device)
+
+
+def _cache_args_slow(cache, device):
     n = 4 if len(cache) == 4 and cache[2] is not None else 2
     if n == 2 and any(x is not None for x in cache[2:]) or len(cache) < 2 or len(cache) > 4:
         raise GdnError("the cache must be (k, v) or (k, v, k_scale, v_scale)")
@@ -1099,17 +1156,10 @@ def _block_table(table, rows, device):
     return table.shape[1], table.stride(0)
 
 
-def kv_append(k, v, cache, block_table, lens, q=None, cos=None, sin=None, interleaved=False,
-              cu_seqlens=None):
-    """Stores new keys and values ``[B, T, Hkv, D]`` in a paged cache: token t of row b
-    in slot ``lens[b] + t`` (``lens`` int32, on the device, left to the caller), which
-    is place ``slot % page`` of page ``block_table[b, slot // page]`` (int32).  With
-    ``cos``, ``sin`` (see ``qk_norm_rope_fwd``) k is rotated by its slot on the way,
-    and so is ``q [B, T, H, D]``, if given; returns the rotated q, or None.
+_NO_STRIDES = (0, 0, 0)
 
-    Packed new tokens: ``k``, ``v``, ``q`` ``[1, T, ...]`` and ``cu_seqlens`` int32
-    ``[rows + 1]``; tokens behind ``cu_seqlens[-1]`` belong to no row.  A row whose
-    ``lens`` is negative is not in use: its tokens are not stored, and their q is 0."""
+
+def _append_args(k, v, cache, block_table, lens, q, cos, sin, cu_seqlens):
     if not isinstance(k, torch.Tensor) or k.dtype not in _DTYPES:
         raise GdnError("k must be a fp32 or bf16 tensor")
     dtype, device = k.dtype, k.device
@@ -1118,7 +1168,7 @@ def kv_append(k, v, cache, block_table, lens, q=None, cos=None, sin=None, interl
     B, T, Hkv, D = shape
     if v.shape != shape:
         raise GdnError(f"k and v differ: {tuple(shape)}, {tuple(v.shape)}")
-    H, qst, qo = 0, (0, 0, 0), None
+    H, qst = 0, _NO_STRIDES
     if q is not None:
         qst = _heads("q", q, dtype, device)
         Bq, Tq, H, Dq = q.shape
@@ -1137,10 +1187,52 @@ def kv_append(k, v, cache, block_table, lens, q=None, cos=None, sin=None, interl
         rows = cu_seqlens.numel() - 1
     _i32("lens", lens, device, (rows,))
     most, stride = _block_table(block_table, rows, device)
-    s = _APPEND.pack(B, T, H, R, P, bool(interleaved), _DTYPES[dtype], rows, most, stride, *qst[:3],
-                     *kst[:3], *vst[:3])
-    if q is not None:
-        qo = _empty(q, dtype, device)
+    return c, B, T, H, R, P, _DTYPES[dtype], rows, most, stride, qst, kst, vst
+
+
+def kv_append(k, v, cache, block_table, lens, q=None, cos=None, sin=None, interleaved=False,
+              cu_seqlens=None):
+    """Stores new keys and values ``[B, T, Hkv, D]`` in a paged cache: token t of row b
+    in slot ``lens[b] + t`` (``lens`` int32, on the device, left to the caller), which
+    is place ``slot % page`` of page ``block_table[b, slot // page]`` (int32).  With
+    ``cos``, ``sin`` (see ``qk_norm_rope_fwd``) k is rotated by its slot on the way,
+    and so is ``q [B, T, H, D]``, if given; returns the rotated q, or None.
+
+    Packed new tokens: ``k``, ``v``, ``q`` ``[1, T, ...]`` and ``cu_seqlens`` int32
+    ``[rows + 1]``; tokens behind ``cu_seqlens[-1]`` belong to no row.  A row whose
+    ``lens`` is negative is not in use: its tokens are not stored, and their q is 0."""
+    rows = None
+    try:  # the looks that every good call passes
+        dtype, device, kst, vst = k.dtype, k.device, k.stride(), v.stride()
+        shape = k.shape
+        B, T, Hkv, D = shape
+        H, qst, R, P = 0, _NO_STRIDES, 0, 0
+        good = (v.shape == shape and v.dtype is dtype and v.device == device and k.is_cuda
+                and kst[3] == 1 and vst[3] == 1)
+        if q is not None:
+            Bq, Tq, H, Dq = q.shape
+            qst = q.stride()
+            good = (good and q.dtype is dtype and q.device == device and Bq == B and Tq == T and Dq == D
+                    and qst[3] == 1)
+        if cos is not None or sin is not None:
+            good = good and _table_ok(cos, sin, D, device)
+            P, R = cos.shape[0], 2 * cos.shape[1]
+        if good and cu_seqlens is None:
+            c, heads, values, form = _cache_args(cache, device)
+            most, stride = _block_table(block_table, B, device)
+            if (heads == Hkv and values == D and (form == 2 or form == _DTYPES[dtype])
+                    and lens.dtype is torch.int32 and lens.shape == (B,) and lens.device == device
+                    and lens.is_contiguous()):
+                rows, code = B, _DTYPES[dtype]
+    except (AttributeError, KeyError, TypeError, ValueError, IndexError):
+        pass
+    if rows is None:  # packed tokens, or a call that one of these says no to
+        c, B, T, H, R, P, code, rows, most, stride, qst, kst, vst = _append_args(
+            k, v, cache, block_table, lens, q, cos, sin, cu_seqlens)
+        dtype, device = k.dtype, k.device
+    s = _APPEND.pack(B, T, H, R, P, bool(interleaved), code, rows, most, stride, qst[0], qst[1], qst[2],
+                     kst[0], kst[1], kst[2], vst[0], vst[1], vst[2])
+    qo = None if q is None else _empty(q, dtype, device)
     _call((_lib or lib()).gdn_kv_append(
         s, c, k.data_ptr(), v.data_ptr(), _addr(q), _addr(cos), _addr(sin), block_table.data_ptr(),
         lens.data_ptr(), _addr(cu_seqlens), _addr(qo), _raw_stream(device)))
