@@ -33,6 +33,10 @@ using namespace rope;
 using tc::sm_count;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
+// CTAs per SM.  The forward, by measurement at 16 x 2048 tokens, 8 + 8 heads of 128: with
+// one pass loaded ahead and 80 registers 48 us; two CTAs and one to three passes ahead
+// 55, four CTAs 56.  The backward's 128 registers allow two.
+constexpr int kPerSmFwd = 3, kPerSmBwd = 2;
 
 // The heads of q, or those of k.
 struct Side {
@@ -119,49 +123,40 @@ __device__ __forceinline__ Side side_of(const Args& a, uint32_t& cta, uint32_t& 
 }
 
 template <typename T, int V, int NP, int LR, bool IL, bool NORM>
-__global__ void __launch_bounds__(kThreads, 2) qk_rope_fwd_kernel(Args a) {
+__global__ void __launch_bounds__(kThreads, kPerSmFwd) qk_rope_fwd_kernel(Args a) {
   using L = Lane<V, NP, LR, IL>;
   using N = Num<V>;
-  constexpr int GW = L::GW, U = V == 1 ? 1 : 2, M = kNums<V>;  // U: passes on their way
+  constexpr int GW = L::GW, M = kNums<V>;
   const L lane(a);
   uint32_t cta, ctas;
   const Side s = side_of(a, cta, ctas);
-  N wa[NP][M], wb[NP][M];
+  __shared__ __align__(16) float w[128];
   if constexpr (NORM) {
-#pragma unroll
-    for (int i = 0; i < NP; ++i) widen<IL>(load<float, V>(s.w, lane.slot[i]), wa[i], wb[i]);
+    for (int i = threadIdx.x; i < a.D; i += kThreads) w[i] = s.w[i];
+    __syncthreads();
   }
   const uint32_t stride = ctas * kWarps;
   Cursor f;
   f.start(a, s, cta * kWarps + (threadIdx.x >> 5));
-  Raw<T, V> next[U][NP];
-  Pass pass[U];
-  auto fetch = [&](int u) {
+  Raw<T, V> next[NP];
+  auto fetch = [&] {
     if (f.p.tok < a.tokens) {  // heads past the last: the last again
       const T* x = static_cast<const T*>(s.x) + f.at + min(f.p.h + lane.grp, f.p.h1 - 1) * s.st[2];
 #pragma unroll
-      for (int i = 0; i < NP; ++i) next[u][i] = load(x, lane.slot[i]);
+      for (int i = 0; i < NP; ++i) next[i] = load(x, lane.slot[i]);
     }
-    pass[u] = f.p;
-    f.next<GW>(a, s, stride);
   };
-#pragma unroll
-  for (int u = 0; u < U; ++u) fetch(u);
+  fetch();
   Angles<V> g[NP];
   bool ok = true;
-  while (pass[0].tok < a.tokens) {
-    const Pass c = pass[0];
+  while (f.p.tok < a.tokens) {
+    const Pass c = f.p;
     if (c.fresh) ok = lane.angles(a, c.pos, g);
     N xa[NP][M], xb[NP][M];
 #pragma unroll
-    for (int i = 0; i < NP; ++i) widen<IL>(next[0][i], xa[i], xb[i]);
-#pragma unroll
-    for (int u = 0; u + 1 < U; ++u) {
-#pragma unroll
-      for (int i = 0; i < NP; ++i) next[u][i] = next[u + 1][i];
-      pass[u] = pass[u + 1];
-    }
-    fetch(U - 1);
+    for (int i = 0; i < NP; ++i) widen<IL>(next[i], xa[i], xb[i]);
+    f.next<GW>(a, s, stride);
+    fetch();
     if constexpr (NORM) {
       N ss = splat<V>(0.f);
 #pragma unroll
@@ -170,9 +165,12 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rope_fwd_kernel(Args a) {
         for (int e = 0; e < M; ++e) ss = fma(xa[i][e], xa[i][e], fma(xb[i][e], xb[i][e], ss));
       const N r = splat<V>(rsqrtf(lane.sum(ss) * a.inv_d + a.eps));
 #pragma unroll
-      for (int i = 0; i < NP; ++i)
+      for (int i = 0; i < NP; ++i) {
+        N wa[M], wb[M];
+        widen<IL>(load<float, V>(w, lane.slot[i]), wa, wb);
 #pragma unroll
-        for (int e = 0; e < M; ++e) xa[i][e] = mul(mul(xa[i][e], r), wa[i][e]), xb[i][e] = mul(mul(xb[i][e], r), wb[i][e]);
+        for (int e = 0; e < M; ++e) xa[i][e] = mul(mul(xa[i][e], r), wa[e]), xb[i][e] = mul(mul(xb[i][e], r), wb[e]);
+      }
     }
     const uint32_t h = c.h + lane.grp;
     if (h < c.h1) {
@@ -191,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_rope_fwd_kernel(Args a) {
 }
 
 template <typename T, int V, int NP, int LR, bool IL, bool NORM>
-__global__ void __launch_bounds__(kThreads, 2) qk_rope_bwd_kernel(Args a) {
+__global__ void __launch_bounds__(kThreads, kPerSmBwd) qk_rope_bwd_kernel(Args a) {
   using L = Lane<V, NP, LR, IL>;
   using N = Num<V>;
   constexpr int GW = L::GW, U = V == 4 ? 2 : 1, M = kNums<V>;
@@ -337,8 +335,6 @@ __global__ void __launch_bounds__(1024) qk_rope_sum_kernel(Args a, int ctas) {
 
 // ---------------------------------------------------------------- host
 
-constexpr int kCtasPerSm = 2;
-
 // Whether all rows go in vectors of V pairs' halves.
 bool use_vectors(const QkRopeProblem& p, int V) {
   const size_t e = p.bf16 ? 2 : 4;
@@ -360,7 +356,7 @@ void set_jobs(Side& s, uint32_t tokens, int gw, long warps) {
 template <typename T, int V, int NP, int LR, bool IL, bool NORM>
 cudaError_t launch(Args a, bool bwd, cudaStream_t s) {
   constexpr int GW = 32 / LR;
-  const int most = kCtasPerSm * sm_count(), H = a.side[0].H + a.side[1].H;
+  const int most = (bwd ? kPerSmBwd : kPerSmFwd) * sm_count(), H = a.side[0].H + a.side[1].H;
   int ctas[2];
   for (int i = 0; i < 2; ++i) {
     Side& x = a.side[i];
@@ -430,7 +426,7 @@ cudaError_t run(const QkRopeProblem& p, bool bwd, cudaStream_t s) {
 
 // Sums of every CTA that may run (each side has one at least).
 size_t qk_rope_bwd_workspace(const QkRopeProblem& p) {
-  return (size_t)(kCtasPerSm * sm_count() + 2) * p.D * sizeof(float);
+  return (size_t)(kPerSmBwd * sm_count() + 2) * p.D * sizeof(float);
 }
 
 cudaError_t qk_rope_fwd(const QkRopeProblem& p, cudaStream_t s) { return run(p, false, s); }
