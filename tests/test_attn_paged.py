@@ -244,6 +244,55 @@ def test_sizes_of_values(size, dtype, bits):
 
 
 @gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("order", ["rising", "falling", "mixed", "by group"])
+def test_steps_of_many_sizes(order, D):
+    """4 bits: steps of values from 2^-12 to 2^12 of one another, along the sequence or
+    from one 32 values to the next.  The fp16 weights' absolute error, 2^-30 of the
+    largest step of a value's 32, is far below the bound's 2^-9 of the weighted sum,
+    in which every key has its part."""
+    lens, page = [700, 45, 31, 3000], 16
+    held = [n + 1 for n in lens]
+
+    def change(cache, table, q):
+        g = torch.Generator().manual_seed(3)
+        for b, n in enumerate(held):
+            at_ = tuple(torch.tensor(x, device="cuda").long() for x in places(np.full(n, b), np.arange(n), table, page))
+            e = torch.linspace(-12, 12, n)[:, None, None].expand(n, 2, D // 32).round()
+            if order == "falling":
+                e = -e
+            elif order == "mixed":
+                e = torch.randint(-12, 13, e.shape, generator=g)
+            elif order == "by group":
+                e = torch.linspace(-12, 12, D // 32).round().expand(e.shape)
+            cache[3][at_] = cache[3][at_] * torch.exp2(e.float()).cuda().to(cache[3].dtype)
+        return cache, table, q
+    check(lens, 1, 8, 2, D, page, BF16, 4, seed=21, change=change)
+
+
+@gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_step_that_is_no_number(bad, D):
+    """4 bits: such a step of a value reaches its own 32 values of its key head, and
+    leaves the others as they were."""
+    lens, page = [300, 20], 16
+    held = [n + 1 for n in lens]
+    table, pages = tables(held, page, 22)
+    q = torch.randn(2, 1, 8, D, generator=torch.Generator().manual_seed(22)).to(BF16).cuda()
+    cache = random_cache(pages, page, 2, D, BF16, 4, 23)
+    o = gdn.attn_paged(q, cache, table, i32(lens))
+    p = places(np.array([0]), np.array([150]), table, page)
+    cache[3][int(p[0][0]), int(p[1][0]), 1, 1] = bad
+    x = gdn.attn_paged(q, cache, table, i32(lens))
+    assert gdn.device_status() == 0
+    hit = torch.zeros_like(o, dtype=torch.bool)
+    hit[0, :, 4:, 32:64] = True
+    assert not torch.isfinite(x[hit]).any()
+    assert torch.equal(x[~hit], o[~hit])
+
+
+@gpu
 @FORMATS
 def test_same_bits_streams_and_graphs(dtype, bits):
     lens = [3000, 1, 333, -1]
