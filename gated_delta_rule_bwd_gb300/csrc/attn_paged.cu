@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, I4 ? kPerSm4 : kPerSm16) attn_paged_
         const Steps *kt = ksb, *vt = vsb;
         if constexpr (I4) kt += (uint64_t)p0 * a.ksr[0], vt += (uint64_t)p0 * a.vsr[0];
         if (a.dense) {  // the keys of a head one after another: the warp copies what follows
-          ks += at * St::NC + lane, vs += at * St::NC + lane;
+          ks += (uint64_t)at * St::NC + lane, vs += (uint64_t)at * St::NC + lane;
 #pragma unroll
           for (int r = 0; r < KS; r += RS) {
             cp_async<16>(to(r), ks + r * St::NC, true);
