@@ -11,10 +11,10 @@
 //
 // Bound by the cache's bytes: 2 Hkv D (old + T) values per row, 2 bytes each or, in 4
 // bits, 9 / 16 of one.  Measured, 64 rows of 1638 to 8192 tokens, 16 heads on 4, D 128:
-// bf16 pages of 16 tokens 104 us the call, 6.2 TB/s; 4 bits, pages of 64: 56 us, 3.3
-// TB/s, one row of 1022361 tokens, 16 heads on 2: 76 us, 3.9 TB/s.  In 4 bits the
-// instructions come before the bytes: some 375 per warp for 16 keys (4096 values of K
-// and V), 160 of them on the integer pipe, issued 61 % of the time.
+// bf16 pages of 16 tokens 105 us the call, 6.1 TB/s; 4 bits, pages of 64: 60 us, 3.0
+// TB/s, one row of 1022361 tokens, 16 heads on 2: 82 us, 3.6 TB/s.  In 4 bits no pipe and
+// not the memory is full: a warp is one chain of products, maxima, exponentials and
+// products per 32 keys, and three warps per scheduler do not cover its waits.
 
 #include <cuda_fp16.h>
 
@@ -289,35 +289,34 @@ __global__ void __launch_bounds__(kThreads) attn_paged_simt_kernel(Args a) {
 //   K's and V's fragments, are whole A operands: with q there, half of it zeros for
 //   8 rows, the registers were moved together again for each product.
 //
-// bf16: fragments by ldmatrix (V transposed on the way); P in two bf16 terms, so that
-// its rounding does not show beside the output's (64 rows of up to 8192 keys: 105 us so,
-// 104 with one term; memory bounds both).
+// P goes in in two bf16 terms, so that its rounding does not show beside the output's:
+// what is left is 2^-16 of it, whatever the probabilities and values are.
+// bf16: fragments by ldmatrix (V transposed on the way).  64 rows of up to 8192 keys: 105 us
+// so, 104 with one term; memory bounds both.
 // 4 bits: the order of the D values within a product is free, and a lane takes whole
-// words of 8 codes, held c = code + 8.
+// words of 8 codes, held c = code + 8.  Integers become floats by being put into the
+// mantissa of a constant, the published way for 4-bit weights:
 //   K: a byte below the exponent of an fp16 1024 is X = 1024 + c0 + 16 c1 (two bytes of a
 //   word by one byte permutation), and without its upper four bits L = 1024 + c0 (one
 //   logic operation), so that
 //     q0 c0 + q1 c1 = (q1 / 16) X + (q0 - q1 / 16) L - 1024 (both weights):
 //   half an operation a code.  The weights are fp16 (q scaled by a power of two per row,
-//   so that its largest value is in [1, 2)): the first is exact, the second off by 2^-12 of
-//   itself, which reaches the score as that part of a c0 (q, as bf16, has 2^-9).  The
-//   constants, with the 8 in c, go back once per key, with the steps, which are
+//   so that its largest value is in [1, 2)): the first is exact, the second off by up to
+//   2^-11 of itself, which reaches the score as that part of step c0 (q, as bf16, has 2^-8).
+//   The constants, with the 8 in c, go back once per key, with the steps, which are
 //   applied to the scores:
 //     s = sum_j step_j (sum_d of the group's products) + sum_j step_j base_j,
 //   the second sum (j a key's groups) as one product of the steps with base in three
 //   bf16 terms.  1024 against c of about 3 costs the fp32 sums over a group some 9 of
 //   their 24 bits.
-//   V: w & 0x000f000f and w & 0x00f000f0 (a word of two keys' halves; then w >> 8), put
-//   into the mantissas of two fp16 1024s, are 1024 + c and 1024 + 16 c: one logic
-//   operation for two codes, a shift for eight, and one packed operation that takes
-//   the 1024 and the 8 off (exactly: sums over thousands of keys of one sign would drown
-//   what is left of codes that cancel).  V's steps go to the probabilities, p step in
-//   fp32, rounded once to fp16: one weight per key, row and 32 values.  fp16 has three bits
-//   more than bf16, so that this rounding does not show beside the output's, and little
-//   range, so a warp keeps the accumulators of each 32 values in units of 2^u and takes
-//   their steps by 2^-u: the largest that it has met is in [2^5, 2^7).  A larger one raises
-//   u, which is rare.  A weight below 2^-14 loses bits and is off by up to 2^-25: 2^-30 of
-//   the largest step.
+//   V: w & 0x000f000f (a word of two keys' halves; then w >> 4, ..) in the mantissas of two
+//   bf16 128s is 128 + c; less 136 (exactly: sums over thousands of keys of one sign would
+//   drown what is left of codes that cancel) and times the keys' steps it is the values
+//   as kv_gather gives them, exact for steps of 5 bits.  Every key then has its own
+//   exponent, as in 16-bit pages: a large value takes no bits from others, weighted or
+//   not.  (One fp16 weight per key, row and 32 values, p step in units of the largest step met,
+//   took 56 and 76 us for 60 and 82, but left keys out beside a hardly weighted value some 2^16
+//   above theirs.)
 //
 // Each warp streams its own blocks of KS keys (w, w + 4, ...) through a ring of
 // kStages stages (cp.async) and keeps its own m, l and accumulators, so the warps
@@ -347,6 +346,11 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
 __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {  // d += a b
@@ -391,35 +395,24 @@ __device__ __forceinline__ uint32_t transposed(uint32_t v) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-// The codes of a word of two keys' halves, by twos, as fp16.  The constants come as
-// registers: with both as immediates it takes two logic operations.
+// The codes of a word of two keys' halves, by twos, as bf16, and the values that they
+// stand for.  The constants come as registers: with both as immediates it takes two
+// logic operations.
 struct Magic {
-  uint32_t low, high, one;
+  uint32_t low, one;
   __device__ __forceinline__ Magic() {
     asm volatile("mov.b32 %0, 0x000f000f;" : "=r"(low));
-    asm volatile("mov.b32 %0, 0x00f000f0;" : "=r"(high));
-    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(one));
+    asm volatile("mov.b32 %0, 0x43004300;" : "=r"(one));
   }
-  __device__ __forceinline__ static __half2 half2_of(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
-  __device__ __forceinline__ static uint32_t bits(__half2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
-  // the codes at bits 0-3, and at bits 4-7
-  __device__ __forceinline__ uint32_t first(uint32_t w) const {
+  __device__ __forceinline__ static __nv_bfloat162 twos(uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); }
+  // the codes at bits 0-3 of w's halves, times the steps
+  __device__ __forceinline__ uint32_t values(uint32_t w, uint32_t steps) const {
     uint32_t x;
     asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(x) : "r"(w), "r"(low), "r"(one));
-    return bits(__hadd2(half2_of(x), half2_of(0xe408e408u)));  // - 1032
-  }
-  __device__ __forceinline__ uint32_t second(uint32_t w) const {
-    uint32_t x;
-    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(x) : "r"(w), "r"(high), "r"(one));
-    return bits(__hfma2(half2_of(x), half2_of(0x2c002c00u), half2_of(0xd480d480u)));  // / 16 - 72
+    const __nv_bfloat162 v = __hmul2_rn(__hadd2_rn(twos(x), twos(0xc308c308u)), twos(steps));  // - 136
+    return *reinterpret_cast<const uint32_t*>(&v);
   }
 };
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float pow2(int n) { return n < -126 ? 0.f : __uint_as_float((uint32_t)(n + 127) << 23); }  // n < 128
 __device__ __forceinline__ float lo16(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi16(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
@@ -618,12 +611,6 @@ __global__ void __launch_bounds__(kThreads, I4 ? kPerSm4 : kPerSm16) attn_paged_
       }
     }
     float acc[DP / 16][NR][4], m[NR][2], l[NR][2];
-    // 4 bits: the accumulators of 32 values are in units of 2^u; by pairs, the largest step
-    // (bf16's bits) that this allows, ((u + 134) << 7) - 1, and 2^-u
-    uint32_t most[NG / 2], unit[NG / 2];
-#pragma unroll
-    for (int j = 0; j < NG / 2; ++j) most[j] = 0x03ff03ff, unit[j] = 0x7e807e80;  // u = -126
-    auto exponent = [&](int j) { return (int)(((most[j / 2] >> (16 * (j % 2)) & 0xffff) + 1) >> 7) - 134; };
     int last[NR][2];  // last key that the row sees
 #pragma unroll
     for (int x = 0; x < NR; ++x) {
@@ -701,38 +688,6 @@ __global__ void __launch_bounds__(kThreads, I4 ? kPerSm4 : kPerSm16) attn_paged_
           }
         }
       }
-      if constexpr (I4) {
-        static_assert(KS == 32);
-        const uint32_t at = st + St::vs + lane * St::step;  // a key's steps to a lane
-        uint32_t y[NG / 2];
-        if constexpr (NG == 4) {
-          const uint2 v = lds64(at);
-          y[0] = v.x, y[1] = v.y;
-        } else {
-          y[0] = lds32(at);
-        }
-        bool over = false;
-#pragma unroll
-        for (int j = 0; j < NG / 2; ++j) over |= __vmaxu2(y[j] & 0x7fff7fff, most[j]) != most[j];
-        if (__any_sync(0xffffffffu, over)) {
-#pragma unroll
-          for (int j = 0; j < NG; ++j) {
-            const int half = 16 * (j % 2), u = exponent(j);
-            uint32_t z = y[j / 2] >> half & 0x7fff;
-            if (z >= 0x7f80) z = 0;  // not a number: it changes no other key's unit
-            z = __reduce_max_sync(0xffffffffu, z);
-            const int to = max(u, (int)(z >> 7) - 127 - 5);
-            const float f = pow2(u - to);
-#pragma unroll
-            for (int x = 0; x < NR; ++x)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) acc[2 * j][x][e] *= f, acc[2 * j + 1][x][e] *= f;
-            const uint32_t keep = 0xffff0000u >> half;
-            most[j / 2] = (most[j / 2] & keep) | (uint32_t)(((to + 134) << 7) - 1) << half;
-            unit[j / 2] = (unit[j / 2] & keep) | (uint32_t)((127 - to) << 7) << half;
-          }
-        }
-      }
       const bool edge = j0 + KS - 1 > old || j0 + KS > k1;  // new tokens' causal order, the segment's end
       bool raise = false;
       float f[NR][2];
@@ -783,55 +738,52 @@ __global__ void __launch_bounds__(kThreads, I4 ? kPerSm4 : kPerSm16) attn_paged_
         }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        if constexpr (I4) {
-          uint32_t sc[2][NG / 2];
+        uint32_t pf[NR][2], pl[NR][2];  // P and what its rounding to bf16 leaves
+#pragma unroll
+        for (int x = 0; x < NR; ++x)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const uint32_t at = st + St::vs + (16 * n + 8 * y + g) * St::step;
-            if constexpr (NG == 4) {
-              const uint2 v = lds64(at);
-              sc[y][0] = v.x, sc[y][1] = v.y;
-            } else {
-              sc[y][0] = lds32(at);
-            }
+            const float p0 = s[n][x][2 * y], p1 = s[n][x][2 * y + 1];
+            const uint32_t p = pack_bf16(p0, p1);
+            pf[x][y] = transposed(p), pl[x][y] = transposed(pack_bf16(p0 - lo16(p), p1 - hi16(p)));
+          }
+        if constexpr (I4) {
+          // steps of keys 2 t and 2 t + 1, 2 t + 8 and 2 t + 9
+          uint32_t sa[2][NG / 2], sb[2][NG / 2];
 #pragma unroll
-            for (int j = 0; j < NG / 2; ++j) {
-              const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&sc[y][j]), *reinterpret_cast<const __nv_bfloat162*>(&unit[j]));
-              sc[y][j] = *reinterpret_cast<const uint32_t*>(&v);
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t at = st + St::vs + (16 * n + 8 * y + 2 * t) * St::step;
+            if constexpr (NG == 4) {
+              const uint4 v = lds128(at);
+              sa[y][0] = v.x, sa[y][1] = v.y, sb[y][0] = v.z, sb[y][1] = v.w;
+            } else {
+              const uint2 v = lds64(at);
+              sa[y][0] = v.x, sb[y][0] = v.y;
             }
           }
           const uint32_t half = g & 1 ? 0x7632 : 0x5410;
 #pragma unroll
           for (int j = 0; j < NG; ++j) {
-            uint32_t pf[NR][2];
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const float e = j & 1 ? hi16(sc[y][j / 2]) : lo16(sc[y][j / 2]);
-#pragma unroll
-              for (int x = 0; x < NR; ++x) pf[x][y] = transposed(pack_f16(s[n][x][2 * y] * e, s[n][x][2 * y + 1] * e));
-            }
-            // values 32 j + 4 g .. + 3 of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+            // values 32 j + 4 g .. + 3 of those keys
             const uint32_t at = st + St::v + 16 * n * St::row + v_at + ((j << 4) ^ v_f);
             const uint32_t v0 = __byte_perm(lds32(at), lds32(at + St::row), half);
             const uint32_t v1 = __byte_perm(lds32(at + 8 * St::row), lds32(at + 9 * St::row), half);
+            const uint32_t e0 = __byte_perm(sa[0][j / 2], sb[0][j / 2], j & 1 ? 0x7632 : 0x5410);
+            const uint32_t e1 = __byte_perm(sa[1][j / 2], sb[1][j / 2], j & 1 ? 0x7632 : 0x5410);
+            uint32_t f[2][4];
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              const uint32_t c0 = v0 >> (8 * y), c1 = v1 >> (8 * y);
-              const uint32_t a0 = magic.first(c0), a1 = magic.second(c0), a2 = magic.first(c1), a3 = magic.second(c1);
+              f[y][0] = magic.values(v0 >> (8 * y), e0), f[y][1] = magic.values(v0 >> (8 * y + 4), e0);
+              f[y][2] = magic.values(v1 >> (8 * y), e1), f[y][3] = magic.values(v1 >> (8 * y + 4), e1);
 #pragma unroll
-              for (int x = 0; x < NR; ++x) mma_f16(acc[2 * j + y][x], a0, a1, a2, a3, pf[x][0], pf[x][1]);
+              for (int x = 0; x < NR; ++x) mma(acc[2 * j + y][x], f[y], pl[x][0], pl[x][1]);
             }
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+              for (int x = 0; x < NR; ++x) mma(acc[2 * j + y][x], f[y], pf[x][0], pf[x][1]);
           }
         } else {
-          uint32_t pf[NR][2], pl[NR][2];  // P and what its rounding to bf16 leaves
-#pragma unroll
-          for (int x = 0; x < NR; ++x)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const float p0 = s[n][x][2 * y], p1 = s[n][x][2 * y + 1];
-              const uint32_t p = pack_bf16(p0, p1);
-              pf[x][y] = transposed(p), pl[x][y] = transposed(pack_bf16(p0 - lo16(p), p1 - hi16(p)));
-            }
 #pragma unroll
           for (int k = 0; k < DP / 16; ++k) {
             uint32_t v[4];
@@ -877,8 +829,7 @@ __global__ void __launch_bounds__(kThreads, I4 ? kPerSm4 : kPerSm16) attn_paged_
         for (int n = 0; n < DP / 16; ++n) {
           float* p = part + (w * kQ + r) * DP;
           if constexpr (I4) {  // rows g and g + 8 of a product are neighbours
-            const float i = f * pow2(exponent(n / 2));
-            *reinterpret_cast<float2*>(p + 32 * (n / 2) + 4 * g + 2 * (n % 2)) = make_float2(acc[n][x][e] * i, acc[n][x][2 + e] * i);
+            *reinterpret_cast<float2*>(p + 32 * (n / 2) + 4 * g + 2 * (n % 2)) = make_float2(acc[n][x][e] * f, acc[n][x][2 + e] * f);
           } else {
             p[16 * n + g] = acc[n][x][e] * f, p[16 * n + g + 8] = acc[n][x][2 + e] * f;
           }

@@ -605,6 +605,11 @@ GDN_API int gdn_kv_gather(const gdn_paged_cache* cache, const int* table, int ro
  * 0, and so does one that would not fit max_pages pages, for which
  * gdn_device_status() returns GDN_ERR_SEQLENS.
  *
+ * With bf16 queries a value from GDN_CACHE_I4 is code * step rounded to bf16, as
+ * gdn_kv_gather gives it (steps of 5 bits: exact).  Weights of up to 2^8 times the
+ * values are added up in fp32 before the sum is divided, which bounds the values:
+ * 2^8 tokens |v| within fp32's range.
+ *
  * q may be bf16 with GDN_CACHE_BF16 or GDN_CACHE_I4, fp32 with GDN_CACHE_F32 or
  * GDN_CACHE_I4.  Limits: max_pages page <= 2^30, B Hkv <= 65535, H / Hkv T <=
  * 65535 * 8, no key heads without query heads.  Errors as above (GDN_ERR_ALIGN:
