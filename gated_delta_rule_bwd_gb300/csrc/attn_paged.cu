@@ -343,6 +343,16 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
+__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"((uint16_t)v) : "memory");
+}
+// Whether the bf16 in the low half is infinite or NaN.
+__device__ __forceinline__ bool no_number(uint32_t v) { return (v & 0x7f80) == 0x7f80; }
 __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
@@ -434,7 +444,10 @@ struct Stage {
   __device__ __forceinline__ static uint32_t at(int r, int c) { return r * row + ((c << 4) ^ f(r)); }
 };
 
-template <int DP, int NR, bool I4>
+// LATER: several new tokens per row, of which the first do not see the last.  As a kernel
+// of its own, because the code alone, never run, costs single tokens 1.5 % (64 rows in
+// 4 bits 60.4 for 59.5 us).
+template <int DP, int NR, bool I4, bool LATER>
 __global__ void __launch_bounds__(kThreads, I4 ? kPerSm4 : kPerSm16) attn_paged_mma_kernel(Args a) {
   using St = Stage<DP, I4>;
   constexpr int KS = St::KS, NG = DP / 32, NT = KS / 16, kQ = 8 * NR;  // kQ: query rows per CTA
@@ -736,6 +749,53 @@ __global__ void __launch_bounds__(kThreads, I4 ? kPerSm4 : kPerSm16) attn_paged_
             l[x][e] += s[n][x][e] + s[n][x][2 + e];
           }
         }
+      // A later new token's values that are no numbers: rows that see the token take them
+      // here, and the products find zeros (the others' weight of 0 times them is none).
+      if (LATER && j0 + KS - 1 > old) {
+        bool bad = false;
+        if constexpr (I4) {
+          for (int i = lane; i < KS * NG / 2; i += 32) {
+            const uint32_t u = lds32(st + St::vs + 4 * i);
+            bad |= no_number(u) || no_number(u >> 16);
+          }
+        } else {
+          for (int i = lane; i < KS * St::NC; i += 32) {
+            const uint4 v = lds128(st + St::v + 16 * i);
+            for (uint32_t u : {v.x, v.y, v.z, v.w}) bad |= no_number(u) || no_number(u >> 16);
+          }
+        }
+        if (__any_sync(0xffffffffu, bad)) {
+#pragma unroll 1
+          for (int r = max(0, old + 1 - j0); r < KS; ++r) {
+            auto take = [&](int n, int y, uint32_t u) {  // acc[n][.][2 y + e] of the rows that see key r
+              if (!no_number(u)) return;
+#pragma unroll
+              for (int x = 0; x < NR; ++x)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (j0 + r <= last[x][e]) acc[n][x][2 * y + e] += I4 ? NAN : lo16(u);
+            };
+#pragma unroll
+            for (int n = 0; n < DP / 16; ++n)
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                if constexpr (I4) take(n, y, lds16(st + St::vs + r * St::step + 2 * (n / 2)));
+                else take(n, y, lds16(st + St::v + St::at(r, 2 * n + y) + 2 * g));
+              }
+            __syncwarp();
+            if constexpr (I4) {
+              const uint32_t at = st + St::vs + r * St::step + 2 * (lane % NG);
+              if (lane < NG && no_number(lds16(at))) sts16(at, 0);
+            } else {
+              for (int c = lane; c < DP; c += 32) {
+                const uint32_t at = st + St::v + r * St::row + 2 * c;
+                if (no_number(lds16(at))) sts16(at, 0);
+              }
+            }
+          }
+          __syncwarp();
+        }
+      }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         uint32_t pf[NR][2], pl[NR][2];  // P and what its rounding to bf16 leaves
@@ -907,12 +967,14 @@ cudaError_t launch_mma(const Args& a, const Plan& pl, cudaStream_t s) {
   auto smem = [&](int stage, int DP) {
     return std::max(4 * kStages * stage, 4 * pl.rows * (DP + 2) * (int)sizeof(float));
   };
-  if (a.D <= 64) {
-    const int n = smem(Stage<64, I4>::bytes, 64);
-    return pl.rows == 8 ? go(attn_paged_mma_kernel<64, 1, I4>, n) : go(attn_paged_mma_kernel<64, 2, I4>, n);
-  }
-  const int n = smem(Stage<128, I4>::bytes, 128);
-  return pl.rows == 8 ? go(attn_paged_mma_kernel<128, 1, I4>, n) : go(attn_paged_mma_kernel<128, 2, I4>, n);
+  auto by_size = [&](auto size) {
+    constexpr int DP = decltype(size)::value;
+    const int n = smem(Stage<DP, I4>::bytes, DP);
+    if (a.T > 1)
+      return pl.rows == 8 ? go(attn_paged_mma_kernel<DP, 1, I4, true>, n) : go(attn_paged_mma_kernel<DP, 2, I4, true>, n);
+    return pl.rows == 8 ? go(attn_paged_mma_kernel<DP, 1, I4, false>, n) : go(attn_paged_mma_kernel<DP, 2, I4, false>, n);
+  };
+  return a.D <= 64 ? by_size(std::integral_constant<int, 64>{}) : by_size(std::integral_constant<int, 128>{});
 }
 
 template <typename T>

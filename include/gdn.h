@@ -603,7 +603,10 @@ GDN_API int gdn_kv_gather(const gdn_paged_cache* cache, const int* table, int ro
  * o [B, T, H, D]; both contiguous.  Rows as in the single-token form on a
  * contiguous cache; a row whose lens[b] is negative is not in use and gets o =
  * 0, and so does one that would not fit max_pages pages, for which
- * gdn_device_status() returns GDN_ERR_SEQLENS.
+ * gdn_device_status() returns GDN_ERR_SEQLENS.  A NaN in a row of q, or in the k of a
+ * slot that it sees, makes that row NaN; a NaN or infinity in the v of a slot makes
+ * those values of the rows that see it NaN or infinite.  It reaches no others: not the
+ * new tokens before its own either.
  *
  * With bf16 queries a value from GDN_CACHE_I4 is code * step rounded to bf16, as
  * gdn_kv_gather gives it (steps of 5 bits: exact).  Weights of up to 2^8 times the
