@@ -916,6 +916,13 @@ _APPEND = struct.Struct("@9i10q")      # gdn_kv_append_shape
 _PAGED = struct.Struct("@5iq")         # gdn_attn_paged_shape
 
 
+def _pack(form, *values):
+    try:
+        return form.pack(*values)
+    except struct.error:
+        raise GdnError(f"a size of the call does not fit the library's integers: {values}") from None
+
+
 def _f32(name, x, device, shape):
     if not _same(x, torch.float32, device, shape):
         _nb_check(name, x, torch.float32, device, shape)
@@ -981,7 +988,7 @@ def _qk_args(q, k, q_weight, k_weight, cos, sin, positions, interleaved):
                          and q_weight.is_contiguous() and k_weight.is_contiguous()))):
             return _QK_ROPE.pack(B, T, H, Hkv, D, 2 * half, cos.shape[0], bool(interleaved),
                                  _DTYPES[dtype], qs[0], qs[1], qs[2], ks[0], ks[1], ks[2])
-    except (AttributeError, KeyError, TypeError, ValueError, IndexError):
+    except (AttributeError, KeyError, TypeError, ValueError, IndexError, struct.error):
         pass
     return _qk_args_slow(q, k, q_weight, k_weight, cos, sin, positions, interleaved)
 
@@ -1007,8 +1014,8 @@ def _qk_args_slow(q, k, q_weight, k_weight, cos, sin, positions, interleaved):
         if R == 0:
             raise GdnError("positions need cos and sin")
         _i32("positions", positions, device, (B, T))
-    return _QK_ROPE.pack(B, T, H, Hkv, D, R, P, bool(interleaved), _DTYPES[dtype], qs[0], qs[1], qs[2],
-                         ks[0], ks[1], ks[2])
+    return _pack(_QK_ROPE, B, T, H, Hkv, D, R, P, bool(interleaved), _DTYPES[dtype], qs[0], qs[1], qs[2],
+                 ks[0], ks[1], ks[2])
 
 
 def qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None,
@@ -1105,7 +1112,7 @@ def _cache_args(cache, device):
                 form = _DTYPES[dtype]
                 return _CACHE.pack(pages, page, Hkv, D, form, k.data_ptr(), v.data_ptr(), 0, 0, a[0],
                                    a[1], a[2], b[0], b[1], b[2], 0, 0, 0, 0, 0, 0), Hkv, D, form
-    except (AttributeError, KeyError, TypeError, ValueError, IndexError):
+    except (AttributeError, KeyError, TypeError, ValueError, IndexError, struct.error):
         pass
     return _cache_args_slow(cache, device)
 
@@ -1131,8 +1138,8 @@ def _cache_args_slow(cache, device):
         if dtype not in _DTYPES:
             raise GdnError(f"a cache of {dtype}: fp32, bf16, or uint8 codes with scales")
         form = _DTYPES[dtype]
-        return _CACHE.pack(pages, page, Hkv, D, form, k.data_ptr(), v.data_ptr(), 0, 0, *kst[:3],
-                           *vst[:3], 0, 0, 0, 0, 0, 0), Hkv, D, form
+        return _pack(_CACHE, pages, page, Hkv, D, form, k.data_ptr(), v.data_ptr(), 0, 0, *kst[:3],
+                     *vst[:3], 0, 0, 0, 0, 0, 0), Hkv, D, form
     ks, vs = cache[2], cache[3]
     steps = (pages, page, Hkv, D // 16)
     if (dtype is not torch.uint8 or D % 16 or ks.dtype is not torch.bfloat16
@@ -1142,8 +1149,8 @@ def _cache_args_slow(cache, device):
     kss, vss = ks.stride(), vs.stride()
     if (kss[3] != 1 or vss[3] != 1) and steps[3] > 1:
         raise GdnError("the scales of a head must be contiguous in the cache")
-    return _CACHE.pack(pages, page, Hkv, 2 * D, 2, k.data_ptr(), v.data_ptr(), ks.data_ptr(),
-                       vs.data_ptr(), *kst[:3], *vst[:3], *kss[:3], *vss[:3]), Hkv, 2 * D, 2
+    return _pack(_CACHE, pages, page, Hkv, 2 * D, 2, k.data_ptr(), v.data_ptr(), ks.data_ptr(),
+                 vs.data_ptr(), *kst[:3], *vst[:3], *kss[:3], *vss[:3]), Hkv, 2 * D, 2
 
 
 def _block_table(table, rows, device):
@@ -1230,8 +1237,8 @@ def kv_append(k, v, cache, block_table, lens, q=None, cos=None, sin=None, interl
         c, B, T, H, R, P, code, rows, most, stride, qst, kst, vst = _append_args(
             k, v, cache, block_table, lens, q, cos, sin, cu_seqlens)
         dtype, device = k.dtype, k.device
-    s = _APPEND.pack(B, T, H, R, P, bool(interleaved), code, rows, most, stride, qst[0], qst[1], qst[2],
-                     kst[0], kst[1], kst[2], vst[0], vst[1], vst[2])
+    s = _pack(_APPEND, B, T, H, R, P, bool(interleaved), code, rows, most, stride, qst[0], qst[1], qst[2],
+              kst[0], kst[1], kst[2], vst[0], vst[1], vst[2])
     qo = None if q is None else _empty(q, dtype, device)
     _call((_lib or lib()).gdn_kv_append(
         s, c, k.data_ptr(), v.data_ptr(), _addr(q), _addr(cos), _addr(sin), block_table.data_ptr(),
@@ -1285,7 +1292,7 @@ def attn_paged(q, cache, block_table, lens, scale=None, workspace=None):
         raise GdnError(f"{Hkv} key heads do not divide the {H} query heads")
     _i32("lens", lens, device, (B,))
     most, stride = _block_table(block_table, B, device)
-    s = _PAGED.pack(B, T, H, _DTYPES[dtype], most, stride)
+    s = _pack(_PAGED, B, T, H, _DTYPES[dtype], most, stride)
     L = _lib or lib()
     o = torch.empty_like(q)
     need = L.gdn_attn_paged_workspace(s, c)
