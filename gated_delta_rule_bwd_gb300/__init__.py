@@ -914,6 +914,7 @@ _QK_ROPE = struct.Struct("@9i6q")      # gdn_qk_rope_shape
 _CACHE = struct.Struct("@5i4P12q")     # gdn_paged_cache
 _APPEND = struct.Struct("@9i10q")      # gdn_kv_append_shape
 _PAGED = struct.Struct("@5iq")         # gdn_attn_paged_shape
+_MOST = 1 << 30                        # tokens, rows and pages of a row that the library takes
 
 
 def _pack(form, *values):
@@ -1260,10 +1261,10 @@ def kv_gather(cache, block_table, cu_seqlens, total, dtype=None):
     if dtype not in _DTYPES or form not in (2, _DTYPES[dtype]):
         raise GdnError(f"a cache of {cache[0].dtype} does not give {dtype}")
     _attn_cu("cu_seqlens", cu_seqlens, device)
-    if total < 0:
-        raise GdnError(f"{total} tokens")
     rows = cu_seqlens.numel() - 1
     most, stride = _block_table(block_table, rows, device)
+    if total < 0 or max(total, rows, most) > _MOST:
+        raise GdnError(f"{total} tokens of {rows} rows of {most} pages: at most {_MOST}")
     k = torch.empty((1, total, Hkv, D), dtype=dtype, device=device)
     v = torch.empty_like(k)
     _call((_lib or lib()).gdn_kv_gather(

@@ -39,3 +39,18 @@ def test_too_many_tokens():
         with pytest.raises(gdn.GdnError):
             call()
     assert gdn.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_gathers_of_too_many_tokens():
+    """Nothing is made for them."""
+    table, off = torch.zeros(1, 4, dtype=I32, device="cuda"), torch.tensor([0, 2], dtype=I32, device="cuda")
+    small = gdn.new_paged_cache(4, 16, 1, 1)
+    for total in (-1, (1 << 30) + 1, BIG, 1 << 32, (1 << 32) + 2):
+        held = torch.cuda.memory_allocated()
+        torch.cuda.reset_peak_memory_stats()
+        with pytest.raises(gdn.GdnError):
+            gdn.kv_gather(small, table, off, total)
+        assert torch.cuda.max_memory_allocated() == held  # nothing is made for it
+    k, v = gdn.kv_gather(small, table, off, 2)
+    assert k.shape == (1, 2, 1, 1) and gdn.device_status() == 0
