@@ -38,9 +38,9 @@ def scored(scores, H, D, page, bits, seed):
         return cache, table, q, at_
     code, step = torch.zeros_like(k0), torch.ones_like(k0)
     for c in (7, 6, 5):  # k0 = sign c 2^x
-        x = torch.log2(k0.abs() / c)
-        hit = (k0 != 0) & (x == x.round())
-        code[hit], step[hit] = (torch.sign(k0) * c)[hit], torch.exp2(x)[hit]
+        x = k0.abs() / c
+        hit = torch.frexp(x).mantissa == 0.5
+        code[hit], step[hit] = (torch.sign(k0) * c)[hit], x[hit]
     assert torch.equal(code * step, k0)
     codes, steps = cache[0][at_], cache[2][at_]
     codes[:, 0, 0] = (codes[:, 0, 0] & 0xf0) | (code + 8).to(torch.uint8)
