@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kThreads) attn_paged_simt_kernel(Args a) {
 //     q0 c0 + q1 c1 = (q1 / 16) X + (q0 - q1 / 16) L - 1024 (both weights):
 //   half an operation a code.  The weights are fp16 (q scaled by a power of two per row,
 //   so that its largest value is in [1, 2)): the first is exact, the second off by up to
-//   2^-11 of itself, which reaches the score as that part of step c0 (q, as bf16, has 2^-8).
+//   2^-11 of itself, which moves scores of normal queries and keys by 1.5e-4 of their spread.
 //   The constants, with the 8 in c, go back once per key, with the steps, which are
 //   applied to the scores:
 //     s = sum_j step_j (sum_d of the group's products) + sum_j step_j base_j,
@@ -322,8 +322,8 @@ __global__ void __launch_bounds__(kThreads) attn_paged_simt_kernel(Args a) {
 // kStages stages (cp.async) and keeps its own m, l and accumulators, so the warps
 // meet only at a segment's end.
 constexpr int kStages = 3;
-// CTAs per SM.  4 bits: at three, 165 registers; four (128) keep the same share of the
-// issue slots busy, and there are more of them to set up (57 us for 55).
+// CTAs per SM.  4 bits: at three, 165 registers; four (128) kept the same share of the
+// issue slots busy, with more of them to set up (57 us for 55, with fp16 weights).
 constexpr int kPerSm16 = 2, kPerSm4 = 3;
 
 template <int n>

@@ -3,7 +3,8 @@
 // 4-bit storage of a row of D values (one head of one token; D a multiple of
 // 32): D / 2 bytes of codes, byte i the values 2 i (low four bits) and 2 i + 1,
 // and a step per 32 values.
-//   step = amax / 7 rounded to 5 significant bits (half up), held as bf16,
+//   step = amax / 7 (the fp32 product with 1 / 7) rounded to 5 significant bits (half
+//   up), held as bf16,
 //   code = rint(x / step) in [-7, 7], held as code + 8;
 // steps of 0 have codes of 0, and a NaN or infinity among the 32 makes the step
 // NaN.  A code has 3 significant bits and a step 5, so that what a code stands

@@ -532,7 +532,7 @@ GDN_API int gdn_qk_norm_rope_bwd(const gdn_qk_rope_shape* shape, const void* q, 
  *
  * Formats: GDN_CACHE_F32, GDN_CACHE_BF16, and GDN_CACHE_I4 (D a multiple of 32),
  * where every 32 values of a head have a step (bf16) and a code of 4 bits each:
- *   step = max|x| / 7, rounded to 5 significant bits (half up),
+ *   step = max|x| / 7 (fp32, the product with 1 / 7) rounded to 5 significant bits (half up),
  *   code = x / step rounded to the nearest integer (half to even), in [-7, 7].
  * k and v are then bytes [pages, page, Hkv, D / 2], byte i holding code + 8 of
  * values 2 i (low four bits) and 2 i + 1; k_scale and v_scale are bf16 [pages,
